@@ -126,6 +126,74 @@ typedef struct {
 } q4moe_layer;
 
 /*
+ * A matrix of symmetric 8-bit codes, or `count` stacked matrices of the same shape:
+ * codes int8 [count][n][k] and one fp32 scale per row (output channel), scales
+ * [count][n], for w[r][j] = scales[r] * codes[r][j].  i8_quantize writes this form.
+ * k a multiple of 64; codes 16-byte aligned, scales 4-byte aligned.
+ */
+typedef struct {
+  const int8_t* codes;
+  const float* scales;
+  int64_t count;  /* >= 1 */
+  int64_t n;      /* rows per matrix */
+  int64_t k;      /* columns, a multiple of 64 */
+} q4moe_i8_matrix;
+
+/*
+ * The experts of a layer in 8-bit integers: gate and up (count n_experts, inter x
+ * hidden), down (count n_experts, hidden x inter); the shared expert, when
+ * sh_gate.codes is non-null, has the same shapes with count 1 and is added with
+ * weight 1.
+ */
+typedef struct {
+  int32_t hidden;
+  int32_t inter;
+  int32_t n_experts;
+  int32_t reserved;  /* 0 */
+  q4moe_i8_matrix gate, up, down;
+  q4moe_i8_matrix sh_gate, sh_up, sh_down;
+} q4moe_i8_experts;
+
+/* Scores of q4moe_routing. */
+enum { Q4MOE_SCORE_SOFTMAX = 0, Q4MOE_SCORE_SIGMOID = 1 };
+
+/*
+ * A routing rule.  With logits l (fp32), scores s = softmax(l) over all experts or
+ * s = sigmoid(l) each, and choices c = s + bias:
+ *  - an expert is closed for a token when its logit or its bias is NaN or
+ *    -infinity; a closed expert is never chosen;
+ *  - with n_groups > 1 the experts form n_groups groups of n_experts / n_groups
+ *    consecutive ones.  A group's value is the sum of the open ones among its
+ *    group_terms largest choices (1 or 2); the top_groups groups of largest value
+ *    stay and the experts of the others are not chosen;
+ *  - the top_k largest choices among what stays are chosen, in descending order.
+ *    Equal values, of experts or of groups, go to the lower index;
+ *  - the weight of a chosen expert is its score s, without the bias; with
+ *    renormalise divided by the sum of the chosen scores (all 0 where that sum is
+ *    0); then times scale;
+ *  - where fewer than top_k experts are open the last slots get id -1 and weight 0.
+ * Scores, choices and sums are computed in 64 bits from the fp32 logits (without a
+ * bias, and with groups valued by one term, choices are compared by their logits)
+ * and each weight is rounded once to fp32.  In a softmax a closed logit counts as 0,
+ * and +infinity takes the whole row (several share it).
+ */
+typedef struct {
+  int32_t n_experts;    /* 1..1024 */
+  int32_t hidden;       /* a multiple of 64; moe_route only */
+  int32_t top_k;        /* 1..32, at most top_groups * (n_experts / n_groups) */
+  int32_t score;        /* Q4MOE_SCORE_* */
+  int32_t n_groups;     /* 1..64, divides n_experts */
+  int32_t top_groups;   /* 1..n_groups */
+  int32_t group_terms;  /* 1 or 2 */
+  int32_t renormalise;  /* 0 or 1 */
+  float scale;          /* finite */
+  int32_t reserved;     /* 0 */
+  const float* bias;    /* null, or fp32 [n_experts] */
+  const q4moe_bf16* router;  /* moe_route: bf16 [n_experts][hidden], may be null with router_q8 */
+  q4moe_matrix router_q8;    /* moe_route: codes null, or the 8-bit router used in its place */
+} q4moe_routing;
+
+/*
  * y = W x, one bf16 vector x[k] against every row of W (count*n rows), fp32
  * accumulation, y written as fp32 or bf16 [count*n].  The decode form of the
  * 4-bit weight stream (lily-qwen3.8-flash-next README, "How the speed was
@@ -174,6 +242,23 @@ int moe_route_topk(const q4moe_bf16* router, int32_t n_experts, int32_t hidden,
 int moe_route_topk_q8(const q4moe_matrix* router_q8, const q4moe_bf16* X, int64_t T, int32_t top_k,
                       int32_t* ids, float* weights, void* workspace, size_t workspace_bytes,
                       q4moe_stream stream);
+
+/*
+ * moe_route_topk with a routing rule (see q4moe_routing): logits of the rows
+ * X bf16 [T][hidden] through rule->router or rule->router_q8 in fp32, as
+ * moe_route_topk and moe_route_topk_q8 compute them, then the rule.  Writes ids
+ * int32 [T][top_k] and weights fp32 [T][top_k].  Needs Q4MOE_OP_ROUTE workspace
+ * (n_experts; T).
+ */
+int moe_route(const q4moe_routing* rule, const q4moe_bf16* X, int64_t T, int32_t* ids, float* weights,
+              void* workspace, size_t workspace_bytes, q4moe_stream stream);
+
+/*
+ * The rule alone, on logits fp32 [T][n_experts] that the caller has; rule->hidden,
+ * router and router_q8 are not read.  No workspace.
+ */
+int moe_route_logits(const q4moe_routing* rule, const float* logits, int64_t T, int32_t* ids, float* weights,
+                     q4moe_stream stream);
 
 /*
  * Stable counting sort of the T*top_k rows r = t*top_k + slot by expert id
@@ -271,6 +356,57 @@ int moe_ffn_decode_batch(const q4moe_layer* layer, const q4moe_bf16* X, int64_t 
  */
 int moe_ffn_prefill(const q4moe_layer* layer, const q4moe_bf16* X, int64_t T, void* Y,
                     int out_dtype, void* workspace, size_t workspace_bytes, q4moe_stream stream);
+
+/*
+ * Symmetric 8-bit form of bf16 rows X[rows][k]: scales[r] is the fp32 nearest to
+ * max|X[r]| / 127 and codes[r][j] the integer nearest to X[r][j] / scales[r] (ties to
+ * even; -127..127).  A row of zeros gets scale 0 and codes 0; a row that holds an
+ * infinity or a NaN gets scale NaN and codes 0, so products with it are NaN.  The
+ * load-time step for weights (a row is an output channel), and what i8_gemm does to
+ * its activations (a row is a token).  k a multiple of 64 up to 65536; X and codes
+ * 16-byte aligned, codes and scales not overlapping X.
+ */
+int i8_quantize(const q4moe_bf16* X, int64_t rows, int64_t k, int8_t* codes, float* scales,
+                q4moe_stream stream);
+
+/*
+ * Y[m][r] = (sum_j q[m][j] codes[r][j] * sx[m]) * scales[r] for bf16 rows X[m][k],
+ * with q, sx the 8-bit form of X's rows (i8_quantize), taken inside the call.  The
+ * product in 8-bit integers next to q4_gemm's fp16 one: the integer sum is exact
+ * (int32) and is rounded where it becomes fp32, at each scale, and to Y's type.
+ * Y fp32 or bf16 [m][count*n], not overlapping X; k up to 65536.  Needs a workspace
+ * of i8_gemm_workspace_bytes.
+ */
+int i8_gemm(const q4moe_i8_matrix* W, const q4moe_bf16* X, int64_t m, void* Y, int out_dtype,
+            void* workspace, size_t workspace_bytes, q4moe_stream stream);
+
+/* Workspace bytes of i8_gemm on m rows; 0 for invalid arguments. */
+size_t i8_gemm_workspace_bytes(const q4moe_i8_matrix* W, int64_t m);
+
+/*
+ * T tokens through the 8-bit experts that a router chose for them: with ids int32
+ * [T][top_k] and weights fp32 [T][top_k] (moe_route's, moe_route_topk's or the
+ * caller's),
+ *   y[t] = sum_i weights[t][i] * down_e(act_e(x[t])), e = ids[t][i], + shared(x[t])
+ *   act_e(x) = silu(gate_e x) * up_e x
+ * Both products are i8_gemm's: x in 8-bit form per token, the fp32 activations in
+ * 8-bit form per token and expert.  A slot whose id lies outside [0, n_experts) adds
+ * nothing (a token all of whose slots do gets the shared expert alone, or zeros); an
+ * id may stand in several slots of a token.  The slots' products are summed in fp32
+ * in slot order, the shared expert last.  With a bf16 Y the integer sums of the down
+ * product may be rounded to 11 significant bits before that (fp16, scaled by a power
+ * of two): by 2^-11 of each summand at most, next to the output's own 2^-8.
+ * Results do not depend on which tokens share a call, except for those roundings.
+ * X bf16 [T][hidden], Y fp32 or bf16 [T][hidden], not overlapping X, ids or weights;
+ * hidden and inter multiples of 64 up to 16384, n_experts up to 1024, top_k up to 32
+ * (not bounded by n_experts).  Needs a workspace of moe_experts_i8_workspace_bytes.
+ */
+int moe_experts_i8(const q4moe_i8_experts* experts, const q4moe_bf16* X, int64_t T, const int32_t* ids,
+                   const float* weights, int32_t top_k, void* Y, int out_dtype, void* workspace,
+                   size_t workspace_bytes, q4moe_stream stream);
+
+/* Workspace bytes of moe_experts_i8 on T tokens of top_k slots; 0 for invalid arguments. */
+size_t moe_experts_i8_workspace_bytes(const q4moe_i8_experts* experts, int64_t T, int32_t top_k);
 
 /*
  * Greedy LM head: logits[b][r] = W[r] . X[b] in fp32 for b < B (1 <= B <= 8),

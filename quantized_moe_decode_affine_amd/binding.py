@@ -22,6 +22,8 @@ OP_GEMV, OP_GEMM, OP_ROUTE, OP_PERMUTE, OP_FFN_DECODE, OP_FFN_PREFILL, OP_LMHEAD
 
 EXPORTS = ("q4_gemv", "q4_gemm", "moe_route_topk", "moe_route_topk_q8", "moe_permute", "moe_ffn_decode", "moe_ffn_decode_noalloc",
            "moe_ffn_decode_batch",
+           "moe_route", "moe_route_logits", "i8_quantize", "i8_gemm", "i8_gemm_workspace_bytes",
+           "moe_experts_i8", "moe_experts_i8_workspace_bytes",
            "moe_ffn_prefill", "lmhead_argmax", "q4moe_pack_group_major", "q4moe_workspace_bytes", "q4moe_strerror")
 
 
@@ -43,6 +45,26 @@ class q4moe_layer(ctypes.Structure):
                 ("gate", q4moe_matrix), ("up", q4moe_matrix), ("down", q4moe_matrix),
                 ("sh_gate", q4moe_matrix), ("sh_up", q4moe_matrix), ("sh_down", q4moe_matrix),
                 ("router_q8", q4moe_matrix), ("sh_gate_w", ctypes.c_void_p)]
+
+
+class q4moe_i8_matrix(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("count", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64)]
+
+
+class q4moe_i8_experts(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_int32), ("inter", ctypes.c_int32), ("n_experts", ctypes.c_int32),
+                ("reserved", ctypes.c_int32),
+                ("gate", q4moe_i8_matrix), ("up", q4moe_i8_matrix), ("down", q4moe_i8_matrix),
+                ("sh_gate", q4moe_i8_matrix), ("sh_up", q4moe_i8_matrix), ("sh_down", q4moe_i8_matrix)]
+
+
+class q4moe_routing(ctypes.Structure):
+    _fields_ = [("n_experts", ctypes.c_int32), ("hidden", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("score", ctypes.c_int32), ("n_groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("group_terms", ctypes.c_int32), ("renormalise", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("bias", ctypes.c_void_p), ("router", ctypes.c_void_p),
+                ("router_q8", q4moe_matrix)]
 
 
 _lib = None
@@ -71,6 +93,11 @@ def load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
         "moe_ffn_prefill": [pl, vp, i64, vp, ctypes.c_int, vp, sz, vp],
         "lmhead_argmax": [pm, vp, i64, vp, vp, vp, sz, vp],
         "q4moe_pack_group_major": [pm, vp, vp],
+        "moe_route": [ctypes.POINTER(q4moe_routing), vp, i64, vp, vp, vp, sz, vp],
+        "moe_route_logits": [ctypes.POINTER(q4moe_routing), vp, i64, vp, vp, vp],
+        "i8_quantize": [vp, i64, i64, vp, vp, vp],
+        "i8_gemm": [ctypes.POINTER(q4moe_i8_matrix), vp, i64, vp, ctypes.c_int, vp, sz, vp],
+        "moe_experts_i8": [ctypes.POINTER(q4moe_i8_experts), vp, i64, vp, vp, i32, vp, ctypes.c_int, vp, sz, vp],
     }
     for name, args in sigs.items():
         f = getattr(lib, name)
@@ -78,6 +105,10 @@ def load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
         f.restype = ctypes.c_int
     lib.q4moe_workspace_bytes.argtypes = [ctypes.c_int, pl, pm, i64]
     lib.q4moe_workspace_bytes.restype = sz
+    lib.i8_gemm_workspace_bytes.argtypes = [ctypes.POINTER(q4moe_i8_matrix), i64]
+    lib.i8_gemm_workspace_bytes.restype = sz
+    lib.moe_experts_i8_workspace_bytes.argtypes = [ctypes.POINTER(q4moe_i8_experts), i64, i32]
+    lib.moe_experts_i8_workspace_bytes.restype = sz
     lib.q4moe_strerror.argtypes = [ctypes.c_int]
     lib.q4moe_strerror.restype = ctypes.c_char_p
     _lib = lib
@@ -114,6 +145,16 @@ def bf16_tensor(bits: np.ndarray, device="cuda") -> torch.Tensor:
     return _dev(bits, device).view(torch.bfloat16)
 
 
+def _need(name: str, t: torch.Tensor, dtype: torch.dtype, shape, device: Optional[torch.device] = None) -> None:
+    """Raise ValueError unless `t` is a contiguous GPU tensor of this type and shape (on `device`)."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: {dtype} of shape {tuple(shape)} wanted, got {t.dtype} of {tuple(t.shape)}")
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{name} is on {t.device}, wanted on {device if device is not None else 'a GPU'}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
 class DeviceQ4:
     """An affine matrix (or a stack of them) resident on the device: 4-bit codes, or 8-bit
     codes when the code words per row hold 4 columns each (k is taken from the groups)."""
@@ -135,6 +176,26 @@ class DeviceQ4:
         self.codes_gm = None
         self.struct = q4moe_matrix(self.codes.data_ptr(), self.scales.data_ptr(), self.biases.data_ptr(),
                                    self.count, self.n, self.k, self.bits, 0)
+
+    @classmethod
+    def from_device(cls, codes: torch.Tensor, scales: torch.Tensor, biases: torch.Tensor) -> "DeviceQ4":
+        """The same from tensors that are on the device already: codes int32 words [n][words] or
+        [count][n][words], scales and biases bfloat16 [..][k/64], all contiguous."""
+        if codes.dim() == 2:
+            codes, scales, biases = codes[None], scales[None], biases[None]
+        count, n, words = codes.shape
+        _need("codes", codes, torch.int32, (count, n, words), codes.device)
+        _need("scales", scales, torch.bfloat16, (count, n, scales.shape[-1]), codes.device)
+        _need("biases", biases, torch.bfloat16, tuple(scales.shape), codes.device)
+        self = cls.__new__(cls)
+        self.count, self.n, self.k = count, n, scales.shape[-1] * 64
+        self.bits = 4 if words * 8 == self.k else 8
+        if words * 32 != self.k * self.bits:
+            raise ValueError(f"{words} code words per row do not hold {self.k} columns at 4 or 8 bits")
+        self.codes, self.scales, self.biases, self.codes_gm = codes, scales, biases, None
+        self.struct = q4moe_matrix(codes.data_ptr(), scales.data_ptr(), biases.data_ptr(), count, n, self.k,
+                                   self.bits, 0)
+        return self
 
     def pack_group_major(self) -> None:
         """Add the group-major copy of the codes that the prefill GEMMs read (4-bit only)."""
@@ -193,6 +254,79 @@ class DeviceLayer:
     def nbytes(self) -> int:
         total = self.gate.nbytes + self.up.nbytes + self.down.nbytes + sum(m.nbytes for m in self.sh)
         return total + (self.router_q8.nbytes if self.router_q8 is not None else self.router.numel() * 2)
+
+
+class DeviceI8:
+    """A matrix of symmetric 8-bit codes (or a stack of them) on the device: codes int8 [n][k] or
+    [count][n][k] and one fp32 scale per row, [n] or [count][n]."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
+        if codes.dim() == 2:
+            codes, scales = codes[None], scales[None]
+        self.count, self.n, self.k = codes.shape
+        _need("codes", codes, torch.int8, (self.count, self.n, self.k))
+        _need("scales", scales, torch.float32, (self.count, self.n), codes.device)
+        self.codes, self.scales = codes, scales
+        self.struct = q4moe_i8_matrix(codes.data_ptr(), scales.data_ptr(), self.count, self.n, self.k)
+
+    @classmethod
+    def quantize(cls, weight: torch.Tensor) -> "DeviceI8":
+        """The 8-bit form of bfloat16 weights [n][k] or [count][n][k], a scale per row."""
+        codes, scales = i8_quantize(weight.reshape(-1, weight.shape[-1]))
+        return cls(codes.view(weight.shape), scales.view(weight.shape[:-1]))
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.scales.numel() * 4
+
+
+class DeviceI8Experts:
+    """The 8-bit experts of a layer: gate and up [n_experts][inter][hidden], down
+    [n_experts][hidden][inter], and optionally the shared expert's (gate, up, down)."""
+
+    def __init__(self, gate: DeviceI8, up: DeviceI8, down: DeviceI8, shared=None):
+        self.n_experts, self.inter, self.hidden = gate.count, gate.n, gate.k
+        self.matrices = (gate, up, down, *(shared or ()))
+        self.has_shared = shared is not None
+        if len(self.matrices) not in (3, 6) or any(m.codes.device != gate.codes.device for m in self.matrices):
+            raise ValueError("experts: gate, up and down, and as many of the shared expert, on one device")
+        for m, count, n, k in zip(self.matrices, (self.n_experts,) * 3 + (1,) * 3, (self.inter, self.inter, self.hidden) * 2,
+                                  (self.hidden, self.hidden, self.inter) * 2):
+            if (m.count, m.n, m.k) != (count, n, k):
+                raise ValueError(f"experts: a matrix of shape {(m.count, m.n, m.k)} where {(count, n, k)} is wanted")
+        self.struct = q4moe_i8_experts(self.hidden, self.inter, self.n_experts, 0, *(m.struct for m in self.matrices))
+
+    @property
+    def nbytes(self) -> int:
+        return sum(m.nbytes for m in self.matrices)
+
+
+class Routing:
+    """A routing rule and its router: bfloat16 [n_experts][hidden], an 8-bit DeviceQ4, or for
+    moe_route_logits the number of experts.  See q4moe_routing in include/q4moe.h."""
+
+    SCORES = {"softmax": 0, "sigmoid": 1}
+
+    def __init__(self, router, top_k: int, score: str = "softmax", bias: Optional[torch.Tensor] = None,
+                 n_groups: int = 1, top_groups: int = 1, group_terms: int = 2, renormalise: bool = True,
+                 scale: float = 1.0):
+        if score not in self.SCORES:
+            raise ValueError(f"score {score!r}: one of {sorted(self.SCORES)} is wanted")
+        self.router, self.bias, self.top_k = router, bias, top_k
+        q8, bf16, self.hidden, self.device = q4moe_matrix(), None, 0, None
+        if isinstance(router, DeviceQ4):
+            q8, self.n_experts, self.hidden, self.device = router.struct, router.n, router.k, router.codes.device
+        elif isinstance(router, torch.Tensor):
+            self.n_experts, self.hidden = router.shape
+            _need("router", router, torch.bfloat16, (self.n_experts, self.hidden))
+            bf16, self.device = router.data_ptr(), router.device
+        else:
+            self.n_experts = int(router)
+        if bias is not None:
+            _need("bias", bias, torch.float32, (self.n_experts,), self.device)
+            self.device = bias.device
+        self.struct = q4moe_routing(self.n_experts, self.hidden, top_k, self.SCORES[score], n_groups, top_groups,
+                                    group_terms, int(renormalise), scale, 0, _ptr(bias), bf16, q8)
 
 
 # ---------------------------------------------------------------- workspaces --
@@ -270,6 +404,73 @@ def gpu_routing(layer: DeviceLayer, X: torch.Tensor):
     if layer.router_q8 is not None:
         return moe_route_topk_q8(layer.router_q8, X, layer.top_k)
     return moe_route_topk(layer.router, X, layer.top_k)
+
+
+def _call(fn: str, device: torch.device, *args) -> None:
+    """Call an entry point on `device` and its current stream."""
+    f = getattr(load_library(), fn)
+    if device.index == torch.cuda.current_device():
+        status = f(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = f(*args, torch.cuda.current_stream(device).cuda_stream)
+    _check(fn, status)
+
+
+def _result(name: str, out: Optional[torch.Tensor], shape, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(name, out, dtype, shape, device)
+    return out
+
+
+def _scratch(ws: Optional[torch.Tensor], nbytes, device: torch.device) -> torch.Tensor:
+    """The caller's workspace, or one of nbytes() for this call."""
+    if ws is None:
+        return torch.empty(max(nbytes(), 256), dtype=torch.uint8, device=device)
+    if ws.dtype != torch.uint8 or ws.device != device or not ws.is_contiguous():
+        raise ValueError("ws: a contiguous uint8 buffer on the inputs' device is wanted")
+    return ws
+
+
+def _out_type(out_dtype: int) -> torch.dtype:
+    if out_dtype not in (OUT_F32, OUT_BF16):
+        raise ValueError(f"out_dtype {out_dtype}: OUT_F32 or OUT_BF16 is wanted")
+    return torch.float32 if out_dtype == OUT_F32 else torch.bfloat16
+
+
+def moe_route_workspace(routing: Routing, T: int) -> torch.Tensor:
+    """A workspace for moe_route on up to T rows."""
+    return torch.empty(max(256, load_library().q4moe_workspace_bytes(
+        OP_ROUTE, ctypes.byref(q4moe_layer(routing.hidden, 0, routing.n_experts, routing.top_k)), None, T)),
+        dtype=torch.uint8, device=routing.device)
+
+
+def moe_route(routing: Routing, X: torch.Tensor, ids: Optional[torch.Tensor] = None,
+              weights: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
+    """Expert ids int32 and weights fp32 [T][top_k] of the rows X by a routing rule."""
+    T, dev = X.shape[0], X.device
+    _need("X", X, torch.bfloat16, (T, routing.hidden), routing.device)
+    ids = _result("ids", ids, (T, routing.top_k), torch.int32, dev)
+    weights = _result("weights", weights, (T, routing.top_k), torch.float32, dev)
+    if T:
+        ws = moe_route_workspace(routing, T) if ws is None else _scratch(ws, None, dev)
+        _call("moe_route", dev, ctypes.byref(routing.struct), X.data_ptr(), T, ids.data_ptr(), weights.data_ptr(),
+              ws.data_ptr(), ws.numel())
+    return ids, weights
+
+
+def moe_route_logits(routing: Routing, logits: torch.Tensor, ids: Optional[torch.Tensor] = None,
+                     weights: Optional[torch.Tensor] = None):
+    """moe_route on logits fp32 [T][n_experts] that the caller has."""
+    T, dev = logits.shape[0], logits.device
+    _need("logits", logits, torch.float32, (T, routing.n_experts), routing.device)
+    ids = _result("ids", ids, (T, routing.top_k), torch.int32, dev)
+    weights = _result("weights", weights, (T, routing.top_k), torch.float32, dev)
+    if T:
+        _call("moe_route_logits", dev, ctypes.byref(routing.struct), logits.data_ptr(), T, ids.data_ptr(),
+              weights.data_ptr())
+    return ids, weights
 
 
 def moe_permute(ids: torch.Tensor, n_experts: int, ws: Optional[torch.Tensor] = None):
@@ -367,3 +568,57 @@ def lmhead_argmax(W: DeviceQ4, X: torch.Tensor, ws: Optional[torch.Tensor] = Non
     _check("lmhead_argmax", load_library().lmhead_argmax(ctypes.byref(W.struct), _ptr(X), B, _ptr(ids), _ptr(mx),
                                                          _ptr(ws), ws.numel(), _stream()))
     return ids, mx
+
+
+def i8_quantize(X: torch.Tensor):
+    """Symmetric 8-bit codes int8 [rows][k] and scales fp32 [rows] of bfloat16 rows."""
+    rows, k = X.shape
+    _need("X", X, torch.bfloat16, (rows, k))
+    codes = torch.empty((rows, k), dtype=torch.int8, device=X.device)
+    scales = torch.empty(rows, dtype=torch.float32, device=X.device)
+    if rows:
+        _call("i8_quantize", X.device, X.data_ptr(), rows, k, codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def i8_gemm_workspace(W: DeviceI8, m: int) -> torch.Tensor:
+    """A workspace for i8_gemm on up to m rows."""
+    return torch.empty(max(256, load_library().i8_gemm_workspace_bytes(ctypes.byref(W.struct), m)),
+                       dtype=torch.uint8, device=W.codes.device)
+
+
+def i8_gemm(W: DeviceI8, X: torch.Tensor, out_dtype: int = OUT_F32, out: Optional[torch.Tensor] = None,
+            ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y = X W^T in 8-bit integers: the rows of X (bfloat16) are quantized per token inside the call."""
+    m, dev = X.shape[0], W.codes.device
+    _need("X", X, torch.bfloat16, (m, W.k), dev)
+    Y = _result("out", out, (m, W.count * W.n), _out_type(out_dtype), dev)
+    if m:
+        ws = _scratch(ws, lambda: load_library().i8_gemm_workspace_bytes(ctypes.byref(W.struct), m), dev)
+        _call("i8_gemm", dev, ctypes.byref(W.struct), X.data_ptr(), m, Y.data_ptr(), out_dtype, ws.data_ptr(),
+              ws.numel())
+    return Y
+
+
+def moe_experts_i8_workspace(experts: DeviceI8Experts, T: int, top_k: int) -> torch.Tensor:
+    """A workspace for moe_experts_i8 on up to T tokens of top_k slots."""
+    return torch.empty(max(256, load_library().moe_experts_i8_workspace_bytes(ctypes.byref(experts.struct), T, top_k)),
+                       dtype=torch.uint8, device=experts.matrices[0].codes.device)
+
+
+def moe_experts_i8(experts: DeviceI8Experts, X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
+                   out_dtype: int = OUT_F32, out: Optional[torch.Tensor] = None,
+                   ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The rows of X through the 8-bit experts of ids [T][top_k] (others than 0..n_experts-1 add
+    nothing), weighted by weights [T][top_k], plus the shared expert."""
+    T, dev = X.shape[0], experts.matrices[0].codes.device
+    _need("X", X, torch.bfloat16, (T, experts.hidden), dev)
+    k = ids.shape[1] if ids.dim() == 2 else 0
+    _need("ids", ids, torch.int32, (T, k), dev)
+    _need("weights", weights, torch.float32, (T, k), dev)
+    Y = _result("out", out, (T, experts.hidden), _out_type(out_dtype), dev)
+    if T:
+        ws = _scratch(ws, lambda: load_library().moe_experts_i8_workspace_bytes(ctypes.byref(experts.struct), T, k), dev)
+        _call("moe_experts_i8", dev, ctypes.byref(experts.struct), X.data_ptr(), T, ids.data_ptr(),
+              weights.data_ptr(), k, Y.data_ptr(), out_dtype, ws.data_ptr(), ws.numel())
+    return Y

@@ -5,6 +5,7 @@
 #include "kernels.h"
 
 #include <algorithm>
+#include <cmath>
 #include <new>
 
 namespace q4moe {
@@ -104,6 +105,70 @@ size_t lmhead_ws(int64_t rows, int64_t k, int64_t B) {
   (void)rows;
   (void)k;
   return 256 + (size_t)B * 8;  // arrival counter, then one 64-bit running maximum per batch row
+}
+
+// [a, a + an) and [b, b + bn) share a byte.
+bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + bn && y < x + an;
+}
+
+// The rule of a routing descriptor (everything but its router).
+int rule_check(const q4moe_routing* R, q4moe::RouteRule* r) {
+  if (!R || R->n_experts < 1 || R->top_k < 1 || R->top_k > R->n_experts) return Q4MOE_EINVAL;
+  if (R->score != Q4MOE_SCORE_SOFTMAX && R->score != Q4MOE_SCORE_SIGMOID) return Q4MOE_EINVAL;
+  if (R->n_groups < 1 || R->n_experts % R->n_groups || R->top_groups < 1 || R->top_groups > R->n_groups)
+    return Q4MOE_EINVAL;
+  if ((int64_t)R->top_k > (int64_t)R->top_groups * (R->n_experts / R->n_groups)) return Q4MOE_EINVAL;
+  if (R->group_terms != 1 && R->group_terms != 2) return Q4MOE_EINVAL;
+  if ((R->renormalise != 0 && R->renormalise != 1) || !std::isfinite(R->scale)) return Q4MOE_EINVAL;
+  if (R->bias && !aligned(R->bias, 4)) return Q4MOE_EINVAL;
+  if (R->n_experts > 1024 || R->top_k > 32 || R->n_groups > q4moe::kMaxGroups) return Q4MOE_EUNSUPPORTED;
+  *r = q4moe::RouteRule{R->n_experts,  R->top_k,       R->score, R->n_groups, R->top_groups,
+                        R->group_terms, R->renormalise, R->scale, R->bias};
+  return Q4MOE_OK;
+}
+
+constexpr int64_t kMaxI8K = 65536;      // 127 * 128 * k stays below 2^31
+constexpr int64_t kMaxExpertK = 16384;  // hidden and intermediate sizes of the 8-bit experts
+
+bool i8_matrix_ok(const q4moe_i8_matrix* W) {
+  return W && W->codes && W->scales && W->count >= 1 && W->n >= 1 && W->k >= 64 && W->k % 64 == 0 &&
+         aligned(W->codes, 16) && aligned(W->scales, 4);
+}
+
+bool i8_shape(const q4moe_i8_matrix& W, int64_t count, int64_t n, int64_t k) {
+  return i8_matrix_ok(&W) && W.count == count && W.n == n && W.k == k;
+}
+
+int i8_gemm_check(const q4moe_i8_matrix* W, int64_t m) {
+  if (!i8_matrix_ok(W) || m < 0) return Q4MOE_EINVAL;
+  // rows and channels are 32-bit in the kernels, and so is the grid of 64 x 64 tiles
+  if (W->k > kMaxI8K || W->count > kMaxRows32 || W->n > kMaxRows32 || W->count * W->n > kMaxRows32 ||
+      m > kMaxRows32 || (m / 64 + 9) * (W->count * W->n / 64 + 1) > kMaxRows32)
+    return Q4MOE_EUNSUPPORTED;
+  return Q4MOE_OK;
+}
+
+int i8_experts_check(const q4moe_i8_experts* L, int64_t T, int64_t top_k, q4moe::I8Experts* d) {
+  if (!L || T < 0 || top_k < 1) return Q4MOE_EINVAL;
+  if (L->hidden < 64 || L->hidden % 64 || L->inter < 64 || L->inter % 64 || L->n_experts < 1) return Q4MOE_EINVAL;
+  if (L->hidden > kMaxExpertK || L->inter > kMaxExpertK || L->n_experts > 1024 || top_k > 32) return Q4MOE_EUNSUPPORTED;
+  const int64_t E = L->n_experts, H = L->hidden, I = L->inter;
+  if (!i8_shape(L->gate, E, I, H) || !i8_shape(L->up, E, I, H) || !i8_shape(L->down, E, H, I)) return Q4MOE_EINVAL;
+  const bool shared = L->sh_gate.codes != nullptr;
+  if (shared && (!i8_shape(L->sh_gate, 1, I, H) || !i8_shape(L->sh_up, 1, I, H) || !i8_shape(L->sh_down, 1, H, I)))
+    return Q4MOE_EINVAL;
+  // sorted positions and the tiles' grid are 32-bit
+  const int64_t rows = T > kMaxRows32 ? kMaxRows32 : T * (top_k + 1);
+  if (T > kMaxRows32 || rows > kMaxRows32 || (rows / 64 + 2 * E + 8) * (std::max(H, I) / 64 + 1) > kMaxRows32)
+    return Q4MOE_EUNSUPPORTED;
+  auto mat = [](const q4moe_i8_matrix& W) { return q4moe::I8Mat{W.codes, W.scales}; };
+  const q4moe::I8Mat none{nullptr, nullptr};
+  *d = q4moe::I8Experts{L->hidden,     L->inter,     L->n_experts,
+                        mat(L->gate),  mat(L->up),   mat(L->down),
+                        shared ? mat(L->sh_gate) : none, shared ? mat(L->sh_up) : none, shared ? mat(L->sh_down) : none};
+  return Q4MOE_OK;
 }
 
 }  // namespace
@@ -363,6 +428,111 @@ int lmhead_argmax(const q4moe_matrix* W, const q4moe_bf16* X, int64_t B, int32_t
                                                     ids, max_logit, keys, done, (hipStream_t)stream));
     return hip_status(q4moe::run_lmhead_argmax(W->codes, W->scales, W->biases, rows, (int)W->k, X, (int)B, ids,
                                                max_logit, keys, done, (hipStream_t)stream));
+  } catch (...) {
+    return Q4MOE_EHIP;
+  }
+}
+
+int moe_route(const q4moe_routing* rule, const q4moe_bf16* X, int64_t T, int32_t* ids, float* weights, void* workspace,
+              size_t workspace_bytes, q4moe_stream stream) {
+  try {
+    q4moe::RouteRule r;
+    const int st = rule_check(rule, &r);
+    if (st != Q4MOE_OK) return st;
+    const bool q8 = rule->router_q8.codes != nullptr;
+    if (rule->hidden < 64 || rule->hidden % 64) return Q4MOE_EINVAL;
+    if (q8 ? !matrix_shape(rule->router_q8, 1, r.n_experts, rule->hidden) || !is_q8(rule->router_q8)
+           : !rule->router || !aligned(rule->router, 16))
+      return Q4MOE_EINVAL;
+    if (!X || !aligned(X, 16) || !ids || !aligned(ids, 4) || !weights || !aligned(weights, 4) || T < 0)
+      return Q4MOE_EINVAL;
+    if (rule->hidden > kMaxGemvK || T > kMaxRows32 || T * r.top_k > kMaxRows32) return Q4MOE_EUNSUPPORTED;
+    if (T == 0) return Q4MOE_OK;
+    if (!workspace || workspace_bytes < q4moe::route_workspace_bytes(T, r.n_experts) || !aligned(workspace, 256))
+      return Q4MOE_EWORKSPACE;
+    const Q4Mat m = q8 ? to_mat(rule->router_q8) : Q4Mat{nullptr, nullptr, nullptr};
+    return hip_status(q4moe::run_route(r, rule->router, &m, rule->hidden, X, T, ids, weights, workspace,
+                                       (hipStream_t)stream));
+  } catch (...) {
+    return Q4MOE_EHIP;
+  }
+}
+
+int moe_route_logits(const q4moe_routing* rule, const float* logits, int64_t T, int32_t* ids, float* weights,
+                     q4moe_stream stream) {
+  try {
+    q4moe::RouteRule r;
+    const int st = rule_check(rule, &r);
+    if (st != Q4MOE_OK) return st;
+    if (!logits || !aligned(logits, 4) || !ids || !aligned(ids, 4) || !weights || !aligned(weights, 4) || T < 0)
+      return Q4MOE_EINVAL;
+    if (T > kMaxRows32 || T * r.top_k > kMaxRows32) return Q4MOE_EUNSUPPORTED;
+    if (T == 0) return Q4MOE_OK;
+    return hip_status(q4moe::run_select(r, logits, T, ids, weights, (hipStream_t)stream));
+  } catch (...) {
+    return Q4MOE_EHIP;
+  }
+}
+
+int i8_quantize(const q4moe_bf16* X, int64_t rows, int64_t k, int8_t* codes, float* scales, q4moe_stream stream) {
+  try {
+    if (!X || !aligned(X, 16) || !codes || !aligned(codes, 16) || !scales || !aligned(scales, 4) || rows < 0)
+      return Q4MOE_EINVAL;
+    if (k < 64 || k % 64) return Q4MOE_EINVAL;
+    if (k > kMaxI8K || rows > kMaxRows32) return Q4MOE_EUNSUPPORTED;
+    if (rows == 0) return Q4MOE_OK;
+    const size_t n = (size_t)rows * k, s = (size_t)rows * 4;
+    if (overlap(codes, n, X, 2 * n) || overlap(scales, s, X, 2 * n) || overlap(scales, s, codes, n)) return Q4MOE_EINVAL;
+    return hip_status(q4moe::run_i8_quantize(X, rows, (int)k, codes, scales, (hipStream_t)stream));
+  } catch (...) {
+    return Q4MOE_EHIP;
+  }
+}
+
+size_t i8_gemm_workspace_bytes(const q4moe_i8_matrix* W, int64_t m) {
+  return i8_gemm_check(W, m) == Q4MOE_OK ? q4moe::i8_gemm_workspace_bytes(m, (int)W->k) : 0;
+}
+
+int i8_gemm(const q4moe_i8_matrix* W, const q4moe_bf16* X, int64_t m, void* Y, int out_dtype, void* workspace,
+            size_t workspace_bytes, q4moe_stream stream) {
+  try {
+    const int st = i8_gemm_check(W, m);
+    if (st != Q4MOE_OK) return st;
+    if (!X || !aligned(X, 16) || !out_ok(Y, out_dtype)) return Q4MOE_EINVAL;
+    if (m == 0) return Q4MOE_OK;
+    const int64_t n = W->count * W->n;
+    if (overlap(Y, (size_t)m * n * (out_dtype == Q4MOE_OUT_F32 ? 4 : 2), X, (size_t)m * W->k * 2)) return Q4MOE_EINVAL;
+    if (!workspace || workspace_bytes < q4moe::i8_gemm_workspace_bytes(m, (int)W->k) || !aligned(workspace, 256))
+      return Q4MOE_EWORKSPACE;
+    return hip_status(q4moe::run_i8_gemm(q4moe::I8Mat{W->codes, W->scales}, n, (int)W->k, X, m, Y,
+                                         out_dtype == Q4MOE_OUT_BF16, workspace, (hipStream_t)stream));
+  } catch (...) {
+    return Q4MOE_EHIP;
+  }
+}
+
+size_t moe_experts_i8_workspace_bytes(const q4moe_i8_experts* experts, int64_t T, int32_t top_k) {
+  q4moe::I8Experts d;
+  return i8_experts_check(experts, T, top_k, &d) == Q4MOE_OK ? q4moe::experts_i8_workspace_bytes(d, T, top_k) : 0;
+}
+
+int moe_experts_i8(const q4moe_i8_experts* experts, const q4moe_bf16* X, int64_t T, const int32_t* ids,
+                   const float* weights, int32_t top_k, void* Y, int out_dtype, void* workspace,
+                   size_t workspace_bytes, q4moe_stream stream) {
+  try {
+    q4moe::I8Experts d;
+    const int st = i8_experts_check(experts, T, top_k, &d);
+    if (st != Q4MOE_OK) return st;
+    if (!X || !aligned(X, 16) || !ids || !aligned(ids, 4) || !weights || !aligned(weights, 4) || !out_ok(Y, out_dtype))
+      return Q4MOE_EINVAL;
+    if (T == 0) return Q4MOE_OK;
+    const size_t yb = (size_t)T * d.hidden * (out_dtype == Q4MOE_OUT_F32 ? 4 : 2), sb = (size_t)T * top_k * 4;
+    if (overlap(Y, yb, X, (size_t)T * d.hidden * 2) || overlap(Y, yb, ids, sb) || overlap(Y, yb, weights, sb))
+      return Q4MOE_EINVAL;
+    if (!workspace || workspace_bytes < q4moe::experts_i8_workspace_bytes(d, T, top_k) || !aligned(workspace, 256))
+      return Q4MOE_EWORKSPACE;
+    return hip_status(q4moe::run_moe_experts_i8(d, X, T, ids, weights, top_k, Y, out_dtype == Q4MOE_OUT_BF16,
+                                                workspace, (hipStream_t)stream));
   } catch (...) {
     return Q4MOE_EHIP;
   }

@@ -1,0 +1,496 @@
+// Products in 8-bit integers: quantization of rows, the dense product Y = X W^T with a
+// scale per token and per output channel (i8_gemm), and the experts' feed-forward on such
+// products from given expert ids and weights (moe_experts_i8).
+//
+//   Y[m][n] = (float(sum_k q[m][k] c[n][k]) * sx[m]) * sw[n]
+//
+// with q, sx the symmetric 8-bit rows of X (int8.h) and c, sw the weight's codes and
+// channel scales.  The integer sum is exact in 32 bits (k is bounded on the host), so every
+// tiling and order gives the same sums, and an output is rounded when the sum becomes a
+// float, at each of the two scales and to its own type.
+#include <algorithm>
+#include <type_traits>
+
+#include "int8.h"
+#include "kernels.h"
+
+namespace q4moe {
+
+namespace {
+
+size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+
+// fp32 -> bf16 bits, nearest even; a NaN stays a NaN (the bare carry could turn it into 0 or infinity).
+__device__ __forceinline__ uint16_t i8_bf16(float f) {
+  return (uint16_t)(f == f ? f32_to_bf16_bits(f) : 0x7FC0u);
+}
+
+typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+
+// One wave per row, two passes over it: the largest magnitude, then the codes (the second
+// pass reads what the first left in the caches).  Bound by the row's bytes.
+template <typename In>
+__global__ __launch_bounds__(256) void i8_quantize_kernel(const In* __restrict__ X, int64_t rows, int K,
+                                                          int8_t* __restrict__ codes, float* __restrict__ scales) {
+  const int lane = lane_id();
+  const int64_t stride = (int64_t)gridDim.x * 4;
+  for (int64_t r = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave; r < rows; r += stride) {
+    const In* x = X + r * K;
+    uint32_t most = 0;
+    for (int j = lane * 8; j < K; j += kWave * 8) {
+      float v[8];
+      i8_load8(x + j, v);
+      most = i8_most(v, most);
+    }
+    const float scale = i8_scale(wave_max_u32(most));
+    const I8Rounder rd(scale);
+    for (int j = lane * 8; j < K; j += kWave * 8) {
+      float v[8];
+      i8_load8(x + j, v);
+      *reinterpret_cast<uint2*>(codes + r * K + j) =
+          make_uint2(rd.pack4(v[0], v[1], v[2], v[3]), rd.pack4(v[4], v[5], v[6], v[7]));
+    }
+    if (lane == 0) scales[r] = scale;
+  }
+}
+
+template <typename In>
+hipError_t launch_quantize(const In* X, int64_t rows, int K, int8_t* codes, float* scales, hipStream_t stream) {
+  if (rows <= 0) return hipSuccess;
+  const int64_t blocks = std::min<int64_t>((rows + 3) / 4, 16384);
+  hipLaunchKernelGGL(i8_quantize_kernel<In>, dim3((unsigned)blocks), dim3(256), 0, stream, X, rows, K, codes, scales);
+  return hipGetLastError();
+}
+
+// ---- tiled product on the i8 matrix cores
+enum { kEpiF32 = 0, kEpiBf16 = 1, kEpiSwiglu = 2, kEpiPartF16 = 3, kEpiPartF32 = 4 };
+
+struct I8GemmArgs {
+  const int8_t* A;         // codes of the rows [.][K]
+  const float* sa;         // their scales
+  const int32_t* row_src;  // grouped: row of A of each sorted position (null: the position itself)
+  const int4* tiles;       // grouped: {expert (-1 shared, -2 none), first position, rows, 0}; null: dense
+  int64_t rows;            // dense: rows of A
+  int64_t P;               // grouped: routed positions; position P + t is token t's for the shared expert
+  int K, N;                // N output columns (SwiGLU: gate columns, as many up columns)
+  I8Mat W, W2;             // weights (stacked by expert), SwiGLU: gate and up
+  I8Mat S, S2;             // the shared expert's
+  int n_slices;            // column slices of a tile
+  int64_t tiles_n;         // row tiles
+  float mul;               // kEpiPartF16: power of two that keeps a sum within fp16's range
+  void* out;               // [position][N]
+};
+
+constexpr int kStepBytes = 128;  // columns of a K step, one cache line of every operand row
+constexpr int kXcds = 8;
+
+__device__ __forceinline__ int row_swz(int r) { return (r >> 1) & 7; }
+
+// Workgroup = WM x WN waves, each FM x FN blocks of 32 x 32 (v_mfma_i32_32x32x32_i8).  Each
+// 128-column K step of both operands goes through LDS by 16-byte DMA loads (8 lanes read a
+// row's whole line) in kStages stages; inside a row the eight 16-byte pieces are
+// XOR-rotated by row bits 1-3 so that the operand reads (a row per lane) spread over all
+// banks.  K is a multiple of 64: where it is not one of 128 the last step's upper pieces
+// repeat the row's last one and are not multiplied.
+template <int WM, int WN, int FM, int FN, int kStages, int EPI>
+__device__ __forceinline__ void i8_tile_body(const I8GemmArgs& p) {
+  constexpr int TM = WM * FM * 32, TN = WN * FN * 32, kWaves = WM * WN;
+  constexpr int kOps = (TM + TN) / 8 / kWaves;  // DMA loads per wave and step, 8 rows each
+  static_assert((TM + TN) / 8 % kWaves == 0 && (kStages == 2 || kStages == 3), "whole blocks of 8 rows per wave");
+  constexpr int kStageBytes = (TM + TN) * kStepBytes;
+  // one array per stage, so that the compiler can tell a stage's reads from the loads
+  // still filling another
+  __shared__ __align__(16) uint8_t s_st0[kStageBytes], s_st1[kStageBytes], s_st2[kStages > 2 ? kStageBytes : 16];
+  constexpr bool kSwiglu = EPI == kEpiSwiglu;
+  constexpr int kCols = kSwiglu ? TN / 2 : TN;  // output columns of a tile
+  const int lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int wm = wave / WN, wn = wave % WN;
+
+  // Workgroups go to the XCDs in turn: all slices of a tile stay on one (its rows of A are
+  // read by every slice).
+  const int xcd = blockIdx.x % kXcds;
+  const int64_t q = blockIdx.x / kXcds;
+  const int64_t tile = q / p.n_slices * kXcds + xcd;
+  const int n0 = (int)(q % p.n_slices) * kCols;
+  if (tile >= p.tiles_n) return;
+  int expert = 0;
+  int64_t first = tile * TM;
+  int rows;
+  if (p.tiles) {
+    const int4 tl = p.tiles[tile];
+    expert = __builtin_amdgcn_readfirstlane(tl.x);
+    if (expert == -2) return;
+    first = __builtin_amdgcn_readfirstlane(tl.y);
+    rows = __builtin_amdgcn_readfirstlane(tl.z);
+  } else {
+    rows = (int)min<int64_t>(TM, p.rows - first);
+  }
+  const I8Mat w = expert < 0 ? p.S : p.W, w2 = expert < 0 ? p.S2 : p.W2;
+  const int64_t e_row = (int64_t)max(expert, 0) * p.N;  // first row of this expert's matrix
+
+  // Column c of the tile, 0..TN: output column and matrix.  SwiGLU: a wave's first FN/2
+  // blocks are gate rows and the rest the up rows of the same columns, so that a lane holds both.
+  auto w_row = [&](int c, bool* up) -> int {
+    if constexpr (kSwiglu) {
+      const int b = c / 32, f = b % FN;
+      *up = f >= FN / 2;
+      return n0 + ((b / FN) * (FN / 2) + f % (FN / 2)) * 32 + c % 32;
+    } else {
+      *up = false;
+      return n0 + c;
+    }
+  };
+
+  const int8_t* src[kOps];
+  int dst[kOps], piece[kOps];
+#pragma unroll
+  for (int j = 0; j < kOps; ++j) {
+    const int blk = wave * kOps + j;
+    const int r = blk * 8 + (lane >> 3);
+    piece[j] = ((lane & 7) ^ row_swz(r)) * 16;
+    dst[j] = blk * 8 * kStepBytes;
+    if (blk < TM / 8) {
+      const int64_t pos = first + min(r, rows - 1);
+      const int64_t a = p.row_src ? (pos < p.P ? (int64_t)p.row_src[pos] : pos - p.P) : pos;
+      src[j] = p.A + a * p.K;
+    } else {
+      bool up;
+      const int row = min(w_row(r - TM, &up), p.N - 1);
+      src[j] = (up ? w2.codes : w.codes) + (e_row + row) * p.K;
+    }
+  }
+  auto stage = [&](int st) -> uint8_t* { return st == 0 ? s_st0 : st == 1 ? s_st1 : s_st2; };
+  const int steps = (p.K + kStepBytes - 1) / kStepBytes;
+  // steps past the last load it again and are not computed
+  auto issue = [&](int i, int st) {
+    const int k0 = min(i, steps - 1) * kStepBytes;
+#pragma unroll
+    for (int j = 0; j < kOps; ++j)
+      __builtin_amdgcn_global_load_lds(src[j] + min(k0 + piece[j], p.K - 16), stage(st) + dst[j], 16, 0, 0);
+  };
+
+  const int m = lane & 31, h = lane >> 5;
+  i32x16_t acc[FM][FN] = {};
+  auto step = [&](int i, auto st_c, auto nf_c) __attribute__((always_inline)) {
+    constexpr int st = decltype(st_c)::value;
+    constexpr int NF = decltype(nf_c)::value;
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(kOps * (kStages - 2)));
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    issue(i + kStages - 1, (st + kStages - 1) % kStages);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (NF > 0) {
+      const uint8_t* base = stage(st);
+      const int half = p.K - i * kStepBytes >= kStepBytes ? 4 : 2;  // MFMA steps of 32 columns
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        if (kk >= half) break;
+        i32x4_t a[NF], b[FN];
+        const int c = 2 * kk + h;
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+          const int r = (wm * FM + f) * 32 + m;
+          a[f] = *reinterpret_cast<const i32x4_t*>(base + r * kStepBytes + ((c ^ row_swz(r)) << 4));
+        }
+#pragma unroll
+        for (int f = 0; f < FN; ++f) {
+          const int r = TM + (wn * FN + f) * 32 + m;
+          b[f] = *reinterpret_cast<const i32x4_t*>(base + r * kStepBytes + ((c ^ row_swz(r)) << 4));
+        }
+#pragma unroll
+        for (int fm = 0; fm < NF; ++fm)
+#pragma unroll
+          for (int fn = 0; fn < FN; ++fn)
+            acc[fm][fn] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[fm], b[fn], acc[fm][fn], 0, 0, 0);
+      }
+    }
+  };
+  auto run = [&](auto nf_c) __attribute__((always_inline)) {
+    using S0 = std::integral_constant<int, 0>;
+    using S1 = std::integral_constant<int, 1>;
+    using S2 = std::integral_constant<int, kStages - 1>;
+    int i = 0;
+    if constexpr (kStages == 2) {
+      for (; i + 2 <= steps; i += 2) {
+        step(i, S0{}, nf_c);
+        step(i + 1, S1{}, nf_c);
+      }
+      if (i < steps) step(i, S0{}, nf_c);
+    } else {
+      for (; i + 3 <= steps; i += 3) {
+        step(i, S0{}, nf_c);
+        step(i + 1, S1{}, nf_c);
+        step(i + 2, S2{}, nf_c);
+      }
+      if (i < steps) step(i, S0{}, nf_c);
+      if (i + 1 < steps) step(i + 1, S1{}, nf_c);
+    }
+  };
+  issue(0, 0);
+  if constexpr (kStages > 2) issue(1, 1);
+  // only the 32-row blocks that hold rows are multiplied
+  const int nf = max(0, min(FM, (rows - wm * FM * 32 + 31) / 32));
+  if (nf == FM) run(std::integral_constant<int, FM>{});
+  else if (FM > 3 && nf == 3) run(std::integral_constant<int, (FM > 3 ? 3 : 0)>{});
+  else if (FM > 2 && nf == 2) run(std::integral_constant<int, (FM > 2 ? 2 : 0)>{});
+  else if (FM > 1 && nf == 1) run(std::integral_constant<int, (FM > 1 ? 1 : 0)>{});
+  else run(std::integral_constant<int, 0>{});
+  __builtin_amdgcn_s_waitcnt(0);  // the repeated loads of the last steps are still landing
+
+  // D layout: column = lane % 32, row = 8*(i/4) + 4*(lane/32) + i%4
+#pragma unroll
+  for (int fm = 0; fm < FM; ++fm) {
+    const int r0 = (wm * FM + fm) * 32;
+    if (r0 >= rows) break;
+    float sa[16];
+    if constexpr (EPI != kEpiPartF16 && EPI != kEpiPartF32) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int64_t pos = first + min(r0 + 8 * (i >> 2) + 4 * h + (i & 3), rows - 1);
+        const int64_t a = p.row_src ? (pos < p.P ? (int64_t)p.row_src[pos] : pos - p.P) : pos;
+        sa[i] = p.sa[a];
+      }
+    }
+    constexpr int kOutF = kSwiglu ? FN / 2 : FN;
+#pragma unroll
+    for (int fn = 0; fn < kOutF; ++fn) {
+      const int n = n0 + (wn * kOutF + fn) * 32 + m;
+      if (n >= p.N) continue;
+      float sw = 0.f, su = 0.f;
+      if constexpr (EPI != kEpiPartF16 && EPI != kEpiPartF32) sw = w.scales[e_row + n];
+      if constexpr (kSwiglu) su = w2.scales[e_row + n];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int r = r0 + 8 * (i >> 2) + 4 * h + (i & 3);
+        if (r >= rows) continue;
+        const int64_t at = (first + r) * p.N + n;
+        const float d = (float)acc[fm][fn][i];
+        if constexpr (EPI == kEpiF32) {
+          static_cast<float*>(p.out)[at] = d * sa[i] * sw;
+        } else if constexpr (EPI == kEpiBf16) {
+          static_cast<uint16_t*>(p.out)[at] = i8_bf16(d * sa[i] * sw);
+        } else if constexpr (kSwiglu) {
+          const float g = d * sa[i] * sw, u = (float)acc[fm][fn + FN / 2][i] * sa[i] * su;
+          static_cast<float*>(p.out)[at] = g / (1.0f + expf(-g)) * u;
+        } else if constexpr (EPI == kEpiPartF16) {
+          static_cast<_Float16*>(p.out)[at] = (_Float16)(d * p.mul);
+        } else {
+          static_cast<float*>(p.out)[at] = d;
+        }
+      }
+    }
+  }
+}
+
+template <int WM, int WN, int FM, int FN, int kStages, int EPI>
+__global__ __launch_bounds__(WM* WN* kWave) void i8_tile_kernel(I8GemmArgs p) {
+  i8_tile_body<WM, WN, FM, FN, kStages, EPI>(p);
+}
+
+template <int WM, int WN, int FM, int FN, int kStages, int EPI>
+hipError_t launch_tiles(I8GemmArgs p, int64_t tiles, hipStream_t stream) {
+  constexpr int kCols = WN * FN * 32 / (EPI == kEpiSwiglu ? 2 : 1);
+  p.n_slices = (p.N + kCols - 1) / kCols;
+  p.tiles_n = tiles;
+  const int64_t blocks = (tiles + kXcds - 1) / kXcds * kXcds * p.n_slices;
+  if (blocks <= 0) return hipSuccess;
+  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((i8_tile_kernel<WM, WN, FM, FN, kStages, EPI>), dim3((unsigned)blocks), dim3(WM * WN * kWave), 0,
+                     stream, p);
+  return hipGetLastError();
+}
+
+// y[t] = sum_i w_i (sums of slot i * its row's scale * the channel's scale) + shared, in slot
+// order, the shared expert last; slots whose id names no expert add nothing.
+template <typename Part>
+__global__ __launch_bounds__(256) void i8_combine_kernel(const Part* __restrict__ part, float unit,
+                                                         const float* __restrict__ sh, const int32_t* __restrict__ inv,
+                                                         const int32_t* __restrict__ ids,
+                                                         const float* __restrict__ weights, int64_t T, int k, int E,
+                                                         int H, int64_t P, const float* __restrict__ sw,
+                                                         const float* __restrict__ sw_shared, void* __restrict__ Y,
+                                                         int out_bf16) {
+  const int per = H / 8;
+  const int64_t total = T * per;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t t = i / per;
+    const int n = (int)(i - t * per) * 8;
+    float y[8] = {};
+    auto add = [&](int64_t pos, float f, const float* s) {
+      float v[8], c[8];
+      if constexpr (std::is_same<Part, float>::value) {
+        i8_load8(part + pos * H + n, v);
+      } else {
+        const half8_t hv = *reinterpret_cast<const half8_t*>(part + pos * H + n);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = (float)hv[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) c[j] = s[n + j];
+      f *= unit;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] += v[j] * f * c[j];
+    };
+    for (int s = 0; s < k; ++s) {
+      const int e = ids[t * k + s];
+      if (e < 0 || e >= E) continue;
+      const int64_t pos = inv[t * k + s];
+      add(pos, sh[pos] * weights[t * k + s], sw + (int64_t)e * H);
+    }
+    if (sw_shared) add(P + t, sh[P + t], sw_shared);
+    if (out_bf16) {
+      uint4 o;
+      o.x = (uint32_t)i8_bf16(y[0]) | ((uint32_t)i8_bf16(y[1]) << 16);
+      o.y = (uint32_t)i8_bf16(y[2]) | ((uint32_t)i8_bf16(y[3]) << 16);
+      o.z = (uint32_t)i8_bf16(y[4]) | ((uint32_t)i8_bf16(y[5]) << 16);
+      o.w = (uint32_t)i8_bf16(y[6]) | ((uint32_t)i8_bf16(y[7]) << 16);
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(Y) + t * H + n) = o;
+    } else {
+      float4* o = reinterpret_cast<float4*>(static_cast<float*>(Y) + t * H + n);
+      o[0] = make_float4(y[0], y[1], y[2], y[3]);
+      o[1] = make_float4(y[4], y[5], y[6], y[7]);
+    }
+  }
+}
+
+constexpr int kExpertRows = 128;  // rows of a grouped tile
+
+struct ExpertsWs {
+  int8_t* xq;            // [T][H] codes of the tokens
+  float* sx;             // [T]
+  int32_t *offsets, *sorted, *inv, *row_src;
+  float* row_w;
+  int4* tiles;
+  void* perm;
+  float* act;            // [R][I] silu(gate) * up of each sorted position
+  int8_t* aq;            // [R][I] its codes
+  float* sh;             // [R]
+  void* part;            // [R][H] sums of the down product: fp16 or fp32
+  size_t total;
+};
+
+ExpertsWs carve(void* base, const I8Experts& L, int64_t T, int k) {
+  ExpertsWs w{};
+  char* c = static_cast<char*>(base);
+  size_t off = 0;
+  auto take = [&](size_t bytes) { char* r = c ? c + off : nullptr; off += align256(bytes); return r; };
+  const int64_t P = T * k, extra = L.sh_gate.codes ? T : 0, R = P + extra;
+  w.xq = reinterpret_cast<int8_t*>(take((size_t)T * L.hidden));
+  w.sx = reinterpret_cast<float*>(take((size_t)T * 4));
+  w.offsets = reinterpret_cast<int32_t*>(take((size_t)(L.n_experts + 1) * 4));
+  w.sorted = reinterpret_cast<int32_t*>(take((size_t)P * 4));
+  w.inv = reinterpret_cast<int32_t*>(take((size_t)P * 4));
+  w.row_src = reinterpret_cast<int32_t*>(take((size_t)P * 4));
+  w.row_w = reinterpret_cast<float*>(take((size_t)P * 4));
+  w.tiles = reinterpret_cast<int4*>(take((size_t)group_max_tiles(P, L.n_experts, extra, kExpertRows) * 16));
+  w.perm = take(permute_workspace_bytes(P, L.n_experts));
+  w.act = reinterpret_cast<float*>(take((size_t)R * L.inter * 4));
+  w.aq = reinterpret_cast<int8_t*>(take((size_t)R * L.inter));
+  w.sh = reinterpret_cast<float*>(take((size_t)R * 4));
+  w.part = take((size_t)R * L.hidden * 4);
+  w.total = off;
+  return w;
+}
+
+}  // namespace
+
+hipError_t run_i8_quantize(const uint16_t* X, int64_t rows, int K, int8_t* codes, float* scales, hipStream_t stream) {
+  return launch_quantize(X, rows, K, codes, scales, stream);
+}
+
+size_t i8_gemm_workspace_bytes(int64_t m, int K) { return align256((size_t)m * K) + align256((size_t)m * 4); }
+
+hipError_t run_i8_gemm(const I8Mat& W, int64_t n, int K, const uint16_t* X, int64_t m, void* Y, int out_bf16, void* ws,
+                       hipStream_t stream) {
+  int8_t* xq = static_cast<int8_t*>(ws);
+  float* sx = reinterpret_cast<float*>(static_cast<char*>(ws) + align256((size_t)m * K));
+  hipError_t e = launch_quantize(X, m, K, xq, sx, stream);
+  if (e != hipSuccess) return e;
+  I8GemmArgs p{};
+  p.A = xq;
+  p.sa = sx;
+  p.rows = m;
+  p.K = K;
+  p.N = (int)n;
+  p.W = p.W2 = p.S = p.S2 = W;
+  p.out = Y;
+  const int64_t tiles = (m + 127) / 128;
+  return out_bf16 ? launch_tiles<2, 2, 2, 2, 3, kEpiBf16>(p, tiles, stream)
+                  : launch_tiles<2, 2, 2, 2, 3, kEpiF32>(p, tiles, stream);
+}
+
+size_t experts_i8_workspace_bytes(const I8Experts& L, int64_t T, int k) { return carve(nullptr, L, T, k).total; }
+
+hipError_t run_moe_experts_i8(const I8Experts& L, const uint16_t* X, int64_t T, const int32_t* ids,
+                              const float* weights, int k, void* Y, int out_bf16, void* ws, hipStream_t stream) {
+  const int H = L.hidden, I = L.inter, E = L.n_experts;
+  const ExpertsWs w = carve(ws, L, T, k);
+  const int64_t P = T * k, extra = L.sh_gate.codes ? T : 0, R = P + extra;
+  const int max_tiles = group_max_tiles(P, E, extra, kExpertRows);
+  hipError_t e = launch_quantize(X, T, H, w.xq, w.sx, stream);
+  if (e != hipSuccess) return e;
+  GroupTiles gt{};
+  gt.tile_rows = kExpertRows;
+  gt.max_tiles = max_tiles;
+  gt.extra_rows = extra;
+  gt.topk = k;
+  gt.table = w.tiles;
+  gt.row_src = w.row_src;
+  gt.row_w = w.row_w;
+  e = run_permute(ids, P, E, w.offsets, w.sorted, w.inv, w.perm, &gt, stream);
+  if (e != hipSuccess) return e;
+
+  I8GemmArgs p{};
+  p.A = w.xq;
+  p.sa = w.sx;
+  p.row_src = w.row_src;
+  p.tiles = w.tiles;
+  p.P = P;
+  p.K = H;
+  p.N = I;
+  p.W = L.gate;
+  p.W2 = L.up;
+  p.S = L.sh_gate;
+  p.S2 = L.sh_up;
+  p.out = w.act;
+  e = launch_tiles<1, 4, 4, 2, 3, kEpiSwiglu>(p, max_tiles, stream);
+  if (e != hipSuccess) return e;
+  e = launch_quantize(w.act, R, I, w.aq, w.sh, stream);
+  if (e != hipSuccess) return e;
+
+  I8GemmArgs d = p;
+  d.A = w.aq;
+  d.sa = w.sh;
+  d.row_src = nullptr;
+  d.K = I;
+  d.N = H;
+  d.W = d.W2 = L.down;
+  d.S = d.S2 = L.sh_down;
+  d.out = w.part;
+  // The sums of a bf16 output are stored as fp16, half the bytes of the round trip: 11
+  // significant bits of each summand against the output's 8.  A sum is at most
+  // 127 * 128 * I, so one power of two per layer keeps it within fp16's range, and the
+  // smallest sums (an integer times it) far above its subnormals.
+  float unit = 1.0f;
+  while (127.0f * 128.0f * I > 65504.0f * unit) unit *= 2.0f;
+  d.mul = 1.0f / unit;
+  e = out_bf16 ? launch_tiles<1, 4, 4, 2, 3, kEpiPartF16>(d, max_tiles, stream)
+               : launch_tiles<1, 4, 4, 2, 3, kEpiPartF32>(d, max_tiles, stream);
+  if (e != hipSuccess) return e;
+
+  const unsigned blocks = (unsigned)std::min<int64_t>((T * (H / 8) + 255) / 256, 65536);
+  const float* sws = extra ? L.sh_down.scales : nullptr;
+  if (out_bf16)
+    hipLaunchKernelGGL(i8_combine_kernel<_Float16>, dim3(blocks), dim3(256), 0, stream,
+                       static_cast<const _Float16*>(w.part), unit, w.sh, w.inv, ids, weights, T, k, E, H, P,
+                       L.down.scales, sws, Y, 1);
+  else
+    hipLaunchKernelGGL(i8_combine_kernel<float>, dim3(blocks), dim3(256), 0, stream,
+                       static_cast<const float*>(w.part), 1.0f, w.sh, w.inv, ids, weights, T, k, E, H, P,
+                       L.down.scales, sws, Y, 0);
+  return hipGetLastError();
+}
+
+}  // namespace q4moe

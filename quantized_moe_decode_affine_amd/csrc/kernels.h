@@ -78,6 +78,23 @@ size_t route_workspace_bytes(int64_t T, int n_experts);
 hipError_t run_route_topk(const uint16_t* router, int E, int H, const uint16_t* X, int64_t T, int k,
                           int32_t* ids, float* weights, void* ws, hipStream_t stream,
                           const Q4Mat* router_q8 = nullptr);
+// The router's logits alone, fp32 [T][E].
+hipError_t run_router_logits(const uint16_t* router, int E, int H, const uint16_t* X, int64_t T, float* logits,
+                             hipStream_t stream, const Q4Mat* router_q8);
+
+// ---- selection rules beyond the softmax top-k (select.hip)
+enum { kScoreSoftmax = 0, kScoreSigmoid = 1 };
+constexpr int kMaxGroups = 64;  // a lane at least per group
+struct RouteRule {
+  int n_experts, top_k, score, n_groups, top_groups, group_terms, renormalise;
+  float scale;
+  const float* bias;  // null, or fp32 [n_experts]
+};
+hipError_t run_select(const RouteRule& r, const float* logits, int64_t T, int32_t* ids, float* weights,
+                      hipStream_t stream);
+// Logits into ws (route_workspace_bytes), then run_select on them.
+hipError_t run_route(const RouteRule& r, const uint16_t* router, const Q4Mat* router_q8, int H, const uint16_t* X,
+                     int64_t T, int32_t* ids, float* weights, void* ws, hipStream_t stream);
 size_t permute_workspace_bytes(int64_t rows, int n_experts);
 
 // Optional output of run_permute for the grouped GEMM: the sorted positions cut
@@ -122,5 +139,23 @@ hipError_t run_pack_group_major(const uint32_t* codes, int64_t count, int64_t n,
 size_t prefill_workspace_bytes(int64_t T, int hidden, int inter, int n_experts, int top_k, int has_shared);
 hipError_t run_moe_ffn_prefill(const DecodeLayer& L, const uint16_t* X, int64_t T, void* Y, int out_bf16,
                                void* ws, hipStream_t stream);
+
+// ---- 8-bit integer products (i8.hip)
+struct I8Mat {
+  const int8_t* codes;  // [count][n][k]
+  const float* scales;  // [count][n]
+};
+struct I8Experts {
+  int hidden, inter, n_experts;
+  I8Mat gate, up, down;           // routed, stacked by expert
+  I8Mat sh_gate, sh_up, sh_down;  // the shared expert, or codes null
+};
+hipError_t run_i8_quantize(const uint16_t* X, int64_t rows, int K, int8_t* codes, float* scales, hipStream_t stream);
+size_t i8_gemm_workspace_bytes(int64_t m, int K);
+hipError_t run_i8_gemm(const I8Mat& W, int64_t n, int K, const uint16_t* X, int64_t m, void* Y, int out_bf16, void* ws,
+                       hipStream_t stream);
+size_t experts_i8_workspace_bytes(const I8Experts& L, int64_t T, int k);
+hipError_t run_moe_experts_i8(const I8Experts& L, const uint16_t* X, int64_t T, const int32_t* ids,
+                              const float* weights, int k, void* Y, int out_bf16, void* ws, hipStream_t stream);
 
 }  // namespace q4moe

@@ -486,16 +486,21 @@ __global__ __launch_bounds__(512) void q8_router_logits_kernel(Q4Mat R, const ui
 
 size_t route_workspace_bytes(int64_t T, int n_experts) { return align256((size_t)T * n_experts * 4); }
 
-hipError_t run_route_topk(const uint16_t* router, int E, int H, const uint16_t* X, int64_t T, int k, int32_t* ids,
-                          float* weights, void* ws, hipStream_t stream, const Q4Mat* router_q8) {
-  float* logits = static_cast<float*>(ws);
+hipError_t run_router_logits(const uint16_t* router, int E, int H, const uint16_t* X, int64_t T, float* logits,
+                             hipStream_t stream, const Q4Mat* router_q8) {
   dim3 grid((unsigned)((T + 31) / 32), (unsigned)((E + 63) / 64));
   if (router_q8 && router_q8->codes)
     hipLaunchKernelGGL(q8_router_logits_kernel, grid, dim3(512), 0, stream, *router_q8, X, T,
                        E, H, logits);
   else
     hipLaunchKernelGGL(router_logits_kernel, grid, dim3(512), 0, stream, router, X, T, E, H, logits);
-  hipError_t e = hipGetLastError();
+  return hipGetLastError();
+}
+
+hipError_t run_route_topk(const uint16_t* router, int E, int H, const uint16_t* X, int64_t T, int k, int32_t* ids,
+                          float* weights, void* ws, hipStream_t stream, const Q4Mat* router_q8) {
+  float* logits = static_cast<float*>(ws);
+  const hipError_t e = run_router_logits(router, E, H, X, T, logits, stream, router_q8);
   if (e != hipSuccess) return e;
   const dim3 tgrid((unsigned)((T + 3) / 4)), tthreads(256);
   if (E <= 4 * kWave)

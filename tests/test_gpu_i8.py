@@ -1,0 +1,334 @@
+"""i8_quantize, i8_gemm and moe_experts_i8 against their 64-bit forms."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import q4moe_oracle as qorc
+from oracle import route_i8_oracle as orc
+from quantized_moe_decode_affine_amd import synth
+from tests.parity_util import bf16_bits, bf16_bits_of_f32, to_f64
+
+pytestmark = pytest.mark.gpu
+
+HALF = 2.0 ** -24       # half a step of fp32 at most, relative
+HALF_F16 = 2.0 ** -11   # the same of fp16
+HALF_BF16 = 2.0 ** -8   # and of bfloat16
+
+
+@pytest.fixture(scope="module")
+def B():
+    from quantized_moe_decode_affine_amd import binding
+    assert torch.cuda.is_available()
+    binding.load_library()
+    return binding
+
+
+def _rows(seed, m, k):
+    rng = np.random.default_rng(seed)
+    x = rng.standard_normal((m, k)) * np.exp(0.7 * rng.standard_normal((m, 1)))
+    return synth.to_bf16_bits(x.astype(np.float32))
+
+
+def _weights(seed, *shape):
+    rng = np.random.default_rng(seed)
+    codes = rng.integers(-127, 128, shape, dtype=np.int8)
+    scales = (rng.random(shape[:-1]) * 0.02 / 73 + 1e-5).astype(np.float32)
+    return codes, scales
+
+
+def _dev(B, w):
+    return B.DeviceI8(torch.from_numpy(w[0]).cuda(), torch.from_numpy(w[1]).cuda())
+
+
+# ------------------------------------------------------------------- quantize --
+
+@pytest.mark.parametrize("rows,k", [(1, 64), (3, 128), (5, 192), (4, 2048), (1030, 320), (2, 16384), (1, 65536)])
+def test_quantize_exact(B, rows, k):
+    X = _rows(rows + k, rows, k)
+    codes, scales = B.i8_quantize(B.bf16_tensor(X))
+    q, s = orc.quantize_rows(qorc.bf16_to_f64(X))
+    np.testing.assert_array_equal(codes.cpu().numpy(), q)
+    np.testing.assert_array_equal(scales.cpu().numpy(), s)
+
+
+def test_quantize_borders_and_extremes(B):
+    k = 128
+    x = np.zeros((12, k), np.float32)
+    x[1] = np.arange(k) / 2 - 32                     # with 127 first: scale 1, halves are ties
+    x[1, 0] = 127.0
+    x[2] = (np.arange(k) / 2 - 32) * 2.0 ** -90
+    x[2, 0] = 127.0 * 2.0 ** -90
+    x[3] = np.arange(k) * 1.0                        # a scale of 127/127 and every integer
+    x[4] = 2.0 ** -133 * (np.arange(k) % 5)          # subnormal bfloat16
+    x[5] = 3.38e38 * (1 - np.arange(k) / 64)         # the type's largest
+    x[6, 5] = np.inf
+    x[7, 9] = np.nan
+    x[8] = -0.0
+    x[9] = 1.0                                       # every value the largest
+    x[10, 3] = -5.5
+    x[11] = np.linspace(-1, 1, k) * 2.0 ** -126
+    X = synth.to_bf16_bits(np.nan_to_num(x, nan=0.0, posinf=0.0))
+    X[6, 5], X[7, 9] = 0x7F80, 0xFFC1
+    codes, scales = B.i8_quantize(B.bf16_tensor(X))
+    v = qorc.bf16_to_f64(X)
+    v[6, 5], v[7, 9] = np.inf, np.nan
+    q, s = orc.quantize_rows(v)
+    np.testing.assert_array_equal(codes.cpu().numpy(), q)
+    np.testing.assert_array_equal(scales.cpu().numpy(), s)
+
+
+# ----------------------------------------------------------------------- gemm --
+
+def _check_gemm(B, W, X, y32, y16):
+    ref = orc.i8_gemm(W[0].reshape(-1, W[0].shape[-1]), W[1].reshape(-1), X)
+    # the sum becomes fp32, then one rounding at each scale
+    assert (np.abs(to_f64(y32) - ref) <= 3 * HALF * (1 + 1e-6) * np.abs(ref) + 2.0 ** -149).all()
+    np.testing.assert_array_equal(bf16_bits(y16), bf16_bits_of_f32(y32))
+
+
+@pytest.mark.parametrize("m,n,k", [
+    (1, 1, 64), (1, 16, 128), (1, 1024, 2048), (2, 17, 192), (3, 100, 64), (4, 1000, 320), (7, 257, 2048),
+    (8, 4099, 256), (9, 64, 4096), (15, 33, 128), (16, 96, 704), (16, 16, 16384), (17, 64, 128), (31, 300, 832),
+    (33, 65, 64), (64, 64, 192), (65, 31, 2048), (100, 513, 320), (127, 128, 128), (129, 255, 576), (256, 1, 64),
+    (381, 1027, 832), (513, 300, 256), (1000, 2048, 192)])
+def test_gemm_parity(B, m, n, k):
+    W, X = _weights(m + n, n, k), _rows(k + m, m, k)
+    d, x = _dev(B, W), B.bf16_tensor(X)
+    _check_gemm(B, W, X, B.i8_gemm(d, x), B.i8_gemm(d, x, B.OUT_BF16))
+
+
+@pytest.mark.parametrize("m", [1, 5, 40, 200])
+def test_gemm_stack(B, m):
+    W, X = _weights(5, 3, 40, 128), _rows(m, m, 128)
+    _check_gemm(B, W, X, B.i8_gemm(_dev(B, W), B.bf16_tensor(X)), B.i8_gemm(_dev(B, W), B.bf16_tensor(X), B.OUT_BF16))
+
+
+@pytest.mark.parametrize("m", [1, 16, 150])
+def test_gemm_largest_sums(B, m):
+    """Every product 127 * -128 over the longest rows: the largest sum there is."""
+    k = 65536
+    W = np.full((3, k), -128, np.int8), np.array([1.0, 0.0, 2.0 ** -20], np.float32)
+    W[0][1] = 127
+    X = synth.to_bf16_bits(np.full((m, k), 3.0, np.float32))
+    _check_gemm(B, W, X, B.i8_gemm(_dev(B, W), B.bf16_tensor(X)), B.i8_gemm(_dev(B, W), B.bf16_tensor(X), B.OUT_BF16))
+
+
+@pytest.mark.parametrize("m", [3, 16, 70])
+def test_gemm_rows_without_values(B, m):
+    """A zero row gives zeros, a row with an infinity or a NaN gives NaN, and no other row notices."""
+    W, X = _weights(1, 200, 192), _rows(m, m, 192)
+    X[0] = 0
+    X[1, 70], X[2, 3] = 0x7F80, 0x7FC1
+    d = _dev(B, W)
+    for out in (B.OUT_F32, B.OUT_BF16):
+        y = B.i8_gemm(d, B.bf16_tensor(X), out)
+        assert (y[0] == 0).all() and torch.isnan(y[1]).all() and torch.isnan(y[2]).all()
+        if m > 3:
+            assert torch.equal(y[3:], B.i8_gemm(d, B.bf16_tensor(X[3:]), out))
+
+
+@pytest.mark.parametrize("m", [2, 33])
+def test_gemm_writes_its_rows_only(B, m):
+    W, X = _weights(2, 72, 128), _rows(m, m, 128)
+    for out, t in ((B.OUT_F32, torch.float32), (B.OUT_BF16, torch.bfloat16)):
+        buf = torch.full((m + 2, 72), 7.0, dtype=t, device="cuda")
+        y = B.i8_gemm(_dev(B, W), B.bf16_tensor(X), out, out=buf[1:m + 1])
+        assert torch.equal(y, B.i8_gemm(_dev(B, W), B.bf16_tensor(X), out))
+        assert (buf[0] == 7).all() and (buf[-1] == 7).all()
+
+
+def test_gemm_of_quantized_weights(B):
+    """From bfloat16 weights on: the product approximates X W^T by the codes' resolution."""
+    w, X = _rows(1, 96, 512), _rows(2, 20, 512)
+    d = B.DeviceI8.quantize(B.bf16_tensor(w))
+    q, s = orc.quantize_rows(qorc.bf16_to_f64(w))
+    _check_gemm(B, (q.astype(np.int8), s.astype(np.float32)), X, B.i8_gemm(d, B.bf16_tensor(X)),
+                B.i8_gemm(d, B.bf16_tensor(X), B.OUT_BF16))
+
+
+def test_gemm_on_two_streams(B):
+    """Calls in flight together, each with a workspace of its own."""
+    W = _dev(B, _weights(3, 512, 1024))
+    xs = [B.bf16_tensor(_rows(n, m, 1024)) for n, m in enumerate((1, 9, 64, 300))]
+    want = [B.i8_gemm(W, x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for x, s in zip(xs, streams):
+            with torch.cuda.stream(s):
+                got.append(B.i8_gemm(W, x))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# -------------------------------------------------------------------- experts --
+
+def _layer(seed, E, H, I, shared):
+    g, u, d = _weights(seed, E, I, H), _weights(seed + 1, E, I, H), _weights(seed + 2, E, H, I)
+    sh = (_weights(seed + 3, 1, I, H), _weights(seed + 4, 1, I, H), _weights(seed + 5, 1, H, I)) if shared else None
+    return g, u, d, sh
+
+
+def _experts(B, layer):
+    g, u, d, sh = layer
+    return B.DeviceI8Experts(*(_dev(B, w) for w in (g, u, d)), shared=None if sh is None else [_dev(B, w) for w in sh])
+
+
+def _ids(seed, T, E, k, empty=0.0):
+    rng = np.random.default_rng(seed)
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    ids[rng.random((T, k)) < empty] = -1
+    return ids, rng.random((T, k)).astype(np.float32)
+
+
+def _check_experts(B, layer, X, ids, w, ex=None):
+    ex = ex or _experts(B, layer)
+    x, i, wt = B.bf16_tensor(X), torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda()
+    y, slack, parts = orc.experts_i8(*layer[:3], X, ids, w, layer[3])
+    y32, y16 = B.moe_experts_i8(ex, x, i, wt), B.moe_experts_i8(ex, x, i, wt, B.OUT_BF16)
+    assert (np.abs(to_f64(y32) - y) <= slack).all()
+    # bfloat16: each summand may be rounded to fp16's 11 significant bits, then the output to 8.
+    # Values in [2^e, 2^(e+1)) with 11 bits are 2^(e-10) apart, so half a step is up to 2^(e-11):
+    # 2^-11 of the value (finfo(float16).eps / 2), not 2^-12.
+    before = slack + HALF_F16 * parts
+    assert (np.abs(to_f64(y16) - y) <= before + HALF_BF16 * (np.abs(y) + before)).all()
+
+
+@pytest.mark.parametrize("T,E,H,I,k,shared", [
+    (1, 8, 64, 64, 1, False), (1, 256, 256, 128, 8, True), (1, 16, 2048, 512, 8, True), (2, 4, 128, 192, 4, False),
+    (3, 60, 1088, 704, 4, True), (5, 16, 192, 64, 2, True), (8, 32, 512, 256, 8, True), (16, 8, 256, 320, 2, False),
+    (17, 16, 256, 128, 4, True), (40, 5, 320, 64, 3, False), (129, 3, 128, 128, 1, True), (300, 2, 192, 64, 2, True),
+    (64, 1, 128, 256, 1, False), (33, 40, 64, 1088, 32, False)])
+def test_experts_parity(B, T, E, H, I, k, shared):
+    layer = _layer(T + E, E, H, I, shared)
+    _check_experts(B, layer, _rows(T, T, H), *_ids(T, T, E, k, 0.1 if T > 2 else 0.0))
+
+
+@pytest.mark.parametrize("T", [1, 6, 150])
+@pytest.mark.parametrize("shared", [False, True])
+def test_experts_empty_slots(B, T, shared):
+    """Tokens whose every slot is empty get the shared expert alone, or zeros."""
+    layer = _layer(9, 6, 128, 64, shared)
+    X = _rows(1, T, 128)
+    ids, w = _ids(2, T, 6, 3)
+    ids[0] = [-1, 6, 2 ** 31 - 1]
+    if T > 2:
+        ids[2] = -2 ** 31
+    w[0] = np.nan                                      # the weight of an empty slot is not read into the sum
+    _check_experts(B, layer, X, ids, w)
+    ids[:] = -1
+    _check_experts(B, layer, X, ids, w)
+    if not shared:
+        y = B.moe_experts_i8(_experts(B, layer), B.bf16_tensor(X), torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda())
+        assert (y == 0).all()
+
+
+@pytest.mark.parametrize("T", [1, 7, 90])
+def test_experts_same_id_twice(B, T):
+    layer = _layer(3, 5, 128, 128, True)
+    ids, w = _ids(4, T, 5, 4)
+    ids[:, 2] = ids[:, 0]
+    ids[:, 3] = ids[:, 0]
+    _check_experts(B, layer, _rows(5, T, 128), ids, w - 0.5)
+
+
+def test_experts_all_to_one(B):
+    """A full expert of several row tiles beside empty ones."""
+    layer = _layer(6, 12, 192, 64, False)
+    ids = np.full((401, 2), 11, np.int32)
+    ids[:, 1] = np.where(np.arange(401) % 5 == 0, 3, -1)
+    _check_experts(B, layer, _rows(7, 401, 192), ids, np.full((401, 2), 0.5, np.float32))
+
+
+@pytest.mark.parametrize("T", [3, 16, 60])
+def test_experts_rows_do_not_mix(B, T):
+    """A token with a NaN, one with an infinity and one of zeros leave the others as they are."""
+    layer = _layer(8, 4, 128, 64, True)
+    ex = _experts(B, layer)
+    X = _rows(9, T, 128)
+    ids, w = _ids(10, T, 4, 2)
+    clean = B.moe_experts_i8(ex, B.bf16_tensor(X), torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda())
+    X[0, 5], X[1, 100] = 0x7FC1, 0xFF80
+    X[2] = 0
+    y = B.moe_experts_i8(ex, B.bf16_tensor(X), torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda())
+    assert torch.isnan(y[:2]).all() and (y[2] == 0).all() and torch.equal(y[3:], clean[3:])
+
+
+def test_experts_workspace_is_not_state(B):
+    """A workspace full of anything, used for calls of several sizes."""
+    layer = _layer(11, 8, 128, 64, True)
+    ex = _experts(B, layer)
+    ws = B.moe_experts_i8_workspace(ex, 200, 3)
+    for n, T in enumerate((200, 1, 17, 4, 130)):
+        X, (ids, w) = B.bf16_tensor(_rows(n, T, 128)), _ids(n, T, 8, 3, 0.3)
+        args = ex, X, torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda()
+        want = B.moe_experts_i8(*args)
+        ws.fill_(255 - n)
+        buf = torch.full((T + 2, 128), 3.0, device="cuda")
+        B.moe_experts_i8(*args, out=buf[1:T + 1], ws=ws)
+        assert torch.equal(buf[1:T + 1], want) and (buf[0] == 3).all() and (buf[-1] == 3).all()
+
+
+@pytest.mark.parametrize("T", [1, 12, 100])
+def test_route_then_experts(B, T):
+    """The router's ids and weights, closed experts among them, into the experts' products; the
+    same in a captured graph that is replayed on other tokens."""
+    E, H, I, k = 24, 256, 128, 4
+    rng = np.random.default_rng(T)
+    R = synth.to_bf16_bits((np.clip(np.round(rng.standard_normal((E, H)) * 20), -255, 255) / 1024).astype(np.float32))
+    tokens = [synth.to_bf16_bits((np.clip(np.round(rng.standard_normal((T, H)) * 8), -40, 40) / 8).astype(np.float32))
+              for _ in range(3)]
+    bias = rng.standard_normal(E).astype(np.float32) * 0.1
+    bias[:4] = -np.inf
+    rule = dict(top_k=k, score="sigmoid", n_groups=6, top_groups=2, scale=2.5)
+    r = B.Routing(B.bf16_tensor(R), bias=torch.from_numpy(bias).cuda(), **rule)
+    layer = _layer(12, E, H, I, True)
+    ex = _experts(B, layer)
+    X = B.bf16_tensor(tokens[0])
+    ws, wr = B.moe_experts_i8_workspace(ex, T, k), B.moe_route_workspace(r, T)
+    ids, w = B.moe_route(r, X, ws=wr)
+    y = B.moe_experts_i8(ex, X, ids, w, ws=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.moe_route(r, X, ids=ids, weights=w, ws=wr)
+        B.moe_experts_i8(ex, X, ids, w, out=y, ws=ws)
+    for bits in tokens:
+        X.copy_(B.bf16_tensor(bits))
+        y.zero_()
+        graph.replay()
+        ref_ids, ref_w = orc.route_rule(qorc.router_logits(R, bits), bias=bias, **rule)
+        np.testing.assert_array_equal(ids.cpu().numpy(), ref_ids)
+        ref, slack, parts = orc.experts_i8(*layer[:3], bits, ref_ids, ref_w, layer[3])
+        assert (np.abs(to_f64(y) - ref) <= slack + 2 * HALF * parts).all()
+        i2, w2 = B.moe_route(r, X)
+        assert torch.equal(B.moe_experts_i8(ex, X, i2, w2), y)
+
+
+def test_refusals(B):
+    W = _dev(B, _weights(1, 64, 128))
+    X = torch.zeros(3, 128, dtype=torch.bfloat16, device="cuda")
+    for bad in (X.float(), X.cpu(), X[:, :64], torch.zeros(128, 3, dtype=torch.bfloat16, device="cuda").T):
+        with pytest.raises(ValueError):
+            B.i8_gemm(W, bad)
+    with pytest.raises(ValueError):
+        B.i8_gemm(W, X, B.OUT_BF16_RESIDUAL)
+    with pytest.raises(ValueError):
+        B.i8_gemm(W, X, out=torch.empty(3, 65, device="cuda"))
+    with pytest.raises(B.Q4Error) as e:
+        B.i8_gemm(W, X, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == B.EWORKSPACE
+    assert B.i8_gemm(W, X[:0]).shape == (0, 64)
+    with pytest.raises(ValueError):
+        B.DeviceI8(torch.zeros(4, 64, dtype=torch.int8, device="cuda"), torch.zeros(5, device="cuda"))
+    ex = _experts(B, _layer(1, 4, 64, 128, False))
+    x = torch.zeros(3, 64, dtype=torch.bfloat16, device="cuda")
+    ids, w = torch.zeros(3, 2, dtype=torch.int32, device="cuda"), torch.zeros(3, 2, device="cuda")
+    with pytest.raises(ValueError):
+        B.moe_experts_i8(ex, x, ids.long(), w)
+    with pytest.raises(ValueError):
+        B.moe_experts_i8(ex, x, ids, w[:, :1])
+    with pytest.raises(ValueError):
+        B.DeviceI8Experts(ex.matrices[0], ex.matrices[1], ex.matrices[0])
+    assert B.moe_experts_i8(ex, x[:0], ids[:0], w[:0]).shape == (0, 64)
