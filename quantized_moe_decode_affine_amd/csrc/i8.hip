@@ -404,6 +404,7 @@ size_t i8_gemm_workspace_bytes(int64_t m, int K) { return align256((size_t)m * K
 
 hipError_t run_i8_gemm(const I8Mat& W, int64_t n, int K, const uint16_t* X, int64_t m, void* Y, int out_bf16, void* ws,
                        hipStream_t stream) {
+  if (i8_few_rows(m, K)) return run_i8_few_rows(W, n, K, X, (int)m, Y, out_bf16, stream);
   int8_t* xq = static_cast<int8_t*>(ws);
   float* sx = reinterpret_cast<float*>(static_cast<char*>(ws) + align256((size_t)m * K));
   hipError_t e = launch_quantize(X, m, K, xq, sx, stream);
@@ -421,10 +422,15 @@ hipError_t run_i8_gemm(const I8Mat& W, int64_t n, int K, const uint16_t* X, int6
                   : launch_tiles<2, 2, 2, 2, 3, kEpiF32>(p, tiles, stream);
 }
 
-size_t experts_i8_workspace_bytes(const I8Experts& L, int64_t T, int k) { return carve(nullptr, L, T, k).total; }
+size_t experts_i8_workspace_bytes(const I8Experts& L, int64_t T, int k) {
+  // a workspace made for T tokens also takes fewer, the few-slots form among them
+  return std::max(carve(nullptr, L, T, k).total, align256(i8_few_slots_bytes(L, T, k)));
+}
 
 hipError_t run_moe_experts_i8(const I8Experts& L, const uint16_t* X, int64_t T, const int32_t* ids,
                               const float* weights, int k, void* Y, int out_bf16, void* ws, hipStream_t stream) {
+  if (i8_few_slots(L, T, k))
+    return run_i8_few_slots(L, X, (int)T, ids, weights, k, Y, out_bf16, static_cast<float*>(ws), stream);
   const int H = L.hidden, I = L.inter, E = L.n_experts;
   const ExpertsWs w = carve(ws, L, T, k);
   const int64_t P = T * k, extra = L.sh_gate.codes ? T : 0, R = P + extra;

@@ -154,6 +154,15 @@ hipError_t run_i8_quantize(const uint16_t* X, int64_t rows, int K, int8_t* codes
 size_t i8_gemm_workspace_bytes(int64_t m, int K);
 hipError_t run_i8_gemm(const I8Mat& W, int64_t n, int K, const uint16_t* X, int64_t m, void* Y, int out_bf16, void* ws,
                        hipStream_t stream);
+// The same for few rows, m <= 16 whose codes fit a workgroup's LDS (i8_small.hip); no workspace.
+bool i8_few_rows(int64_t m, int K);
+hipError_t run_i8_few_rows(const I8Mat& W, int64_t n, int K, const uint16_t* X, int m, void* Y, int out_bf16,
+                           hipStream_t stream);
+// The experts on few slots (a decode step), act: i8_few_slots_bytes of scratch.
+bool i8_few_slots(const I8Experts& L, int64_t T, int k);
+size_t i8_few_slots_bytes(const I8Experts& L, int64_t T, int k);
+hipError_t run_i8_few_slots(const I8Experts& L, const uint16_t* X, int T, const int32_t* ids, const float* weights,
+                            int k, void* Y, int out_bf16, float* act, hipStream_t stream);
 size_t experts_i8_workspace_bytes(const I8Experts& L, int64_t T, int k);
 hipError_t run_moe_experts_i8(const I8Experts& L, const uint16_t* X, int64_t T, const int32_t* ids,
                               const float* weights, int k, void* Y, int out_bf16, void* ws, hipStream_t stream);

@@ -88,7 +88,7 @@ def _check_gemm(B, W, X, y32, y16):
 
 @pytest.mark.parametrize("m,n,k", [
     (1, 1, 64), (1, 16, 128), (1, 1024, 2048), (2, 17, 192), (3, 100, 64), (4, 1000, 320), (7, 257, 2048),
-    (8, 4099, 256), (9, 64, 4096), (15, 33, 128), (16, 96, 704), (16, 16, 16384), (17, 64, 128), (31, 300, 832),
+    (8, 4099, 256), (9, 64, 4096), (15, 33, 128), (16, 96, 704), (16, 40, 4096), (13, 20000, 1088), (5, 40000, 192), (16, 16, 16384), (17, 64, 128), (31, 300, 832),
     (33, 65, 64), (64, 64, 192), (65, 31, 2048), (100, 513, 320), (127, 128, 128), (129, 255, 576), (256, 1, 64),
     (381, 1027, 832), (513, 300, 256), (1000, 2048, 192)])
 def test_gemm_parity(B, m, n, k):
