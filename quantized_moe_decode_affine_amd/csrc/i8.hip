@@ -10,6 +10,7 @@
 // float, at each of the two scales and to its own type.
 #include <algorithm>
 #include <type_traits>
+#include <utility>
 
 #include "int8.h"
 #include "kernels.h"
@@ -27,38 +28,53 @@ __device__ __forceinline__ uint16_t i8_bf16(float f) {
 
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 
-// One wave per row, two passes over it: the largest magnitude, then the codes (the second
-// pass reads what the first left in the caches).  Bound by the row's bytes.
-template <typename In>
+// One wave per row.  Up to kHeld chunks of 8 values per lane stay in registers between the
+// largest magnitude and the codes, the rest of a longer row is read again (from the caches).
+// Bound by the row's bytes.
+template <typename In, int kHeld>
 __global__ __launch_bounds__(256) void i8_quantize_kernel(const In* __restrict__ X, int64_t rows, int K,
                                                           int8_t* __restrict__ codes, float* __restrict__ scales) {
   const int lane = lane_id();
-  const int64_t stride = (int64_t)gridDim.x * 4;
-  for (int64_t r = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave; r < rows; r += stride) {
-    const In* x = X + r * K;
-    uint32_t most = 0;
-    for (int j = lane * 8; j < K; j += kWave * 8) {
-      float v[8];
-      i8_load8(x + j, v);
-      most = i8_most(v, most);
-    }
-    const float scale = i8_scale(wave_max_u32(most));
-    const I8Rounder rd(scale);
-    for (int j = lane * 8; j < K; j += kWave * 8) {
-      float v[8];
-      i8_load8(x + j, v);
-      *reinterpret_cast<uint2*>(codes + r * K + j) =
-          make_uint2(rd.pack4(v[0], v[1], v[2], v[3]), rd.pack4(v[4], v[5], v[6], v[7]));
-    }
-    if (lane == 0) scales[r] = scale;
+  const int64_t r = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave;
+  if (r >= rows) return;
+  const In* x = X + r * K;
+  int8_t* c = codes + r * K;
+  I8Chunk<In> held[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) held[i].load(x + min((i * kWave + lane) * 8, K - 8));
+  uint32_t most = 0;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) most = held[i].most(most);
+  for (int j = (kHeld * kWave + lane) * 8; j < K; j += kWave * 8) {
+    I8Chunk<In> v;
+    v.load(x + j);
+    most = v.most(most);
   }
+  const float scale = i8_scale(wave_max_u32(most));
+  const I8Rounder rd(scale);
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int j = (i * kWave + lane) * 8;
+    if (j < K) *reinterpret_cast<uint2*>(c + j) = held[i].codes(rd);
+  }
+  for (int j = (kHeld * kWave + lane) * 8; j < K; j += kWave * 8) {
+    I8Chunk<In> v;
+    v.load(x + j);
+    *reinterpret_cast<uint2*>(c + j) = v.codes(rd);
+  }
+  if (lane == 0) scales[r] = scale;
 }
 
 template <typename In>
 hipError_t launch_quantize(const In* X, int64_t rows, int K, int8_t* codes, float* scales, hipStream_t stream) {
   if (rows <= 0) return hipSuccess;
-  const int64_t blocks = std::min<int64_t>((rows + 3) / 4, 16384);
-  hipLaunchKernelGGL(i8_quantize_kernel<In>, dim3((unsigned)blocks), dim3(256), 0, stream, X, rows, K, codes, scales);
+  const dim3 grid((unsigned)((rows + 3) / 4)), threads(256);
+  if (K <= 512)
+    hipLaunchKernelGGL((i8_quantize_kernel<In, 1>), grid, threads, 0, stream, X, rows, K, codes, scales);
+  else if (K <= 2048)
+    hipLaunchKernelGGL((i8_quantize_kernel<In, 4>), grid, threads, 0, stream, X, rows, K, codes, scales);
+  else
+    hipLaunchKernelGGL((i8_quantize_kernel<In, 8>), grid, threads, 0, stream, X, rows, K, codes, scales);
   return hipGetLastError();
 }
 
@@ -83,8 +99,14 @@ struct I8GemmArgs {
 
 constexpr int kStepBytes = 128;  // columns of a K step, one cache line of every operand row
 constexpr int kXcds = 8;
+constexpr int kBand = 4;
 
 __device__ __forceinline__ int row_swz(int r) { return (r >> 1) & 7; }
+
+template <typename F, int... St>
+__device__ __forceinline__ void each_stage(F f, std::integer_sequence<int, St...>) {
+  (f(std::integral_constant<int, St>{}), ...);
+}
 
 // Workgroup = WM x WN waves, each FM x FN blocks of 32 x 32 (v_mfma_i32_32x32x32_i8).  Each
 // 128-column K step of both operands goes through LDS by 16-byte DMA loads (8 lanes read a
@@ -96,24 +118,38 @@ template <int WM, int WN, int FM, int FN, int kStages, int EPI>
 __device__ __forceinline__ void i8_tile_body(const I8GemmArgs& p) {
   constexpr int TM = WM * FM * 32, TN = WN * FN * 32, kWaves = WM * WN;
   constexpr int kOps = (TM + TN) / 8 / kWaves;  // DMA loads per wave and step, 8 rows each
-  static_assert((TM + TN) / 8 % kWaves == 0 && (kStages == 2 || kStages == 3), "whole blocks of 8 rows per wave");
+  static_assert((TM + TN) / 8 % kWaves == 0 && kStages >= 2 && kStages <= 6, "whole blocks of 8 rows per wave");
   constexpr int kStageBytes = (TM + TN) * kStepBytes;
   // one array per stage, so that the compiler can tell a stage's reads from the loads
   // still filling another
-  __shared__ __align__(16) uint8_t s_st0[kStageBytes], s_st1[kStageBytes], s_st2[kStages > 2 ? kStageBytes : 16];
+  constexpr auto size = [](int st) { return st < kStages ? kStageBytes : 16; };
+  __shared__ __align__(16) uint8_t s_st0[size(0)], s_st1[size(1)], s_st2[size(2)], s_st3[size(3)], s_st4[size(4)],
+      s_st5[size(5)];
   constexpr bool kSwiglu = EPI == kEpiSwiglu;
   constexpr int kCols = kSwiglu ? TN / 2 : TN;  // output columns of a tile
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int wm = wave / WN, wn = wave % WN;
 
-  // Workgroups go to the XCDs in turn: all slices of a tile stay on one (its rows of A are
-  // read by every slice).
+  // Workgroups go to the XCDs in turn.  Grouped: all slices of a tile stay on one (they read
+  // the same rows of A).  Dense: an XCD takes a run of the tiles in bands of kBand tile rows,
+  // so that the workgroups it runs at a time share rows of A and of W in its L2.
   const int xcd = blockIdx.x % kXcds;
   const int64_t q = blockIdx.x / kXcds;
-  const int64_t tile = q / p.n_slices * kXcds + xcd;
-  const int n0 = (int)(q % p.n_slices) * kCols;
-  if (tile >= p.tiles_n) return;
+  int64_t tile, slice;
+  if (p.tiles) {
+    tile = q / p.n_slices * kXcds + xcd;
+    slice = q % p.n_slices;
+    if (tile >= p.tiles_n) return;
+  } else {
+    const int64_t id = xcd * (int64_t)(gridDim.x / kXcds) + q;
+    if (id >= p.tiles_n * p.n_slices) return;
+    const int64_t band = id / (kBand * p.n_slices), in_band = id - band * kBand * p.n_slices;
+    const int64_t high = min<int64_t>(kBand, p.tiles_n - band * kBand);
+    tile = band * kBand + in_band % high;
+    slice = in_band / high;
+  }
+  const int n0 = (int)slice * kCols;
   int expert = 0;
   int64_t first = tile * TM;
   int rows;
@@ -160,78 +196,110 @@ __device__ __forceinline__ void i8_tile_body(const I8GemmArgs& p) {
       src[j] = (up ? w2.codes : w.codes) + (e_row + row) * p.K;
     }
   }
-  auto stage = [&](int st) -> uint8_t* { return st == 0 ? s_st0 : st == 1 ? s_st1 : s_st2; };
+  auto stage = [&](int st) -> uint8_t* {
+    return st == 0 ? s_st0 : st == 1 ? s_st1 : st == 2 ? s_st2 : st == 3 ? s_st3 : st == 4 ? s_st4 : s_st5;
+  };
   const int steps = (p.K + kStepBytes - 1) / kStepBytes;
   // steps past the last load it again and are not computed
-  auto issue = [&](int i, int st) {
+  auto issue_op = [&](int i, int st, int j) __attribute__((always_inline)) {
     const int k0 = min(i, steps - 1) * kStepBytes;
-#pragma unroll
-    for (int j = 0; j < kOps; ++j)
-      __builtin_amdgcn_global_load_lds(src[j] + min(k0 + piece[j], p.K - 16), stage(st) + dst[j], 16, 0, 0);
+    __builtin_amdgcn_global_load_lds(src[j] + min(k0 + piece[j], p.K - 16), stage(st) + dst[j], 16, 0, 0);
   };
 
+  // Operand reads run one MFMA step (32 columns) ahead of the products.  At the end of a K
+  // step, with the last 32 columns' operands in registers, the workgroup meets: every wave
+  // has read the stage, so its next loads go out, the next stage's first operands are read,
+  // and the last products cover both.
   const int m = lane & 31, h = lane >> 5;
   i32x16_t acc[FM][FN] = {};
-  auto step = [&](int i, auto st_c, auto nf_c) __attribute__((always_inline)) {
-    constexpr int st = decltype(st_c)::value;
+  auto run = [&](auto nf_c) __attribute__((always_inline)) {
     constexpr int NF = decltype(nf_c)::value;
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(kOps * (kStages - 2)));
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    issue(i + kStages - 1, (st + kStages - 1) % kStages);
-    __builtin_amdgcn_sched_barrier(0);
-    if constexpr (NF > 0) {
-      const uint8_t* base = stage(st);
-      const int half = p.K - i * kStepBytes >= kStepBytes ? 4 : 2;  // MFMA steps of 32 columns
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        if (kk >= half) break;
-        i32x4_t a[NF], b[FN];
+    i32x4_t a[2][NF > 0 ? NF : 1], b[2][FN];
+    auto read = [&](const uint8_t* base, int kk, int set) __attribute__((always_inline)) {
+      __builtin_amdgcn_sched_barrier(0);  // these reads go out before the products that follow in the source
+      if constexpr (NF > 0) {
         const int c = 2 * kk + h;
 #pragma unroll
         for (int f = 0; f < NF; ++f) {
           const int r = (wm * FM + f) * 32 + m;
-          a[f] = *reinterpret_cast<const i32x4_t*>(base + r * kStepBytes + ((c ^ row_swz(r)) << 4));
+          a[set][f] = *reinterpret_cast<const i32x4_t*>(base + r * kStepBytes + ((c ^ row_swz(r)) << 4));
         }
 #pragma unroll
         for (int f = 0; f < FN; ++f) {
           const int r = TM + (wn * FN + f) * 32 + m;
-          b[f] = *reinterpret_cast<const i32x4_t*>(base + r * kStepBytes + ((c ^ row_swz(r)) << 4));
+          b[set][f] = *reinterpret_cast<const i32x4_t*>(base + r * kStepBytes + ((c ^ row_swz(r)) << 4));
         }
-#pragma unroll
-        for (int fm = 0; fm < NF; ++fm)
-#pragma unroll
-          for (int fn = 0; fn < FN; ++fn)
-            acc[fm][fn] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[fm], b[fn], acc[fm][fn], 0, 0, 0);
       }
-    }
-  };
-  auto run = [&](auto nf_c) __attribute__((always_inline)) {
-    using S0 = std::integral_constant<int, 0>;
-    using S1 = std::integral_constant<int, 1>;
-    using S2 = std::integral_constant<int, kStages - 1>;
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    // One MFMA step, with the loads [j0, j1) of a K step into stage st between its products.
+    auto mul = [&](int set, int i, auto st_c, auto j0_c, auto j1_c) __attribute__((always_inline)) {
+      constexpr int st = decltype(st_c)::value, j0 = decltype(j0_c)::value, j1 = decltype(j1_c)::value;
+      constexpr int kPer = NF > 0 ? (j1 - j0 + NF - 1) / NF : 0;  // loads after each row of products
+#pragma unroll
+      for (int fm = 0; fm < NF; ++fm) {
+#pragma unroll
+        for (int fn = 0; fn < FN; ++fn)
+          acc[fm][fn] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b[set][fn], a[set][fm], acc[fm][fn], 0, 0, 0);
+        if constexpr (j1 > j0) {
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int j = j0 + fm * kPer; j < min(j1, j0 + (fm + 1) * kPer); ++j) issue_op(i, st, j);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      if constexpr (NF == 0) {
+#pragma unroll
+        for (int j = j0; j < j1; ++j) issue_op(i, st, j);
+      }
+    };
+    auto meet = [&](auto left_c) __attribute__((always_inline)) {  // with that many loads in flight
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(decltype(left_c)::value));
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    using None = std::integral_constant<int, 0>;
+    using Half = std::integral_constant<int, kOps / 2>;
+    using All = std::integral_constant<int, kOps>;
+    // kk = 0's operands are in set 0 on entry, and the next step's on return
+    auto step = [&](int i, auto st_c) __attribute__((always_inline)) {
+      constexpr int st = decltype(st_c)::value;
+      using Free = std::integral_constant<int, (st + kStages - 1) % kStages>;  // the stage read before this one
+      read(stage(st), 1, 1);
+      mul(0, i + kStages - 1, Free{}, Half{}, All{});
+      read(stage(st), 2, 0);
+      mul(1, 0, st_c, None{}, None{});
+      read(stage(st), 3, 1);
+      mul(0, 0, st_c, None{}, None{});
+      meet(std::integral_constant<int, kOps * (kStages - 2)>{});
+      read(stage((st + 1) % kStages), 0, 0);
+      mul(1, i + kStages, st_c, None{}, Half{});
+    };
+    meet(std::integral_constant<int, kOps * (kStages - 2) + kOps / 2>{});
+    read(stage(0), 0, 0);
+    const int full = p.K / kStepBytes;
     int i = 0;
-    if constexpr (kStages == 2) {
-      for (; i + 2 <= steps; i += 2) {
-        step(i, S0{}, nf_c);
-        step(i + 1, S1{}, nf_c);
-      }
-      if (i < steps) step(i, S0{}, nf_c);
-    } else {
-      for (; i + 3 <= steps; i += 3) {
-        step(i, S0{}, nf_c);
-        step(i + 1, S1{}, nf_c);
-        step(i + 2, S2{}, nf_c);
-      }
-      if (i < steps) step(i, S0{}, nf_c);
-      if (i + 1 < steps) step(i + 1, S1{}, nf_c);
+    for (; i + kStages <= full; i += kStages)
+      each_stage([&](auto st_c) { step(i + decltype(st_c)::value, st_c); }, std::make_integer_sequence<int, kStages>{});
+    each_stage(
+        [&](auto st_c) {
+          if (i + decltype(st_c)::value < full) step(i + decltype(st_c)::value, st_c);
+        },
+        std::make_integer_sequence<int, kStages - 1>{});
+    if (p.K % kStepBytes) {  // the last 64 columns
+      read(stage(full % kStages), 1, 1);
+      mul(0, 0, None{}, None{}, None{});
+      mul(1, 0, None{}, None{}, None{});
     }
   };
-  issue(0, 0);
-  if constexpr (kStages > 2) issue(1, 1);
-  // only the 32-row blocks that hold rows are multiplied
-  const int nf = max(0, min(FM, (rows - wm * FM * 32 + 31) / 32));
+#pragma unroll
+  for (int st = 0; st < kStages; ++st)
+#pragma unroll
+    for (int j = 0; j < (st + 1 < kStages ? kOps : kOps / 2); ++j) issue_op(st, st, j);
+  // grouped tiles are often part full: only the 32-row blocks that hold rows are multiplied
+  constexpr bool kPart = EPI != kEpiF32 && EPI != kEpiBf16;
+  const int nf = kPart ? max(0, min(FM, (rows - wm * FM * 32 + 31) / 32)) : FM;
   if (nf == FM) run(std::integral_constant<int, FM>{});
   else if (FM > 3 && nf == 3) run(std::integral_constant<int, (FM > 3 ? 3 : 0)>{});
   else if (FM > 2 && nf == 2) run(std::integral_constant<int, (FM > 2 ? 2 : 0)>{});
@@ -239,48 +307,80 @@ __device__ __forceinline__ void i8_tile_body(const I8GemmArgs& p) {
   else run(std::integral_constant<int, 0>{});
   __builtin_amdgcn_s_waitcnt(0);  // the repeated loads of the last steps are still landing
 
-  // D layout: column = lane % 32, row = 8*(i/4) + 4*(lane/32) + i%4
+  // The weight is the first operand of the products, so that a lane holds sums of one row of
+  // A (lane % 32) and four consecutive output columns (8*(i/4) + 4*(lane/32) + i%4).  Stored
+  // from there a column quad of 32 rows would touch 32 cache lines, at a power-of-two
+  // distance for most N; so each wave turns 32 rows at a time in LDS and stores whole rows
+  // of its columns, 16 bytes a lane.
+  constexpr bool kPartial = EPI == kEpiPartF16 || EPI == kEpiPartF32;
+  constexpr bool kHalf = EPI == kEpiBf16 || EPI == kEpiPartF16;
+  typedef typename std::conditional<kHalf, uint16_t, float>::type out_t;
+  constexpr int kOutF = kSwiglu ? FN / 2 : FN;
+  constexpr int kRow = kOutF * 32 * sizeof(out_t), kPitch = kRow + 16;  // the pad spreads the rows over the banks
+  constexpr int kVec = 16 / sizeof(out_t);
+  static_assert(kWaves % 2 == 0 && kWaves / 2 * 32 * kPitch <= kStageBytes, "the waves' blocks fit two stages");
+  uint8_t* turn = (wave < kWaves / 2 ? s_st0 : s_st1) + wave % (kWaves / 2) * 32 * kPitch;
+  const bool whole = p.N % kVec == 0;  // 16 bytes of a row are inside or outside together, and aligned
+  const int c0 = n0 + wn * kOutF * 32;
+  __builtin_amdgcn_s_barrier();  // no wave reads the stages any more
 #pragma unroll
   for (int fm = 0; fm < FM; ++fm) {
     const int r0 = (wm * FM + fm) * 32;
     if (r0 >= rows) break;
-    float sa[16];
-    if constexpr (EPI != kEpiPartF16 && EPI != kEpiPartF32) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int64_t pos = first + min(r0 + 8 * (i >> 2) + 4 * h + (i & 3), rows - 1);
-        const int64_t a = p.row_src ? (pos < p.P ? (int64_t)p.row_src[pos] : pos - p.P) : pos;
-        sa[i] = p.sa[a];
-      }
+    float sa = 0.f;
+    if constexpr (!kPartial) {
+      const int64_t pos = first + min(r0 + m, rows - 1);
+      sa = p.sa[p.row_src ? (pos < p.P ? (int64_t)p.row_src[pos] : pos - p.P) : pos];
     }
-    constexpr int kOutF = kSwiglu ? FN / 2 : FN;
 #pragma unroll
-    for (int fn = 0; fn < kOutF; ++fn) {
-      const int n = n0 + (wn * kOutF + fn) * 32 + m;
-      if (n >= p.N) continue;
-      float sw = 0.f, su = 0.f;
-      if constexpr (EPI != kEpiPartF16 && EPI != kEpiPartF32) sw = w.scales[e_row + n];
-      if constexpr (kSwiglu) su = w2.scales[e_row + n];
+    for (int fn = 0; fn < kOutF; ++fn)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int r = r0 + 8 * (i >> 2) + 4 * h + (i & 3);
-        if (r >= rows) continue;
-        const int64_t at = (first + r) * p.N + n;
-        const float d = (float)acc[fm][fn][i];
-        if constexpr (EPI == kEpiF32) {
-          static_cast<float*>(p.out)[at] = d * sa[i] * sw;
-        } else if constexpr (EPI == kEpiBf16) {
-          static_cast<uint16_t*>(p.out)[at] = i8_bf16(d * sa[i] * sw);
-        } else if constexpr (kSwiglu) {
-          const float g = d * sa[i] * sw, u = (float)acc[fm][fn + FN / 2][i] * sa[i] * su;
-          static_cast<float*>(p.out)[at] = g / (1.0f + expf(-g)) * u;
-        } else if constexpr (EPI == kEpiPartF16) {
-          static_cast<_Float16*>(p.out)[at] = (_Float16)(d * p.mul);
-        } else {
-          static_cast<float*>(p.out)[at] = d;
+      for (int q = 0; q < 4; ++q) {
+        const int c = fn * 32 + 8 * q + 4 * h;
+        out_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float d = (float)acc[fm][fn][4 * q + j];
+          const int64_t row = e_row + min(c0 + c + j, p.N - 1);
+          if constexpr (kSwiglu) {
+            const float g = d * sa * w.scales[row];
+            const float u = (float)acc[fm][fn + FN / 2][4 * q + j] * sa * w2.scales[row];
+            o[j] = g / (1.0f + expf(-g)) * u;
+          } else if constexpr (EPI == kEpiPartF16) {
+            o[j] = __builtin_bit_cast(uint16_t, (_Float16)(d * p.mul));
+          } else if constexpr (EPI == kEpiPartF32) {
+            o[j] = d;
+          } else if constexpr (EPI == kEpiBf16) {
+            o[j] = i8_bf16(d * sa * w.scales[row]);
+          } else {
+            o[j] = d * sa * w.scales[row];
+          }
         }
+        uint8_t* to = turn + m * kPitch + c * sizeof(out_t);
+        if constexpr (kHalf)
+          *reinterpret_cast<uint2*>(to) = make_uint2(o[0] | (uint32_t)o[1] << 16, o[2] | (uint32_t)o[3] << 16);
+        else
+          *reinterpret_cast<float4*>(to) = make_float4(o[0], o[1], o[2], o[3]);
+      }
+    __builtin_amdgcn_wave_barrier();  // the block is the wave's own, and LDS keeps its order
+    constexpr int kLanes = kRow / 16;
+#pragma unroll
+    for (int b = 0; b < 32; b += kWave / kLanes) {
+      const int r = b + lane / kLanes, c = lane % kLanes * kVec;
+      const uint4 v = *reinterpret_cast<const uint4*>(turn + r * kPitch + c * sizeof(out_t));
+      if (r0 + r >= rows || c0 + c >= p.N) continue;
+      out_t* out = static_cast<out_t*>(p.out) + (first + r0 + r) * p.N + c0 + c;
+      if (whole) {
+        *reinterpret_cast<uint4*>(out) = v;
+      } else {
+        out_t e[kVec];
+        __builtin_memcpy(e, &v, 16);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+          if (c0 + c + j < p.N) out[j] = e[j];
       }
     }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -294,7 +394,8 @@ hipError_t launch_tiles(I8GemmArgs p, int64_t tiles, hipStream_t stream) {
   constexpr int kCols = WN * FN * 32 / (EPI == kEpiSwiglu ? 2 : 1);
   p.n_slices = (p.N + kCols - 1) / kCols;
   p.tiles_n = tiles;
-  const int64_t blocks = (tiles + kXcds - 1) / kXcds * kXcds * p.n_slices;
+  const int64_t blocks = p.tiles ? (tiles + kXcds - 1) / kXcds * kXcds * p.n_slices
+                                 : (tiles * p.n_slices + kXcds - 1) / kXcds * kXcds;
   if (blocks <= 0) return hipSuccess;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
   hipLaunchKernelGGL((i8_tile_kernel<WM, WN, FM, FN, kStages, EPI>), dim3((unsigned)blocks), dim3(WM * WN * kWave), 0,
@@ -321,7 +422,9 @@ __global__ __launch_bounds__(256) void i8_combine_kernel(const Part* __restrict_
     auto add = [&](int64_t pos, float f, const float* s) {
       float v[8], c[8];
       if constexpr (std::is_same<Part, float>::value) {
-        i8_load8(part + pos * H + n, v);
+        const float4* q = reinterpret_cast<const float4*>(part + pos * H + n);
+        v[0] = q[0].x; v[1] = q[0].y; v[2] = q[0].z; v[3] = q[0].w;
+        v[4] = q[1].x; v[5] = q[1].y; v[6] = q[1].z; v[7] = q[1].w;
       } else {
         const half8_t hv = *reinterpret_cast<const half8_t*>(part + pos * H + n);
 #pragma unroll
@@ -417,9 +520,13 @@ hipError_t run_i8_gemm(const I8Mat& W, int64_t n, int K, const uint16_t* X, int6
   p.N = (int)n;
   p.W = p.W2 = p.S = p.S2 = W;
   p.out = Y;
-  const int64_t tiles = (m + 127) / 128;
-  return out_bf16 ? launch_tiles<2, 2, 2, 2, 3, kEpiBf16>(p, tiles, stream)
-                  : launch_tiles<2, 2, 2, 2, 3, kEpiF32>(p, tiles, stream);
+#ifndef CFG
+#define CFG 2, 2, 2, 2, 3
+#define CTM 128
+#endif
+  const int64_t tiles = (m + CTM - 1) / CTM;
+  return out_bf16 ? launch_tiles<CFG, kEpiBf16>(p, tiles, stream)
+                  : launch_tiles<CFG, kEpiF32>(p, tiles, stream);
 }
 
 size_t experts_i8_workspace_bytes(const I8Experts& L, int64_t T, int k) {

@@ -29,17 +29,6 @@ constexpr int kBatchCols = kBatch * 64;
 // bytes.
 __device__ __forceinline__ int image_at(int col, int r, int m) { return ((col >> 4) * m + r) * 16 + (col & 15); }
 
-typedef uint16_t u16x8_t __attribute__((ext_vector_type(8)));
-typedef float f32x8_t __attribute__((ext_vector_type(8)));
-__device__ __forceinline__ void widen(u16x8_t c, float (&v)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = bf16_bits_to_f32(c[j]);
-}
-__device__ __forceinline__ void widen(f32x8_t c, float (&v)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = c[j];
-}
-
 // Quantizes a row of K values into row r of the image, by `parts` waves of which this is
 // number `part` (parts = 1: meet does nothing): they meet once, to share their maxima.
 // between() runs when the row's loads are on their way: what it loads arrives behind them
@@ -50,43 +39,33 @@ __device__ __forceinline__ float quantize_row(const In* x, int K, int Kpad, uint
   const int lane = lane_id();
   // chunks of 8 values per lane that stay in registers between the two passes
   constexpr int kHeld = sizeof(In) == 2 ? 4 : 2;
-  typedef In chunk_t __attribute__((ext_vector_type(8)));
   const int j0 = (part * kWave + lane) * 8, step = parts * kWave * 8;
-  chunk_t held[kHeld];
+  I8Chunk<In> held[kHeld];
 #pragma unroll
-  for (int c = 0; c < kHeld; ++c) held[c] = *reinterpret_cast<const chunk_t*>(x + min(j0 + c * step, K - 8));
+  for (int c = 0; c < kHeld; ++c) held[c].load(x + min(j0 + c * step, K - 8));
   __builtin_amdgcn_sched_barrier(0);
   between();
   __builtin_amdgcn_sched_barrier(0);
   uint32_t most = 0;
 #pragma unroll
-  for (int c = 0; c < kHeld; ++c) {
-    float u[8];
-    widen(held[c], u);
-    most = i8_most(u, most);
-  }
+  for (int c = 0; c < kHeld; ++c) most = held[c].most(most);
   for (int j = j0 + kHeld * step; j < K; j += step) {
-    float u[8];
-    i8_load8(x + j, u);
-    most = i8_most(u, most);
+    I8Chunk<In> v;
+    v.load(x + j);
+    most = v.most(most);
   }
   const float scale = i8_scale(meet(wave_max_u32(most)));
   const I8Rounder rd(scale);
-  auto put = [&](int j, const float (&u)[8]) {
-    *reinterpret_cast<uint2*>(image + image_at(j, r, m)) =
-        make_uint2(rd.pack4(u[0], u[1], u[2], u[3]), rd.pack4(u[4], u[5], u[6], u[7]));
-  };
+  auto put = [&](int j, const I8Chunk<In>& v) { *reinterpret_cast<uint2*>(image + image_at(j, r, m)) = v.codes(rd); };
 #pragma unroll
   for (int c = 0; c < kHeld; ++c) {
     if (j0 - lane * 8 + c * step >= K) break;  // uniform: the rest holds nothing of the row
-    float u[8];
-    widen(held[c], u);
-    if (j0 + c * step < K) put(j0 + c * step, u);
+    if (j0 + c * step < K) put(j0 + c * step, held[c]);
   }
   for (int j = j0 + kHeld * step; j < K; j += step) {
-    float u[8];
-    i8_load8(x + j, u);
-    put(j, u);
+    I8Chunk<In> v;
+    v.load(x + j);
+    put(j, v);
   }
   for (int j = K + j0; j < Kpad; j += step)
     *reinterpret_cast<uint2*>(image + image_at(j, r, m)) = make_uint2(0u, 0u);

@@ -47,27 +47,25 @@ struct I8Rounder {
   }
 };
 
-// Eight consecutive values of a row as fp32.
-__device__ __forceinline__ void i8_load8(const uint16_t* p, float (&v)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    v[2 * j] = __uint_as_float(w[j] << 16);
-    v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+// Eight consecutive values of a row as they lie in memory.
+template <typename In>
+struct I8Chunk {
+  typedef In vec_t __attribute__((ext_vector_type(8)));
+  vec_t raw;
+  __device__ __forceinline__ void load(const In* p) { raw = *reinterpret_cast<const vec_t*>(p); }
+  __device__ __forceinline__ float at(int j) const {
+    if constexpr (sizeof(In) == 2) return bf16_bits_to_f32(raw[j]);
+    else return raw[j];
   }
-}
-__device__ __forceinline__ void i8_load8(const float* p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-
-// Bits of the largest magnitude among eight values, and the running maximum before them.
-__device__ __forceinline__ uint32_t i8_most(const float (&v)[8], uint32_t most) {
+  // Bits of the largest magnitude among them and `m`.
+  __device__ __forceinline__ uint32_t most(uint32_t m) const {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) most = max(most, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-  return most;
-}
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(at(j)) & 0x7FFFFFFFu);
+    return m;
+  }
+  __device__ __forceinline__ uint2 codes(const I8Rounder& rd) const {
+    return make_uint2(rd.pack4(at(0), at(1), at(2), at(3)), rd.pack4(at(4), at(5), at(6), at(7)));
+  }
+};
 
 }  // namespace q4moe
