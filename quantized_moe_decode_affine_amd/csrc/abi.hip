@@ -159,9 +159,9 @@ int i8_experts_check(const q4moe_i8_experts* L, int64_t T, int64_t top_k, q4moe:
   const bool shared = L->sh_gate.codes != nullptr;
   if (shared && (!i8_shape(L->sh_gate, 1, I, H) || !i8_shape(L->sh_up, 1, I, H) || !i8_shape(L->sh_down, 1, H, I)))
     return Q4MOE_EINVAL;
-  // sorted positions and the tiles' grid are 32-bit
+  // sorted positions, the tiles' grid and the offsets of gathered rows are 32-bit
   const int64_t rows = T > kMaxRows32 ? kMaxRows32 : T * (top_k + 1);
-  if (T > kMaxRows32 || rows > kMaxRows32 || (rows / 64 + 2 * E + 8) * (std::max(H, I) / 64 + 1) > kMaxRows32)
+  if (T > kMaxRows32 || rows > kMaxRows32 || T * H > 0xFFFFFFFFll || (rows / 64 + 2 * E + 8) * (std::max(H, I) / 64 + 1) > kMaxRows32)
     return Q4MOE_EUNSUPPORTED;
   auto mat = [](const q4moe_i8_matrix& W) { return q4moe::I8Mat{W.codes, W.scales}; };
   const q4moe::I8Mat none{nullptr, nullptr};

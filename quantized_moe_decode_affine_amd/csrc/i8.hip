@@ -87,6 +87,7 @@ struct I8GemmArgs {
   const int32_t* row_src;  // grouped: row of A of each sorted position (null: the position itself)
   const int4* tiles;       // grouped: {expert (-1 shared, -2 none), first position, rows, 0}; null: dense
   int64_t rows;            // dense: rows of A
+  uint32_t a_rows;         // gathered: rows of A (a_rows * K below 2^32)
   int64_t P;               // grouped: routed positions; position P + t is token t's for the shared expert
   int K, N;                // N output columns (SwiGLU: gate columns, as many up columns)
   I8Mat W, W2;             // weights (stacked by expert), SwiGLU: gate and up
@@ -112,8 +113,8 @@ __device__ __forceinline__ void each_stage(F f, std::integer_sequence<int, St...
 // 128-column K step of both operands goes through LDS by 16-byte DMA loads (8 lanes read a
 // row's whole line) in kStages stages; inside a row the eight 16-byte pieces are
 // XOR-rotated by row bits 1-3 so that the operand reads (a row per lane) spread over all
-// banks.  K is a multiple of 64: where it is not one of 128 the last step's upper pieces
-// repeat the row's last one and are not multiplied.
+// banks.  K is a multiple of 64: where it is not one of 128 the last step's upper half is
+// not multiplied (its bytes are the next row's, or zeros).
 template <int WM, int WN, int FM, int FN, int kStages, int EPI>
 __device__ __forceinline__ void i8_tile_body(const I8GemmArgs& p) {
   constexpr int TM = WM * FM * 32, TN = WN * FN * 32, kWaves = WM * WN;
@@ -134,24 +135,26 @@ __device__ __forceinline__ void i8_tile_body(const I8GemmArgs& p) {
   // Workgroups go to the XCDs in turn.  Grouped: all slices of a tile stay on one (they read
   // the same rows of A).  Dense: an XCD takes a run of the tiles in bands of kBand tile rows,
   // so that the workgroups it runs at a time share rows of A and of W in its L2.
-  const int xcd = blockIdx.x % kXcds;
-  const int64_t q = blockIdx.x / kXcds;
-  int64_t tile, slice;
+  const uint32_t xcd = blockIdx.x % kXcds, q = blockIdx.x / kXcds, slices = p.n_slices;
+  uint32_t tile, slice;
   if (p.tiles) {
-    tile = q / p.n_slices * kXcds + xcd;
-    slice = q % p.n_slices;
-    if (tile >= p.tiles_n) return;
+    tile = q / slices * kXcds + xcd;
+    slice = q % slices;
   } else {
-    const int64_t id = xcd * (int64_t)(gridDim.x / kXcds) + q;
-    if (id >= p.tiles_n * p.n_slices) return;
-    const int64_t band = id / (kBand * p.n_slices), in_band = id - band * kBand * p.n_slices;
-    const int64_t high = min<int64_t>(kBand, p.tiles_n - band * kBand);
+    const uint32_t id = xcd * (gridDim.x / kXcds) + q;
+    if (id >= (uint32_t)p.tiles_n * slices) return;  // the grid is rounded up to the XCDs
+    const uint32_t band = id / (kBand * slices), in_band = id - band * (kBand * slices);
+    const uint32_t high = min((uint32_t)kBand, (uint32_t)p.tiles_n - band * kBand);
     tile = band * kBand + in_band % high;
     slice = in_band / high;
   }
+  // (uniform, but divisions leave them in vector registers)
+  tile = __builtin_amdgcn_readfirstlane(tile);
+  slice = __builtin_amdgcn_readfirstlane(slice);
+  if (tile >= p.tiles_n) return;
   const int n0 = (int)slice * kCols;
   int expert = 0;
-  int64_t first = tile * TM;
+  int64_t first = (int64_t)tile * TM;
   int rows;
   if (p.tiles) {
     const int4 tl = p.tiles[tile];
@@ -160,50 +163,58 @@ __device__ __forceinline__ void i8_tile_body(const I8GemmArgs& p) {
     first = __builtin_amdgcn_readfirstlane(tl.y);
     rows = __builtin_amdgcn_readfirstlane(tl.z);
   } else {
-    rows = (int)min<int64_t>(TM, p.rows - first);
+    rows = min(TM, (int)(p.rows - first));
   }
   const I8Mat w = expert < 0 ? p.S : p.W, w2 = expert < 0 ? p.S2 : p.W2;
   const int64_t e_row = (int64_t)max(expert, 0) * p.N;  // first row of this expert's matrix
 
-  // Column c of the tile, 0..TN: output column and matrix.  SwiGLU: a wave's first FN/2
-  // blocks are gate rows and the rest the up rows of the same columns, so that a lane holds both.
-  auto w_row = [&](int c, bool* up) -> int {
-    if constexpr (kSwiglu) {
-      const int b = c / 32, f = b % FN;
-      *up = f >= FN / 2;
-      return n0 + ((b / FN) * (FN / 2) + f % (FN / 2)) * 32 + c % 32;
-    } else {
-      *up = false;
-      return n0 + c;
-    }
-  };
-
-  const int8_t* src[kOps];
-  int dst[kOps], piece[kOps];
+  // Loads of this wave: kOpsA blocks of 8 rows of A and kOpsW of W.  The buffers' bounds are
+  // the matrix (or the tile's rows): what lies beyond reads as zero, and the 32-bit offsets
+  // need no arithmetic per step.  SwiGLU: the first half of the loads are gate rows, the
+  // second the up rows of the same columns, placed so that a wave's first FN/2 blocks of 32
+  // columns are gate and the rest up, and a lane holds both.
+  constexpr int kOpsA = TM / 8 / kWaves, kOpsW = TN / 8 / kWaves;
+  constexpr int kOpsG = kSwiglu ? kOpsW / 2 : kOpsW;
+  int off[kOps], dst[kOps];
+  const int piece = lane & 7;
 #pragma unroll
   for (int j = 0; j < kOps; ++j) {
-    const int blk = wave * kOps + j;
-    const int r = blk * 8 + (lane >> 3);
-    piece[j] = ((lane & 7) ^ row_swz(r)) * 16;
-    dst[j] = blk * 8 * kStepBytes;
-    if (blk < TM / 8) {
-      const int64_t pos = first + min(r, rows - 1);
-      const int64_t a = p.row_src ? (pos < p.P ? (int64_t)p.row_src[pos] : pos - p.P) : pos;
-      src[j] = p.A + a * p.K;
+    int blk, row;  // block of 8 rows in the stage, row of the operand
+    if (j < kOpsA) {
+      blk = wave * kOpsA + j;
+      const int r = blk * 8 + (lane >> 3);
+      row = r;
+      if (p.row_src) {  // gathered rows: offsets from the whole matrix
+        const int64_t pos = first + min(r, rows - 1);
+        row = pos < p.P ? p.row_src[pos] : (int)(pos - p.P);
+      }
     } else {
-      bool up;
-      const int row = min(w_row(r - TM, &up), p.N - 1);
-      src[j] = (up ? w2.codes : w.codes) + (e_row + row) * p.K;
+      const bool up = j - kOpsA >= kOpsG;
+      const int i = wave * kOpsG + (j - kOpsA) % kOpsG;  // block of 8 of this matrix's columns
+      row = i * 8 + (lane >> 3);
+      const int b = i / 4;  // block of 32 of them
+      blk = TM / 8 + (kSwiglu ? (b / (FN / 2) * FN + b % (FN / 2) + (up ? FN / 2 : 0)) * 4 + i % 4 : i);
     }
+    const int r = blk * 8 + (lane >> 3);
+    off[j] = (int)((uint32_t)row * (uint32_t)p.K + (uint32_t)(piece ^ row_swz(r)) * 16);
+    dst[j] = blk * 8 * kStepBytes;
   }
+  auto rsrc = [&](const int8_t* base, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(base), 0, (int)bytes, kBufferRsrcWord3);
+  };
+  const int64_t w_off = (e_row + n0) * p.K;
+  const uint32_t w_bytes = (uint32_t)min(kCols, p.N - n0) * (uint32_t)p.K;  // a tile's rows: at most 256 * 65536
+  const __amdgpu_buffer_rsrc_t ra =
+      rsrc(p.row_src ? p.A : p.A + first * p.K, (p.row_src ? p.a_rows : (uint32_t)rows) * (uint32_t)p.K);
+  const __amdgpu_buffer_rsrc_t rw = rsrc(w.codes + w_off, w_bytes), ru = rsrc(w2.codes + w_off, w_bytes);
   auto stage = [&](int st) -> uint8_t* {
     return st == 0 ? s_st0 : st == 1 ? s_st1 : st == 2 ? s_st2 : st == 3 ? s_st3 : st == 4 ? s_st4 : s_st5;
   };
   const int steps = (p.K + kStepBytes - 1) / kStepBytes;
   // steps past the last load it again and are not computed
   auto issue_op = [&](int i, int st, int j) __attribute__((always_inline)) {
-    const int k0 = min(i, steps - 1) * kStepBytes;
-    __builtin_amdgcn_global_load_lds(src[j] + min(k0 + piece[j], p.K - 16), stage(st) + dst[j], 16, 0, 0);
+    const __amdgpu_buffer_rsrc_t r = j < kOpsA ? ra : j < kOpsA + kOpsG ? rw : ru;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, stage(st) + dst[j], 16, off[j], min(i, steps - 1) * kStepBytes, 0, 0);
   };
 
   // Operand reads run one MFMA step (32 columns) ahead of the products.  At the end of a K
@@ -520,13 +531,24 @@ hipError_t run_i8_gemm(const I8Mat& W, int64_t n, int K, const uint16_t* X, int6
   p.N = (int)n;
   p.W = p.W2 = p.S = p.S2 = W;
   p.out = Y;
-#ifndef CFG
-#define CFG 2, 2, 2, 2, 3
-#define CTM 128
-#endif
-  const int64_t tiles = (m + CTM - 1) / CTM;
-  return out_bf16 ? launch_tiles<CFG, kEpiBf16>(p, tiles, stream)
-                  : launch_tiles<CFG, kEpiF32>(p, tiles, stream);
+  // The tile by the time that its rounds of workgroups take, in microseconds per 128 columns
+  // of K (measured on 8192 x 8192 x 4096): 256 x 256, one workgroup on a compute unit, 1.95;
+  // 128 x 128, two, 1.14; 64 x 64, three, 0.63.  The large tile moves the fewest bytes (that
+  // product takes 250, 292 and 430 us), a small one spreads few rows over the chip: 512 rows
+  // on 2048 x 2048 take 32, 21 and 13 us with it.
+  const int64_t cus = device_cu_count();
+  auto rounds = [&](int64_t t, int64_t at_once) {
+    return (double)(((m + t - 1) / t * ((n + t - 1) / t) + cus * at_once - 1) / (cus * at_once));
+  };
+  const double large = rounds(256, 1) * 1.95, middle = rounds(128, 2) * 1.14, small = rounds(64, 3) * 0.63;
+  if (large <= middle && large <= small)
+    return out_bf16 ? launch_tiles<2, 4, 4, 2, 2, kEpiBf16>(p, (m + 255) / 256, stream)
+                    : launch_tiles<2, 4, 4, 2, 2, kEpiF32>(p, (m + 255) / 256, stream);
+  if (middle <= small)
+    return out_bf16 ? launch_tiles<2, 2, 2, 2, 2, kEpiBf16>(p, (m + 127) / 128, stream)
+                    : launch_tiles<2, 2, 2, 2, 2, kEpiF32>(p, (m + 127) / 128, stream);
+  return out_bf16 ? launch_tiles<2, 2, 1, 1, 3, kEpiBf16>(p, (m + 63) / 64, stream)
+                  : launch_tiles<2, 2, 1, 1, 3, kEpiF32>(p, (m + 63) / 64, stream);
 }
 
 size_t experts_i8_workspace_bytes(const I8Experts& L, int64_t T, int k) {
@@ -559,6 +581,7 @@ hipError_t run_moe_experts_i8(const I8Experts& L, const uint16_t* X, int64_t T, 
   p.A = w.xq;
   p.sa = w.sx;
   p.row_src = w.row_src;
+  p.a_rows = (uint32_t)T;
   p.tiles = w.tiles;
   p.P = P;
   p.K = H;

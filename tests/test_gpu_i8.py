@@ -80,17 +80,20 @@ def test_quantize_borders_and_extremes(B):
 # ----------------------------------------------------------------------- gemm --
 
 def _check_gemm(B, W, X, y32, y16):
-    ref = orc.i8_gemm(W[0].reshape(-1, W[0].shape[-1]), W[1].reshape(-1), X)
+    some = slice(None) if X.shape[0] <= 1000 else slice(X.shape[0] % 17, None, 17)
+    np.testing.assert_array_equal(bf16_bits(y16), bf16_bits_of_f32(y32))
+    y32 = y32[some]
+    ref = orc.i8_gemm(W[0].reshape(-1, W[0].shape[-1]), W[1].reshape(-1), X[some])
     # the sum becomes fp32, then one rounding at each scale
     assert (np.abs(to_f64(y32) - ref) <= 3 * HALF * (1 + 1e-6) * np.abs(ref) + 2.0 ** -149).all()
-    np.testing.assert_array_equal(bf16_bits(y16), bf16_bits_of_f32(y32))
 
 
 @pytest.mark.parametrize("m,n,k", [
     (1, 1, 64), (1, 16, 128), (1, 1024, 2048), (2, 17, 192), (3, 100, 64), (4, 1000, 320), (7, 257, 2048),
     (8, 4099, 256), (9, 64, 4096), (15, 33, 128), (16, 96, 704), (16, 40, 4096), (13, 20000, 1088), (5, 40000, 192), (16, 16, 16384), (17, 64, 128), (31, 300, 832),
     (33, 65, 64), (64, 64, 192), (65, 31, 2048), (100, 513, 320), (127, 128, 128), (129, 255, 576), (256, 1, 64),
-    (381, 1027, 832), (513, 300, 256), (1000, 2048, 192)])
+    (381, 1027, 832), (513, 300, 256), (1000, 2048, 192),
+    (2000, 2100, 320), (3900, 4100, 128), (4100, 3999, 64), (2049, 4095, 448)])
 def test_gemm_parity(B, m, n, k):
     W, X = _weights(m + n, n, k), _rows(k + m, m, k)
     d, x = _dev(B, W), B.bf16_tensor(X)
