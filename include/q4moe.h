@@ -62,7 +62,8 @@ enum {
   Q4MOE_OP_FFN_DECODE = 4,
   Q4MOE_OP_FFN_PREFILL = 5,
   Q4MOE_OP_LMHEAD = 6,
-  Q4MOE_OP_FFN_DECODE_BATCH = 7
+  Q4MOE_OP_FFN_DECODE_BATCH = 7,
+  Q4MOE_OP_ROUTE_RULE = 8
 };
 
 /* An affine matrix of 4-bit codes (the default), or of 8-bit codes (the
@@ -247,8 +248,11 @@ int moe_route_topk_q8(const q4moe_matrix* router_q8, const q4moe_bf16* X, int64_
  * moe_route_topk with a routing rule (see q4moe_routing): logits of the rows
  * X bf16 [T][hidden] through rule->router or rule->router_q8 in fp32, as
  * moe_route_topk and moe_route_topk_q8 compute them, then the rule.  Writes ids
- * int32 [T][top_k] and weights fp32 [T][top_k].  Needs Q4MOE_OP_ROUTE workspace
- * (n_experts; T).
+ * int32 [T][top_k] and weights fp32 [T][top_k].  Needs Q4MOE_OP_ROUTE_RULE
+ * workspace (n_experts; T), zero-filled before its first use and used by moe_route
+ * alone: up to four rows run as one launch whose last workgroup selects, by an
+ * arrival count that each call leaves at zero again.  Calls that share a workspace
+ * must not overlap.
  */
 int moe_route(const q4moe_routing* rule, const q4moe_bf16* X, int64_t T, int32_t* ids, float* weights,
               void* workspace, size_t workspace_bytes, q4moe_stream stream);
@@ -431,7 +435,7 @@ int q4moe_pack_group_major(const q4moe_matrix* W, uint32_t* dst, q4moe_stream st
 
 /*
  * Workspace bytes for an operation.  `layer` is read for the FFN and ROUTE
- * ops (ROUTE uses layer->n_experts), `W` for GEMM and LMHEAD; `rows` is T, m
+ * ops (ROUTE and ROUTE_RULE use layer->n_experts), `W` for GEMM and LMHEAD; `rows` is T, m
  * or B.  Returns 0 when no workspace is needed or the arguments are invalid.
  */
 size_t q4moe_workspace_bytes(int op, const q4moe_layer* layer, const q4moe_matrix* W, int64_t rows);

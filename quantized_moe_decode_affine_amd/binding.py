@@ -19,6 +19,7 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libq4moe.s
 OK, EINVAL, EUNSUPPORTED, EWORKSPACE, EHIP = 0, 1, 2, 3, 4
 OUT_F32, OUT_BF16, OUT_BF16_RESIDUAL = 0, 1, 2  # residual: bf16(x + y), moe_ffn_decode only
 OP_GEMV, OP_GEMM, OP_ROUTE, OP_PERMUTE, OP_FFN_DECODE, OP_FFN_PREFILL, OP_LMHEAD, OP_FFN_DECODE_BATCH = range(8)
+OP_ROUTE_RULE = 8
 
 EXPORTS = ("q4_gemv", "q4_gemm", "moe_route_topk", "moe_route_topk_q8", "moe_permute", "moe_ffn_decode", "moe_ffn_decode_noalloc",
            "moe_ffn_decode_batch",
@@ -406,15 +407,22 @@ def gpu_routing(layer: DeviceLayer, X: torch.Tensor):
     return moe_route_topk(layer.router, X, layer.top_k)
 
 
+# The current stream's handle of a device by its index: torch's raw form where this torch has it
+# (0.1 us instead of the 1.9 us of a Stream object, next to the 4 us of a launch).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _call(fn: str, device: torch.device, *args) -> None:
     """Call an entry point on `device` and its current stream."""
     f = getattr(load_library(), fn)
     if device.index == torch.cuda.current_device():
-        status = f(*args, torch.cuda.current_stream(device).cuda_stream)
+        status = f(*args, _raw_stream(device.index))
     else:
         with torch.cuda.device(device):
-            status = f(*args, torch.cuda.current_stream(device).cuda_stream)
-    _check(fn, status)
+            status = f(*args, _raw_stream(device.index))
+    if status != OK:
+        _check(fn, status)
 
 
 def _result(name: str, out: Optional[torch.Tensor], shape, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
@@ -440,10 +448,10 @@ def _out_type(out_dtype: int) -> torch.dtype:
 
 
 def moe_route_workspace(routing: Routing, T: int) -> torch.Tensor:
-    """A workspace for moe_route on up to T rows."""
-    return torch.empty(max(256, load_library().q4moe_workspace_bytes(
-        OP_ROUTE, ctypes.byref(q4moe_layer(routing.hidden, 0, routing.n_experts, routing.top_k)), None, T)),
-        dtype=torch.uint8, device=routing.device)
+    """A workspace for moe_route on up to T rows, zero-filled as its first call needs it."""
+    return workspace(load_library().q4moe_workspace_bytes(
+        OP_ROUTE_RULE, ctypes.byref(q4moe_layer(routing.hidden, 0, routing.n_experts, routing.top_k)), None, T),
+        routing.device)
 
 
 def moe_route(routing: Routing, X: torch.Tensor, ids: Optional[torch.Tensor] = None,

@@ -161,7 +161,7 @@ int i8_experts_check(const q4moe_i8_experts* L, int64_t T, int64_t top_k, q4moe:
     return Q4MOE_EINVAL;
   // sorted positions, the tiles' grid and the offsets of gathered rows are 32-bit
   const int64_t rows = T > kMaxRows32 ? kMaxRows32 : T * (top_k + 1);
-  if (T > kMaxRows32 || rows > kMaxRows32 || T * H > 0xFFFFFFFFll || (rows / 64 + 2 * E + 8) * (std::max(H, I) / 64 + 1) > kMaxRows32)
+  if (T > kMaxRows32 || rows > kMaxRows32 || T * H > 0xFFF00000ll || (rows / 64 + 2 * E + 8) * (std::max(H, I) / 64 + 1) > kMaxRows32)
     return Q4MOE_EUNSUPPORTED;
   auto mat = [](const q4moe_i8_matrix& W) { return q4moe::I8Mat{W.codes, W.scales}; };
   const q4moe::I8Mat none{nullptr, nullptr};
@@ -196,6 +196,9 @@ size_t q4moe_workspace_bytes(int op, const q4moe_layer* layer, const q4moe_matri
     case Q4MOE_OP_ROUTE:
       if (!layer || layer->n_experts < 1) return 0;
       return q4moe::route_workspace_bytes(rows, layer->n_experts);
+    case Q4MOE_OP_ROUTE_RULE:
+      if (!layer || layer->n_experts < 1) return 0;
+      return q4moe::route_rule_workspace_bytes(rows, layer->n_experts);
     case Q4MOE_OP_PERMUTE:
       if (!layer || layer->n_experts < 1 || layer->top_k < 1) return 0;
       return q4moe::permute_workspace_bytes(rows * layer->top_k, layer->n_experts);
@@ -448,7 +451,7 @@ int moe_route(const q4moe_routing* rule, const q4moe_bf16* X, int64_t T, int32_t
       return Q4MOE_EINVAL;
     if (rule->hidden > kMaxGemvK || T > kMaxRows32 || T * r.top_k > kMaxRows32) return Q4MOE_EUNSUPPORTED;
     if (T == 0) return Q4MOE_OK;
-    if (!workspace || workspace_bytes < q4moe::route_workspace_bytes(T, r.n_experts) || !aligned(workspace, 256))
+    if (!workspace || workspace_bytes < q4moe::route_rule_workspace_bytes(T, r.n_experts) || !aligned(workspace, 256))
       return Q4MOE_EWORKSPACE;
     const Q4Mat m = q8 ? to_mat(rule->router_q8) : Q4Mat{nullptr, nullptr, nullptr};
     return hip_status(q4moe::run_route(r, rule->router, &m, rule->hidden, X, T, ids, weights, workspace,

@@ -175,11 +175,14 @@ __device__ __forceinline__ void i8_tile_body(const I8GemmArgs& p) {
   // columns are gate and the rest up, and a lane holds both.
   constexpr int kOpsA = TM / 8 / kWaves, kOpsW = TN / 8 / kWaves;
   constexpr int kOpsG = kSwiglu ? kOpsW / 2 : kOpsW;
+  constexpr int kPairs = FN > 1 ? FN / 2 : 1;  // SwiGLU: a wave's gate blocks, and its up blocks
+  static_assert(!kSwiglu || FN % 2 == 0, "gate and up blocks come in pairs");
   int off[kOps], dst[kOps];
   const int piece = lane & 7;
 #pragma unroll
   for (int j = 0; j < kOps; ++j) {
     int blk, row;  // block of 8 rows in the stage, row of the operand
+    bool inside = true;
     if (j < kOpsA) {
       blk = wave * kOpsA + j;
       const int r = blk * 8 + (lane >> 3);
@@ -188,15 +191,17 @@ __device__ __forceinline__ void i8_tile_body(const I8GemmArgs& p) {
         const int64_t pos = first + min(r, rows - 1);
         row = pos < p.P ? p.row_src[pos] : (int)(pos - p.P);
       }
+      inside = r < rows;
     } else {
       const bool up = j - kOpsA >= kOpsG;
       const int i = wave * kOpsG + (j - kOpsA) % kOpsG;  // block of 8 of this matrix's columns
       row = i * 8 + (lane >> 3);
       const int b = i / 4;  // block of 32 of them
-      blk = TM / 8 + (kSwiglu ? (b / (FN / 2) * FN + b % (FN / 2) + (up ? FN / 2 : 0)) * 4 + i % 4 : i);
+      blk = TM / 8 + (kSwiglu ? (b / kPairs * FN + b % kPairs + (up ? kPairs : 0)) * 4 + i % 4 : i);
     }
     const int r = blk * 8 + (lane >> 3);
-    off[j] = (int)((uint32_t)row * (uint32_t)p.K + (uint32_t)(piece ^ row_swz(r)) * 16);
+    // a row past the tile's last one lies beyond every buffer: it costs no traffic
+    off[j] = inside ? (int)((uint32_t)row * (uint32_t)p.K + (uint32_t)(piece ^ row_swz(r)) * 16) : (int)0xFFFFFFF0u;
     dst[j] = blk * 8 * kStepBytes;
   }
   auto rsrc = [&](const int8_t* base, uint32_t bytes) {
@@ -213,8 +218,9 @@ __device__ __forceinline__ void i8_tile_body(const I8GemmArgs& p) {
   const int steps = (p.K + kStepBytes - 1) / kStepBytes;
   // steps past the last load it again and are not computed
   auto issue_op = [&](int i, int st, int j) __attribute__((always_inline)) {
+    const int k0 = min(i, steps - 1) * kStepBytes;
     const __amdgpu_buffer_rsrc_t r = j < kOpsA ? ra : j < kOpsA + kOpsG ? rw : ru;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, stage(st) + dst[j], 16, off[j], min(i, steps - 1) * kStepBytes, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, stage(st) + dst[j], 16, off[j], k0, 0, 0);
   };
 
   // Operand reads run one MFMA step (32 columns) ahead of the products.  At the end of a K
@@ -246,7 +252,7 @@ __device__ __forceinline__ void i8_tile_body(const I8GemmArgs& p) {
     // One MFMA step, with the loads [j0, j1) of a K step into stage st between its products.
     auto mul = [&](int set, int i, auto st_c, auto j0_c, auto j1_c) __attribute__((always_inline)) {
       constexpr int st = decltype(st_c)::value, j0 = decltype(j0_c)::value, j1 = decltype(j1_c)::value;
-      constexpr int kPer = NF > 0 ? (j1 - j0 + NF - 1) / NF : 0;  // loads after each row of products
+      constexpr int kPer = (j1 - j0 + NF - 1) / (NF > 0 ? NF : 1);  // loads after each row of products
 #pragma unroll
       for (int fm = 0; fm < NF; ++fm) {
 #pragma unroll
@@ -447,11 +453,22 @@ __global__ __launch_bounds__(256) void i8_combine_kernel(const Part* __restrict_
 #pragma unroll
       for (int j = 0; j < 8; ++j) y[j] += v[j] * f * c[j];
     };
-    for (int s = 0; s < k; ++s) {
-      const int e = ids[t * k + s];
-      if (e < 0 || e >= E) continue;
-      const int64_t pos = inv[t * k + s];
-      add(pos, sh[pos] * weights[t * k + s], sw + (int64_t)e * H);
+    for (int s0 = 0; s0 < k; s0 += 4) {  // four slots' loads in flight
+      int e[4];
+      int64_t pos[4];
+      float f[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t r = t * k + min(s0 + j, k - 1);
+        e[j] = ids[r];
+        pos[j] = s0 + j < k && e[j] >= 0 && e[j] < E ? inv[r] : -1;
+        f[j] = weights[r];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] *= sh[pos[j] < 0 ? 0 : pos[j]];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (pos[j] >= 0) add(pos[j], f[j], sw + (int64_t)e[j] * H);
     }
     if (sw_shared) add(P + t, sh[P + t], sw_shared);
     if (out_bf16) {
@@ -591,7 +608,7 @@ hipError_t run_moe_experts_i8(const I8Experts& L, const uint16_t* X, int64_t T, 
   p.S = L.sh_gate;
   p.S2 = L.sh_up;
   p.out = w.act;
-  e = launch_tiles<1, 4, 4, 2, 3, kEpiSwiglu>(p, max_tiles, stream);
+  e = launch_tiles<2, 4, 2, 2, 3, kEpiSwiglu>(p, max_tiles, stream);
   if (e != hipSuccess) return e;
   e = launch_quantize(w.act, R, I, w.aq, w.sh, stream);
   if (e != hipSuccess) return e;
@@ -612,8 +629,8 @@ hipError_t run_moe_experts_i8(const I8Experts& L, const uint16_t* X, int64_t T, 
   float unit = 1.0f;
   while (127.0f * 128.0f * I > 65504.0f * unit) unit *= 2.0f;
   d.mul = 1.0f / unit;
-  e = out_bf16 ? launch_tiles<1, 4, 4, 2, 3, kEpiPartF16>(d, max_tiles, stream)
-               : launch_tiles<1, 4, 4, 2, 3, kEpiPartF32>(d, max_tiles, stream);
+  e = out_bf16 ? launch_tiles<2, 4, 2, 2, 3, kEpiPartF16>(d, max_tiles, stream)
+               : launch_tiles<2, 4, 2, 2, 3, kEpiPartF32>(d, max_tiles, stream);
   if (e != hipSuccess) return e;
 
   const unsigned blocks = (unsigned)std::min<int64_t>((T * (H / 8) + 255) / 256, 65536);

@@ -92,7 +92,9 @@ struct RouteRule {
 };
 hipError_t run_select(const RouteRule& r, const float* logits, int64_t T, int32_t* ids, float* weights,
                       hipStream_t stream);
-// Logits into ws (route_workspace_bytes), then run_select on them.
+// The router's logits, then the selection; ws: an arrival counter that is zero between the
+// calls, then the logits (route_rule_workspace_bytes).
+size_t route_rule_workspace_bytes(int64_t T, int n_experts);
 hipError_t run_route(const RouteRule& r, const uint16_t* router, const Q4Mat* router_q8, int H, const uint16_t* X,
                      int64_t T, int32_t* ids, float* weights, void* ws, hipStream_t stream);
 size_t permute_workspace_bytes(int64_t rows, int n_experts);

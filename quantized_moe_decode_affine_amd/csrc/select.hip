@@ -45,16 +45,14 @@ __device__ __forceinline__ double wave_sum_f64(double v) {
 
 __device__ __forceinline__ double sigmoid64(double l) { return 1.0 / (1.0 + exp(-l)); }
 
-template <int V>
-__global__ __launch_bounds__(kSelWaves * kWave) void select_kernel(RouteRule r, const float* __restrict__ logits,
-                                                                   int64_t T, int32_t* __restrict__ ids,
-                                                                   float* __restrict__ weights) {
-  __shared__ double s_c[kSelWaves][V * kWave];
+__device__ __forceinline__ float load_logit(const float* p, bool fresh) { return fresh ? ld_agent(p) : *p; }
+
+// One token by one wave.  sc: V * 64 doubles of LDS of the wave's own.  kFresh: the logits
+// were written by other workgroups of this launch.
+template <int V, bool kFresh>
+__device__ __forceinline__ void select_row(const RouteRule& r, const float* row, double* sc, int32_t* ids,
+                                           float* weights) {
   const int lane = lane_id();
-  const int wave = threadIdx.x / kWave;
-  const int64_t t = (int64_t)blockIdx.x * kSelWaves + wave;
-  if (t >= T) return;  // no workgroup barrier below: each wave works on its own row of s_c
-  const float* row = logits + t * r.n_experts;
   const bool softmax = r.score == kScoreSoftmax;
   // the order of the choices is that of the logits unless something is added to the scores
   const bool scored = r.bias != nullptr || (r.n_groups > 1 && r.group_terms > 1);
@@ -67,7 +65,7 @@ __global__ __launch_bounds__(kSelWaves * kWave) void select_kernel(RouteRule r, 
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int e = lane * V + j;
-    l[j] = e < r.n_experts ? row[e] : -INFINITY;
+    l[j] = e < r.n_experts ? load_logit(row + e, kFresh) : -INFINITY;
     open[j] = l[j] > -INFINITY;  // false for NaN
     if (open[j]) top = fmaxf(top, l[j]);
   }
@@ -100,7 +98,6 @@ __global__ __launch_bounds__(kSelWaves * kWave) void select_kernel(RouteRule r, 
 
   if (r.n_groups > 1) {
     // 2^shift lanes per group scan its experts, then merge their largest two
-    double* sc = s_c[wave];
 #pragma unroll
     for (int j = 0; j < V; ++j) sc[lane * V + j] = c[j];
     __builtin_amdgcn_wave_barrier();
@@ -174,7 +171,7 @@ __global__ __launch_bounds__(kSelWaves * kWave) void select_kernel(RouteRule r, 
 
   double w = 0.0;
   if (my_id >= 0) {
-    const float v = row[my_id];
+    const float v = load_logit(row + my_id, kFresh);
     w = softmax ? expl(v) : sigmoid64(v);
     if (need_sum) w /= sum;
   }
@@ -183,12 +180,136 @@ __global__ __launch_bounds__(kSelWaves * kWave) void select_kernel(RouteRule r, 
     w = total > 0.0 ? w / total : 0.0;
   }
   if (lane < r.top_k) {
-    ids[t * r.top_k + lane] = my_id;
-    weights[t * r.top_k + lane] = (float)(w * (double)r.scale);
+    ids[lane] = my_id;
+    weights[lane] = (float)(w * (double)r.scale);
   }
 }
 
+template <int V>
+__global__ __launch_bounds__(kSelWaves * kWave) void select_kernel(RouteRule r, const float* __restrict__ logits,
+                                                                   int64_t T, int32_t* __restrict__ ids,
+                                                                   float* __restrict__ weights) {
+  __shared__ double s_c[kSelWaves][V * kWave];
+  const int wave = threadIdx.x / kWave;
+  const int64_t t = (int64_t)blockIdx.x * kSelWaves + wave;
+  if (t >= T) return;  // no workgroup barrier below: each wave works on its own row of s_c
+  select_row<V, false>(r, logits + t * r.n_experts, s_c[wave], ids + t * r.top_k, weights + t * r.top_k);
+}
+
+// Routing of at most kSelWaves tokens in one launch: a wave per expert takes its row of the
+// router once for all tokens, and the last workgroup to finish selects, a wave per token.
+// The launch is bound by latencies (its bytes, 1 MB at 256 experts of 2,048 columns, take
+// 0.2 us): one launch instead of two saves one of each.  `arrived` is zero before the launch
+// and after it.
+template <int V, bool kQ8>
+__global__ __launch_bounds__(kSelWaves * kWave) void route_few_kernel(RouteRule r, const uint16_t* __restrict__ router,
+                                                                      Q4Mat q8, int H, const uint16_t* __restrict__ X,
+                                                                      int T, float* logits, unsigned* arrived,
+                                                                      int32_t* __restrict__ ids,
+                                                                      float* __restrict__ weights) {
+  __shared__ double s_c[kSelWaves][V * kWave];
+  __shared__ bool s_last;
+  const int lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int e = blockIdx.x * kSelWaves + wave;
+  if (e < r.n_experts) {
+    float acc[kSelWaves] = {};
+    if constexpr (kQ8) {
+      // 16 columns a lane and step, a quarter of a group: w = scale * q + bias
+      const uint8_t* codes = reinterpret_cast<const uint8_t*>(q8.codes) + (int64_t)e * H;
+      for (int j = lane * 16; j < H; j += kWave * 16) {
+        const uint4 c = *reinterpret_cast<const uint4*>(codes + j);
+        const float s = bf16_bits_to_f32(q8.scales[(int64_t)e * (H / kGroup) + j / kGroup]);
+        const float b = bf16_bits_to_f32(q8.biases[(int64_t)e * (H / kGroup) + j / kGroup]);
+        const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+        for (int t = 0; t < T; ++t) {
+          float p = 0.f, sum = 0.f;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint4 x = *reinterpret_cast<const uint4*>(X + (int64_t)t * H + j + 8 * h);
+            const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float lo = __uint_as_float(xw[i] << 16), hi = __uint_as_float(xw[i] & 0xFFFF0000u);
+              const uint32_t w = cw[2 * h + i / 2] >> (16 * (i & 1));
+              p = fmaf((float)(w & 0xFFu), lo, p);
+              p = fmaf((float)((w >> 8) & 0xFFu), hi, p);
+              sum += lo + hi;
+            }
+          }
+#pragma unroll
+          for (int o = 0; o < kSelWaves; ++o)
+            if (o == t) acc[o] += fmaf(s, p, b * sum);
+        }
+      }
+    } else {
+      constexpr int kAhead = 4;  // pieces of 8 columns in flight per lane: 2,048 columns
+      for (int j0 = 0; j0 < H; j0 += kAhead * kWave * 8) {
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        uint4 w[kAhead];
+        auto piece = [&](const uint16_t* row, int c) {
+          const int j = j0 + (c * kWave + lane) * 8;
+          return j < H ? *reinterpret_cast<const uint4*>(row + j) : zero;
+        };
+#pragma unroll
+        for (int c = 0; c < kAhead; ++c) w[c] = piece(router + (int64_t)e * H, c);
+#pragma unroll
+        for (int t = 0; t < kSelWaves; ++t) {
+          if (t >= T) break;
+          uint4 x[kAhead];
+#pragma unroll
+          for (int c = 0; c < kAhead; ++c) x[c] = piece(X + (int64_t)t * H, c);
+#pragma unroll
+          for (int c = 0; c < kAhead; ++c) {
+            acc[t] = dot2_bf16(w[c].x, x[c].x, acc[t]);
+            acc[t] = dot2_bf16(w[c].y, x[c].y, acc[t]);
+            acc[t] = dot2_bf16(w[c].z, x[c].z, acc[t]);
+            acc[t] = dot2_bf16(w[c].w, x[c].w, acc[t]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < kSelWaves; ++t) {
+      if (t >= T) break;
+      const float l = group_sum<kWave>(acc[t]);
+      if (lane == 0) st_agent(logits + (int64_t)t * r.n_experts + e, l);
+    }
+  }
+  wait_vmem();  // this wave's logits are where every workgroup sees them
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const unsigned n = __hip_atomic_fetch_add(arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    s_last = n == gridDim.x - 1;
+    if (s_last) __hip_atomic_store(arrived, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  if (!s_last || wave >= T) return;
+  select_row<V, true>(r, logits + (int64_t)wave * r.n_experts, s_c[wave], ids + wave * r.top_k,
+                      weights + wave * r.top_k);
+}
+
+template <int V>
+hipError_t launch_route_few(const RouteRule& r, const uint16_t* router, const Q4Mat* q8, int H, const uint16_t* X,
+                            int T, float* logits, unsigned* arrived, int32_t* ids, float* weights,
+                            hipStream_t stream) {
+  const dim3 grid((unsigned)((r.n_experts + kSelWaves - 1) / kSelWaves)), threads(kSelWaves * kWave);
+  if (q8->codes)
+    hipLaunchKernelGGL((route_few_kernel<V, true>), grid, threads, 0, stream, r, router, *q8, H, X, T, logits, arrived,
+                       ids, weights);
+  else
+    hipLaunchKernelGGL((route_few_kernel<V, false>), grid, threads, 0, stream, r, router, *q8, H, X, T, logits,
+                       arrived, ids, weights);
+  return hipGetLastError();
+}
+
+constexpr size_t kArrivedBytes = 256;  // the arrival counter, before the logits
+
 }  // namespace
+
+size_t route_rule_workspace_bytes(int64_t T, int n_experts) {
+  return kArrivedBytes + route_workspace_bytes(T, n_experts);
+}
 
 hipError_t run_select(const RouteRule& r, const float* logits, int64_t T, int32_t* ids, float* weights,
                       hipStream_t stream) {
@@ -206,7 +327,18 @@ hipError_t run_select(const RouteRule& r, const float* logits, int64_t T, int32_
 
 hipError_t run_route(const RouteRule& r, const uint16_t* router, const Q4Mat* router_q8, int H, const uint16_t* X,
                      int64_t T, int32_t* ids, float* weights, void* ws, hipStream_t stream) {
-  float* logits = static_cast<float*>(ws);
+  unsigned* arrived = static_cast<unsigned*>(ws);
+  float* logits = reinterpret_cast<float*>(static_cast<char*>(ws) + kArrivedBytes);
+  if (T <= kSelWaves) {
+    if (r.n_experts <= kWave)
+      return launch_route_few<1>(r, router, router_q8, H, X, (int)T, logits, arrived, ids, weights, stream);
+    if (r.n_experts <= 4 * kWave)
+      return launch_route_few<4>(r, router, router_q8, H, X, (int)T, logits, arrived, ids, weights, stream);
+    if (r.n_experts <= 8 * kWave)
+      return launch_route_few<8>(r, router, router_q8, H, X, (int)T, logits, arrived, ids, weights, stream);
+    return launch_route_few<kMaxExperts / kWave>(r, router, router_q8, H, X, (int)T, logits, arrived, ids, weights,
+                                                 stream);
+  }
   const hipError_t e = run_router_logits(router, r.n_experts, H, X, T, logits, stream, router_q8);
   return e != hipSuccess ? e : run_select(r, logits, T, ids, weights, stream);
 }

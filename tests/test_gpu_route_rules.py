@@ -103,7 +103,7 @@ def _grid(seed, shape, std, step, most):
     return synth.to_bf16_bits((np.clip(np.round(v), -most, most) * step).astype(np.float32))
 
 
-@pytest.mark.parametrize("T,E,H,k", [(1, 256, 2048, 8), (2, 16, 64, 4), (3, 60, 1088, 6), (15, 256, 128, 8), (16, 512, 320, 10),
+@pytest.mark.parametrize("T,E,H,k", [(1, 256, 2048, 8), (2, 16, 64, 4), (3, 60, 1088, 6), (4, 1000, 576, 9), (4, 257, 4096, 3), (15, 256, 128, 8), (16, 512, 320, 10),
                                      (17, 512, 2048, 10), (33, 1024, 192, 32), (64, 8, 256, 2), (130, 257, 448, 5),
                                      (2048, 256, 2048, 8)])
 def test_route_bf16_router(B, T, E, H, k):
@@ -117,7 +117,7 @@ def test_route_bf16_router(B, T, E, H, k):
     _check(ids[some], w[some], *ref)
 
 
-@pytest.mark.parametrize("T,E,H,k", [(1, 256, 2048, 8), (5, 60, 192, 6), (16, 100, 320, 4), (37, 512, 1088, 10)])
+@pytest.mark.parametrize("T,E,H,k", [(1, 256, 2048, 8), (2, 7, 64, 3), (3, 600, 1088, 8), (4, 60, 192, 6), (5, 60, 192, 6), (16, 100, 320, 4), (37, 512, 1088, 10)])
 def test_route_q8_router(B, T, E, H, k):
     rng = np.random.default_rng(E + T)
     codes = rng.integers(0, 256, (E, H), dtype=np.uint8).view(np.uint32)
@@ -149,6 +149,29 @@ def test_outputs_beyond_the_rows_stay(B):
     assert (ids[[0, 8]] == 77).all() and (w[[0, 8]] == 5.0).all()
 
 
+@pytest.mark.parametrize("E,H,q8", [(256, 2048, False), (60, 192, True), (1024, 64, False)])
+def test_one_workspace_for_many_calls(B, E, H, q8):
+    """A workspace serves calls of few and of many rows in turn, on one stream after the other."""
+    if q8:
+        router = B.DeviceQ4(np.random.default_rng(1).integers(0, 256, (E, H), dtype=np.uint8).view(np.uint32),
+                            synth.to_bf16_bits(np.full((E, H // 64), 2.0 ** -12, np.float32)),
+                            synth.to_bf16_bits(np.full((E, H // 64), -2.0 ** -5, np.float32)))
+    else:
+        router = B.bf16_tensor(_grid(1, (E, H), 0.02, 2.0 ** -10, 255))
+    r = B.Routing(router, 7, score="sigmoid")
+    ws = B.moe_route_workspace(r, 50)
+    side = torch.cuda.Stream()
+    for n, T in enumerate((1, 4, 50, 2, 5, 3, 1, 1)):
+        X = B.bf16_tensor(_grid(n, (T, H), 1.0, 2.0 ** -3, 40))
+        want = B.moe_route(r, X)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side if n % 2 else torch.cuda.current_stream()):
+            got = B.moe_route(r, X, ws=ws)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert not ws[:4].any()
+
+
 def test_empty_batch_and_refusals(B):
     r = B.Routing(B.bf16_tensor(_grid(1, (16, 64), 0.02, 2.0 ** -10, 255)), 4)
     X = torch.zeros(3, 64, dtype=torch.bfloat16, device="cuda")
@@ -170,7 +193,7 @@ def test_empty_batch_and_refusals(B):
     assert e.value.status == B.EWORKSPACE
 
 
-@pytest.mark.parametrize("T", [1, 40])
+@pytest.mark.parametrize("T", [1, 3, 40])
 def test_captured_route_replays(B, T):
     R = B.bf16_tensor(_grid(1, (64, 256), 0.02, 2.0 ** -10, 255))
     r = B.Routing(R, 6, score="sigmoid", bias=torch.linspace(-0.1, 0.1, 64, device="cuda"), n_groups=4, top_groups=2)

@@ -33,7 +33,7 @@ BAD_RULES = [dict(n_experts=0), dict(top_k=0), dict(top_k=33), dict(score=2), di
 
 
 def test_route_rejects(lib):
-    need = lib.q4moe_workspace_bytes(B.OP_ROUTE, ctypes.byref(B.q4moe_layer(128, 0, 64, 4)), None, 10)
+    need = lib.q4moe_workspace_bytes(B.OP_ROUTE_RULE, ctypes.byref(B.q4moe_layer(128, 0, 64, 4)), None, 10)
     f, g = lib.moe_route, lib.moe_route_logits
     for bad in BAD_RULES:
         assert f(_rule(**bad), A, 10, A2, A2, A, need, None) == B.EINVAL, bad
