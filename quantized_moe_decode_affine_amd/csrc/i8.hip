@@ -28,41 +28,13 @@ __device__ __forceinline__ uint16_t i8_bf16(float f) {
 
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 
-// One wave per row.  Up to kHeld chunks of 8 values per lane stay in registers between the
-// largest magnitude and the codes, the rest of a longer row is read again (from the caches).
-// Bound by the row's bytes.
+// One wave per row; bound by the row's bytes.
 template <typename In, int kHeld>
 __global__ __launch_bounds__(256) void i8_quantize_kernel(const In* __restrict__ X, int64_t rows, int K,
                                                           int8_t* __restrict__ codes, float* __restrict__ scales) {
-  const int lane = lane_id();
   const int64_t r = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave;
   if (r >= rows) return;
-  const In* x = X + r * K;
-  int8_t* c = codes + r * K;
-  I8Chunk<In> held[kHeld];
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i) held[i].load(x + min((i * kWave + lane) * 8, K - 8));
-  uint32_t most = 0;
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i) most = held[i].most(most);
-  for (int j = (kHeld * kWave + lane) * 8; j < K; j += kWave * 8) {
-    I8Chunk<In> v;
-    v.load(x + j);
-    most = v.most(most);
-  }
-  const float scale = i8_scale(wave_max_u32(most));
-  const I8Rounder rd(scale);
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i) {
-    const int j = (i * kWave + lane) * 8;
-    if (j < K) *reinterpret_cast<uint2*>(c + j) = held[i].codes(rd);
-  }
-  for (int j = (kHeld * kWave + lane) * 8; j < K; j += kWave * 8) {
-    I8Chunk<In> v;
-    v.load(x + j);
-    *reinterpret_cast<uint2*>(c + j) = v.codes(rd);
-  }
-  if (lane == 0) scales[r] = scale;
+  i8_quantize_row<kHeld>(X + r * K, K, codes + r * K, scales + r);
 }
 
 template <typename In>
@@ -581,8 +553,6 @@ hipError_t run_moe_experts_i8(const I8Experts& L, const uint16_t* X, int64_t T, 
   const ExpertsWs w = carve(ws, L, T, k);
   const int64_t P = T * k, extra = L.sh_gate.codes ? T : 0, R = P + extra;
   const int max_tiles = group_max_tiles(P, E, extra, kExpertRows);
-  hipError_t e = launch_quantize(X, T, H, w.xq, w.sx, stream);
-  if (e != hipSuccess) return e;
   GroupTiles gt{};
   gt.tile_rows = kExpertRows;
   gt.max_tiles = max_tiles;
@@ -591,7 +561,9 @@ hipError_t run_moe_experts_i8(const I8Experts& L, const uint16_t* X, int64_t T, 
   gt.table = w.tiles;
   gt.row_src = w.row_src;
   gt.row_w = w.row_w;
-  e = run_permute(ids, P, E, w.offsets, w.sorted, w.inv, w.perm, &gt, stream);
+  // the tokens' codes are made in the sort's first launch, beside its few workgroups
+  const I8RowsJob job{X, T, H, w.xq, w.sx};
+  hipError_t e = run_permute(ids, P, E, w.offsets, w.sorted, w.inv, w.perm, &gt, stream, nullptr, &job);
   if (e != hipSuccess) return e;
 
   I8GemmArgs p{};

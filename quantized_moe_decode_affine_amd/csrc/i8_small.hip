@@ -33,12 +33,11 @@ __device__ __forceinline__ int image_at(int col, int r, int m) { return ((col >>
 // number `part` (parts = 1: meet does nothing): they meet once, to share their maxima.
 // between() runs when the row's loads are on their way: what it loads arrives behind them
 // and meanwhile the codes are made.
-template <typename In, typename Between, typename Meet>
+template <int kHeld, typename In, typename Between, typename Meet>
 __device__ __forceinline__ float quantize_row(const In* x, int K, int Kpad, uint8_t* image, int r, int m, int part,
                                               int parts, Between between, Meet meet) {
   const int lane = lane_id();
-  // chunks of 8 values per lane that stay in registers between the two passes
-  constexpr int kHeld = sizeof(In) == 2 ? 4 : 2;
+  // kHeld chunks of 8 values per lane stay in registers between the two passes, others are read again
   const int j0 = (part * kWave + lane) * 8, step = parts * kWave * 8;
   I8Chunk<In> held[kHeld];
 #pragma unroll
@@ -74,7 +73,7 @@ __device__ __forceinline__ float quantize_row(const In* x, int K, int Kpad, uint
 
 // A workgroup's m rows into the image: one wave a row, or for fewer than four rows two or
 // four waves a row.  row(r) is row r's address; every wave passes the same barriers.
-template <typename Row, typename Between>
+template <int kHeld, typename Row, typename Between>
 __device__ __forceinline__ void quantize_rows(Row row, int m, int K, int Kpad, uint8_t* image, float* s_scale,
                                               uint32_t* s_most, Between between) {
   const int lane = lane_id();
@@ -93,8 +92,8 @@ __device__ __forceinline__ void quantize_rows(Row row, int m, int K, int Kpad, u
       return most;
     };
     float scale;
-    if (r0 == 0) scale = quantize_row(row(r), K, Kpad, image, r, m, part, parts, between, meet);
-    else scale = quantize_row(row(r), K, Kpad, image, r, m, part, parts, [] {}, meet);
+    if (r0 == 0) scale = quantize_row<kHeld>(row(r), K, Kpad, image, r, m, part, parts, between, meet);
+    else scale = quantize_row<kHeld>(row(r), K, Kpad, image, r, m, part, parts, [] {}, meet);
     if (lane == 0) s_scale[r] = scale;
     if (parts > 1 && r0 + at_once < m) lds_sync();  // s_most is read before the next rows' maxima
   }
@@ -147,7 +146,7 @@ __global__ __launch_bounds__(kSmallWaves* kWave) void i8_few_rows_kernel(I8Mat W
 
   // the first weights are on their way while the rows are quantized
   i32x4_t w[kBatch];
-  quantize_rows([&](int r) { return X + (int64_t)r * K; }, m, K, Kpad, s_image, s_scale, s_most, [&] {
+  quantize_rows<4>([&](int r) { return X + (int64_t)r * K; }, m, K, Kpad, s_image, s_scale, s_most, [&] {
     if (first < blocks && b0 < batches) load_batch(row_of(first), b0 * kBatchCols, K, w);
   });
 
@@ -221,7 +220,7 @@ namespace {
 // Gate/up: a workgroup per (slot, 8 intermediate columns): the 16 rows of its operand are 8
 // rows of gate and the same 8 of up, its four waves share the columns.  The first slot of an
 // expert takes all slots of that expert (up to 16 at a time), the others leave.
-constexpr int kMaxSlots = 256;  // one per thread of a workgroup
+constexpr int kMaxSlots = 64;
 constexpr int kUpCols = 8;
 
 __global__ __launch_bounds__(kSmallWaves* kWave) void i8_slots_up_kernel(I8Experts L, const uint16_t* __restrict__ X,
@@ -231,7 +230,7 @@ __global__ __launch_bounds__(kSmallWaves* kWave) void i8_slots_up_kernel(I8Exper
   __shared__ float s_scale[16];
   __shared__ uint32_t s_most[kSmallWaves];
   __shared__ i32x4acc_t s_sum[kSmallWaves][kWave];
-  __shared__ int s_slot[kMaxSlots];
+  __shared__ int s_slot[kMaxSlots];  // i8_few_slots: no more, nor more than 16 tokens
   __shared__ int s_count[kSmallWaves];
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -239,23 +238,27 @@ __global__ __launch_bounds__(kSmallWaves* kWave) void i8_slots_up_kernel(I8Exper
   const int slot0 = blockIdx.y;
   const int n0 = blockIdx.x * kUpCols;
   const bool sh = slot0 >= P;  // the shared expert's workgroups take every token
-  const int mine = threadIdx.x;
-  const int my_e = !sh && mine < P ? ids[mine] : -1;
   const int e = sh ? 0 : ids[slot0];
   if (e < 0 || e >= L.n_experts) return;
-  const bool same = sh ? mine < T : my_e == e;
-  const uint64_t ball = __ballot(same);
-  if (lane == 0) s_count[wave] = __popcll(ball);
-  lds_sync();
-  int base = 0, count = 0;
+  int count = 1;
+  if (T > 1) {  // one token's slots are each their own
+    const int mine = threadIdx.x;
+    const bool same = sh ? mine < T : mine < P && ids[mine] == e;
+    const uint64_t ball = __ballot(same);
+    if (lane == 0) s_count[wave] = __popcll(ball);
+    lds_sync();
+    int base = 0;
+    count = 0;
 #pragma unroll
-  for (int o = 0; o < kSmallWaves; ++o) {
-    base += o < wave ? s_count[o] : 0;
-    count += s_count[o];
+    for (int o = 0; o < kSmallWaves; ++o) {
+      base += o < wave ? s_count[o] : 0;
+      count += s_count[o];
+    }
+    if (same) s_slot[base + __popcll(ball & ((1ull << lane) - 1ull))] = sh ? P + mine : mine;
+    lds_sync();
+    if (s_slot[0] != slot0) return;  // uniform: an earlier slot has the same expert
   }
-  if (same) s_slot[base + __popcll(ball & ((1ull << lane) - 1ull))] = sh ? P + mine : mine;
-  lds_sync();
-  if (s_slot[0] != slot0) return;  // uniform: an earlier slot has the same expert
+  auto slot_of = [&](int i) { return T > 1 ? s_slot[i] : slot0; };
 
   const int Kpad = (H + kBatchCols - 1) / kBatchCols * kBatchCols;
   const int batches = Kpad / kBatchCols;
@@ -270,9 +273,9 @@ __global__ __launch_bounds__(kSmallWaves* kWave) void i8_slots_up_kernel(I8Exper
     const int m = min(16, count - s0);
     if (s0 > 0) __syncthreads();  // the image and the sums are read no more
     i32x4_t w[kBatch];
-    quantize_rows(
+    quantize_rows<1>(  // a lone row, the usual case, is one chunk a wave up to 2,048 columns
         [&](int r) {
-          const int s = s_slot[s0 + r];
+          const int s = slot_of(s0 + r);
           return X + (int64_t)(s >= P ? s - P : s / k) * H;
         },
         m, H, Kpad, s_image, s_scale, s_most, [&] {
@@ -299,7 +302,7 @@ __global__ __launch_bounds__(kSmallWaves* kWave) void i8_slots_up_kernel(I8Exper
       }
       const float sx = s_scale[tok];
       const float gv = (float)g * sx * sg, uv = (float)u * sx * su;
-      act[(int64_t)s_slot[s0 + tok] * I + n0 + col] = gv / (1.0f + expf(-gv)) * uv;
+      act[(int64_t)slot_of(s0 + tok) * I + n0 + col] = gv / (1.0f + expf(-gv)) * uv;
     }
   }
 }
@@ -330,7 +333,7 @@ __global__ void i8_slots_down_kernel(I8Experts L, int T, int k, const int32_t* _
       const int64_t slot = sh ? P + t : t * k + s;
       i32x4_t w[kBatch];
       float sw[4], f = 1.0f;
-      const float scale = quantize_row(
+      const float scale = quantize_row<1>(
           act + slot * I, I, Kpad, image, 0, 1, 0, 1,
           [&] {
             load_batch(row, 0, I, w);
@@ -369,8 +372,11 @@ int down_waves(int I, int slots) {
 
 }  // namespace
 
+// Up to 64 slots: one token 13 us against the grouped form's 39, 64 slots over 256 experts
+// 54 against 69 and over 16 experts 41 against 40; at 128 slots the two are level (97 and 99
+// us over 256 experts) and more tokens share an expert's rows in the grouped form.
 bool i8_few_slots(const I8Experts& L, int64_t T, int k) {
-  return T * k <= 128 && T <= 16 && image_bytes(T * k < 16 ? T * k : 16, L.hidden) <= kSmallLds;
+  return T * k <= 64 && T <= 16 && image_bytes(T * k < 16 ? T * k : 16, L.hidden) <= kSmallLds;
 }
 
 size_t i8_few_slots_bytes(const I8Experts& L, int64_t T, int k) {

@@ -68,4 +68,36 @@ struct I8Chunk {
   }
 };
 
+// A row of K values to its codes and scale, by one wave.  Up to kHeld chunks of 8 values per
+// lane stay in registers between the largest magnitude and the codes, the rest of a longer
+// row is read again (from the caches).
+template <int kHeld, typename In>
+__device__ __forceinline__ void i8_quantize_row(const In* x, int K, int8_t* codes, float* scale_out) {
+  const int lane = lane_id();
+  I8Chunk<In> held[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) held[i].load(x + min((i * kWave + lane) * 8, K - 8));
+  uint32_t most = 0;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) most = held[i].most(most);
+  for (int j = (kHeld * kWave + lane) * 8; j < K; j += kWave * 8) {
+    I8Chunk<In> v;
+    v.load(x + j);
+    most = v.most(most);
+  }
+  const float scale = i8_scale(wave_max_u32(most));
+  const I8Rounder rd(scale);
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int j = (i * kWave + lane) * 8;
+    if (j < K) *reinterpret_cast<uint2*>(codes + j) = held[i].codes(rd);
+  }
+  for (int j = (kHeld * kWave + lane) * 8; j < K; j += kWave * 8) {
+    I8Chunk<In> v;
+    v.load(x + j);
+    *reinterpret_cast<uint2*>(codes + j) = v.codes(rd);
+  }
+  if (lane == 0) *scale_out = scale;
+}
+
 }  // namespace q4moe

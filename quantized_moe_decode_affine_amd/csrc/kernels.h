@@ -125,11 +125,20 @@ struct PrepRowsJob {
   int32_t* exps;      // [rows]
 };
 
-// Stable counting sort of `rows` ids by expert (tiles may be null); prep (optional)
-// prepares rows beside the rank step, in the same launch.
+// Symmetric 8-bit form of bf16 rows (int8.h), run the same way.
+struct I8RowsJob {
+  const uint16_t* X;  // bf16 [rows][K]
+  int64_t rows;
+  int K;
+  int8_t* codes;      // [rows][K]
+  float* scales;      // [rows]
+};
+
+// Stable counting sort of `rows` ids by expert (tiles may be null); prep or i8 (optional,
+// one of them) prepares rows beside the rank step, in the same launch.
 hipError_t run_permute(const int32_t* ids, int64_t rows, int n_experts, int32_t* offsets, int32_t* sorted_rows,
                        int32_t* inv_rows, void* ws, const GroupTiles* tiles, hipStream_t stream,
-                       const PrepRowsJob* prep = nullptr);
+                       const PrepRowsJob* prep = nullptr, const I8RowsJob* i8 = nullptr);
 
 // ---- grouped MFMA GEMM and the prefill layer (gemm.hip)
 size_t gemm_workspace_bytes(int64_t m, int k);

@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "int8.h"
 #include "kernels.h"
 #include "preprows.h"
 #include "topk.h"
@@ -175,17 +176,24 @@ __global__ __launch_bounds__(256) void topk_rows_kernel(const float* __restrict_
 constexpr int kRankThreads = 256;
 constexpr int kRankChunk = kMaxExperts;  // rows per chunk: one per thread of the scatter kernel
 
-// Workgroups from nchunks on prepare rows (PrepRowsJob) instead: work of their own that
-// only shares the launch, so that it runs beside the few rank workgroups.
+__device__ __forceinline__ void run_rows_job(const PrepRowsJob& job, int64_t block, int64_t blocks) {
+  prep::prep_rows_body<uint16_t>(job.A, job.rows, job.K, job.Gp, job.out, job.sums, job.exps,
+                                 prep::SplitRows{nullptr, INT64_MAX, 0, 1}, block, blocks);
+}
+__device__ __forceinline__ void run_rows_job(const I8RowsJob& job, int64_t block, int64_t blocks) {
+  for (int64_t r = block * 4 + threadIdx.x / kWave; r < job.rows; r += blocks * 4)
+    i8_quantize_row<4>(job.X + r * job.K, job.K, job.codes + r * job.K, job.scales + r);
+}
+
+// Workgroups from nchunks on prepare rows (a job) instead: work of their own that only
+// shares the launch, so that it runs beside the few rank workgroups.
+template <typename Job>
 __global__ __launch_bounds__(kRankThreads) void chunk_rank_kernel(const int32_t* __restrict__ ids, int64_t rows, int E,
                                                                   int32_t* __restrict__ local_rank,
-                                                                  int32_t* __restrict__ hist, int nchunks,
-                                                                  PrepRowsJob prep) {
+                                                                  int32_t* __restrict__ hist, int nchunks, Job job) {
   __shared__ int32_t s_cnt[kMaxExperts];
   if ((int)blockIdx.x >= nchunks) {
-    prep::prep_rows_body<uint16_t>(prep.A, prep.rows, prep.K, prep.Gp, prep.out, prep.sums, prep.exps,
-                                   prep::SplitRows{nullptr, INT64_MAX, 0, 1}, (int64_t)blockIdx.x - nchunks,
-                                   (int64_t)gridDim.x - nchunks);
+    run_rows_job(job, (int64_t)blockIdx.x - nchunks, (int64_t)gridDim.x - nchunks);
     return;
   }
   for (int e = threadIdx.x; e < E; e += kRankThreads) s_cnt[e] = 0;
@@ -524,29 +532,35 @@ int group_max_tiles(int64_t rows, int n_experts, int64_t extra_rows, int tile_ro
 
 hipError_t run_permute(const int32_t* ids, int64_t rows, int E, int32_t* offsets, int32_t* sorted_rows,
                        int32_t* inv_rows, void* ws, const GroupTiles* tiles, hipStream_t stream,
-                       const PrepRowsJob* prep) {
+                       const PrepRowsJob* prep, const I8RowsJob* i8) {
   char* w = static_cast<char*>(ws);
   const int nchunks = (int)((rows + kRankChunk - 1) / kRankChunk);
   int32_t* local_rank = reinterpret_cast<int32_t*>(w);
   int32_t* hist = reinterpret_cast<int32_t*>(w + align256((size_t)rows * 4));
   GroupTiles none{};
   // the row preparation's workgroups (one wave per row) after the rank workgroups
-  const PrepRowsJob pj = prep ? *prep : PrepRowsJob{};
-  const int64_t prep_blocks = prep && prep->rows > 0 ? std::min<int64_t>((prep->rows + 3) / 4, 8192) : 0;
+  const int64_t prep_rows = i8 ? i8->rows : prep ? prep->rows : 0;
+  const int64_t prep_blocks = prep_rows > 0 ? std::min<int64_t>((prep_rows + 3) / 4, 8192) : 0;
+  auto rank = [&]() {
+    const dim3 grid((unsigned)(nchunks + prep_blocks));
+    if (i8)
+      hipLaunchKernelGGL(chunk_rank_kernel<I8RowsJob>, grid, dim3(kRankThreads), 0, stream, ids, rows, E, local_rank,
+                         hist, nchunks, *i8);
+    else
+      hipLaunchKernelGGL(chunk_rank_kernel<PrepRowsJob>, grid, dim3(kRankThreads), 0, stream, ids, rows, E, local_rank,
+                         hist, nchunks, prep ? *prep : PrepRowsJob{});
+    return hipGetLastError();
+  };
   if (nchunks == 0) {  // no rows: offsets and the tile table still get written
     if (prep_blocks > 0) {
-      hipLaunchKernelGGL(chunk_rank_kernel, dim3((unsigned)prep_blocks), dim3(kRankThreads), 0, stream, ids, rows, E,
-                         local_rank, hist, 0, pj);
-      const hipError_t e = hipGetLastError();
+      const hipError_t e = rank();
       if (e != hipSuccess) return e;
     }
     hipLaunchKernelGGL(expert_scatter_kernel, dim3(1), dim3(kMaxExperts), 0, stream, ids, rows, E, local_rank, hist,
                        0, offsets, sorted_rows, inv_rows, tiles ? *tiles : none);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL(chunk_rank_kernel, dim3((unsigned)(nchunks + prep_blocks)), dim3(kRankThreads), 0, stream, ids,
-                     rows, E, local_rank, hist, nchunks, pj);
-  hipError_t e = hipGetLastError();
+  const hipError_t e = rank();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(expert_scatter_kernel, dim3(nchunks), dim3(kMaxExperts), 0, stream, ids, rows, E, local_rank,
                      hist, nchunks, offsets, sorted_rows, inv_rows, tiles ? *tiles : none);

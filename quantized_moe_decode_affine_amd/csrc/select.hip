@@ -26,21 +26,36 @@ __device__ __forceinline__ uint64_t double_key(double d) {
   return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
 }
 
-// Largest key of the wave, and the lowest lane that holds it: the maximum of the high
-// words, then of the low words of the lanes that have it (12 DPP/permlane maxima instead
-// of 6 64-bit compare-and-select steps of five instructions).
+// Largest key of the wave, and the lowest lane that holds it: the maximum of the high words,
+// and only where several lanes have it (equal or nearly equal choices) that of their low words.
 __device__ __forceinline__ uint64_t wave_max_u64(uint64_t key, int* src) {
   const uint32_t hi = (uint32_t)(key >> 32), lo = (uint32_t)key;
   const uint32_t mh = wave_max_u32(hi);
-  const uint32_t ml = wave_max_u32(hi == mh ? lo : 0u);
-  *src = __builtin_ctzll(__ballot(hi == mh && lo == ml));
-  return ((uint64_t)mh << 32) | ml;
+  uint64_t at = __ballot(hi == mh);
+  if (at & (at - 1)) {
+    const uint32_t ml = wave_max_u32(hi == mh ? lo : 0u);
+    at = __ballot(hi == mh && lo == ml);
+  }
+  *src = __builtin_ctzll(at);
+  return ((uint64_t)mh << 32) | (uint32_t)__builtin_amdgcn_readlane((int)lo, *src);
 }
 
+// Sum over the wave, by the steps of group_sum_rt on both words.
 __device__ __forceinline__ double wave_sum_f64(double v) {
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) v += __shfl_xor(v, d, kWave);
-  return v;
+  auto both = [](double x, auto step) {
+    const uint64_t u = (uint64_t)__double_as_longlong(x);
+    uint32_t a[2], b[2];
+    step((uint32_t)u, a[0], b[0]);
+    step((uint32_t)(u >> 32), a[1], b[1]);
+    return __longlong_as_double((long long)(((uint64_t)a[1] << 32) | a[0])) +
+           __longlong_as_double((long long)(((uint64_t)b[1] << 32) | b[0]));
+  };
+  v = both(v, [](uint32_t x, uint32_t& a, uint32_t& b) { a = x; b = dpp_u32<kDppQuadXor1>(x); });
+  v = both(v, [](uint32_t x, uint32_t& a, uint32_t& b) { a = x; b = dpp_u32<kDppQuadXor2>(x); });
+  v = both(v, [](uint32_t x, uint32_t& a, uint32_t& b) { a = x; b = dpp_u32<kDppRowHalfMirror>(x); });
+  v = both(v, [](uint32_t x, uint32_t& a, uint32_t& b) { a = x; b = dpp_u32<kDppRowMirror>(x); });
+  v = both(v, [](uint32_t x, uint32_t& a, uint32_t& b) { swap_rows16(x, a, b); });
+  return both(v, [](uint32_t x, uint32_t& a, uint32_t& b) { swap_halves32(x, a, b); });
 }
 
 __device__ __forceinline__ double sigmoid64(double l) { return 1.0 / (1.0 + exp(-l)); }
@@ -106,10 +121,19 @@ __device__ __forceinline__ void select_row(const RouteRule& r, const float* row,
     const int g = lane >> shift, sub = lane & ((1 << shift) - 1);
     double t1 = -INFINITY, t2 = -INFINITY;
     if (g < r.n_groups)
-      for (int j = sub; j < per; j += 1 << shift) {
-        const double v = sc[g * per + j];
-        t2 = fmax(t2, fmin(t1, v));
-        t1 = fmax(t1, v);
+      for (int j0 = sub; j0 < per; j0 += 4 << shift) {  // four reads at a time
+        double v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = j0 + (i << shift);
+          v[i] = sc[g * per + min(j, per - 1)];
+          if (j >= per) v[i] = -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          t2 = fmax(t2, fmin(t1, v[i]));
+          t1 = fmax(t1, v[i]);
+        }
       }
     for (int d = 1; d < (1 << shift); d <<= 1) {
       const double o1 = __shfl_xor(t1, d, kWave), o2 = __shfl_xor(t2, d, kWave);
