@@ -344,11 +344,13 @@ constexpr int kQ8RouterOps = 6;  // per wave and step: 2 token-row and 2 code-ro
 
 __device__ __forceinline__ int code_swz(int r) { return (r >> 2) & 3; }
 
-__global__ __launch_bounds__(512) void q8_router_logits_kernel(Q4Mat R, const uint16_t* __restrict__ X, int64_t T,
-                                                               int E, int H, float* __restrict__ logits) {
+template <int kStages>
+__device__ __forceinline__ void q8_router_logits_body(Q4Mat R, const uint16_t* __restrict__ X, int64_t T, int E, int H,
+                                                      float* __restrict__ logits) {
+  static_assert(kStages == 2 || kStages == 3, "stages");
   __shared__ __align__(16) uint8_t s_st0[4 * kQ8RouterQuarterBytes], s_st1[4 * kQ8RouterQuarterBytes],
-      s_st2[4 * kQ8RouterQuarterBytes];
-  __shared__ __align__(16) uint8_t s_cd0[4 * 64 * 64], s_cd1[4 * 64 * 64], s_cd2[4 * 64 * 64];
+      s_st2[kStages > 2 ? 4 * kQ8RouterQuarterBytes : 16];
+  __shared__ __align__(16) uint8_t s_cd0[4 * 64 * 64], s_cd1[4 * 64 * 64], s_cd2[kStages > 2 ? 4 * 64 * 64 : 16];
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int eh = wave & 1, kq = wave >> 1;
@@ -379,7 +381,7 @@ __global__ __launch_bounds__(512) void q8_router_logits_kernel(Q4Mat R, const ui
   const uint16_t* bi = R.biases + (int64_t)erow * G;
   auto stage = [&](int st) -> uint8_t* { return st == 0 ? s_st0 : st == 1 ? s_st1 : s_st2; };
   auto cstage = [&](int st) -> uint8_t* { return st == 0 ? s_cd0 : st == 1 ? s_cd1 : s_cd2; };
-  uint32_t scv[kRouterStages], biv[kRouterStages];  // raw bf16 scale and bias of the group in each stage
+  uint32_t scv[kStages], biv[kStages];  // raw bf16 scale and bias of the group in each stage
   // ga: the step's load addresses, returned so that the caller can keep them live past
   // its LDS reads (the compiler waits for every load in flight before it reuses a load's
   // address registers, e.g. as an LDS read's destination)
@@ -405,11 +407,11 @@ __global__ __launch_bounds__(512) void q8_router_logits_kernel(Q4Mat R, const ui
     constexpr int st = decltype(st_c)::value;
     constexpr bool kGuard = decltype(guard_c)::value;
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(kQ8RouterOps * (kRouterStages - 2)));
+    __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(kQ8RouterOps * (kStages - 2)));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     uintptr_t ga[6];
-    issue(i + kRouterStages - 1, (st + kRouterStages - 1) % kRouterStages, ga);
+    issue(i + kStages - 1, (st + kStages - 1) % kStages, ga);
     __builtin_amdgcn_sched_barrier(0);
     const uint8_t* xb = stage(st) + kq * kQ8RouterQuarterBytes;
     const uint8_t* cbp = cstage(st) + kq * 64 * 64;
@@ -444,20 +446,20 @@ __global__ __launch_bounds__(512) void q8_router_logits_kernel(Q4Mat R, const ui
   auto run = [&](auto guard_c) __attribute__((always_inline)) {
     using S0 = std::integral_constant<int, 0>;
     using S1 = std::integral_constant<int, 1>;
-    using S2 = std::integral_constant<int, 2>;
+    using S2 = std::integral_constant<int, kStages - 1>;
     int i = 0;
-    for (; i + kRouterStages <= per_q; i += kRouterStages) {
+    for (; i + kStages <= per_q; i += kStages) {
       step(i, S0{}, guard_c);
       step(i + 1, S1{}, guard_c);
-      step(i + 2, S2{}, guard_c);
+      if constexpr (kStages > 2) step(i + 2, S2{}, guard_c);
     }
     if (i < per_q) step(i, S0{}, guard_c);
-    if (i + 1 < per_q) step(i + 1, S1{}, guard_c);
+    if (kStages > 2 && i + 1 < per_q) step(i + 1, S1{}, guard_c);
   };
   {
     uintptr_t ga[6];
     issue(0, 0, ga);
-    issue(1, 1, ga);
+    if constexpr (kStages > 2) issue(1, 1, ga);
   }
   if (4 * per_q == G)
     run(std::false_type{});
@@ -490,6 +492,21 @@ __global__ __launch_bounds__(512) void q8_router_logits_kernel(Q4Mat R, const ui
   }
 }
 
+// Three stages, one workgroup on a compute unit: for a grid of one round, where each step's
+// loads have the longest to land.  Two stages, two workgroups on one (64 KB of LDS and at
+// most 128 registers each): for more, where one's start and end run under the other's steps.
+// 2,048 rows on 256 experts (256 workgroups) take 17 us with three; 4,093 on 512 (1,024) 50
+// with three and 38 with two.
+__global__ __launch_bounds__(512) void q8_router_logits_kernel(Q4Mat R, const uint16_t* __restrict__ X, int64_t T,
+                                                               int E, int H, float* __restrict__ logits) {
+  q8_router_logits_body<3>(R, X, T, E, H, logits);
+}
+__global__ __launch_bounds__(512, 4) void q8_router_logits_rounds_kernel(Q4Mat R, const uint16_t* __restrict__ X,
+                                                                         int64_t T, int E, int H,
+                                                                         float* __restrict__ logits) {
+  q8_router_logits_body<2>(R, X, T, E, H, logits);
+}
+
 }  // namespace
 
 size_t route_workspace_bytes(int64_t T, int n_experts) { return align256((size_t)T * n_experts * 4); }
@@ -497,7 +514,10 @@ size_t route_workspace_bytes(int64_t T, int n_experts) { return align256((size_t
 hipError_t run_router_logits(const uint16_t* router, int E, int H, const uint16_t* X, int64_t T, float* logits,
                              hipStream_t stream, const Q4Mat* router_q8) {
   dim3 grid((unsigned)((T + 31) / 32), (unsigned)((E + 63) / 64));
-  if (router_q8 && router_q8->codes)
+  const bool rounds = (int64_t)grid.x * grid.y > device_cu_count();
+  if (router_q8 && router_q8->codes && rounds)
+    hipLaunchKernelGGL(q8_router_logits_rounds_kernel, grid, dim3(512), 0, stream, *router_q8, X, T, E, H, logits);
+  else if (router_q8 && router_q8->codes)
     hipLaunchKernelGGL(q8_router_logits_kernel, grid, dim3(512), 0, stream, *router_q8, X, T,
                        E, H, logits);
   else

@@ -117,7 +117,8 @@ def test_route_bf16_router(B, T, E, H, k):
     _check(ids[some], w[some], *ref)
 
 
-@pytest.mark.parametrize("T,E,H,k", [(1, 256, 2048, 8), (2, 7, 64, 3), (3, 600, 1088, 8), (4, 60, 192, 6), (5, 60, 192, 6), (16, 100, 320, 4), (37, 512, 1088, 10)])
+@pytest.mark.parametrize("T,E,H,k", [(1, 256, 2048, 8), (2, 7, 64, 3), (3, 600, 1088, 8), (4, 60, 192, 6), (5, 60, 192, 6), (16, 100, 320, 4), (37, 512, 1088, 10),
+                                     (1111, 509, 448, 7), (2100, 256, 128, 3)])
 def test_route_q8_router(B, T, E, H, k):
     rng = np.random.default_rng(E + T)
     codes = rng.integers(0, 256, (E, H), dtype=np.uint8).view(np.uint32)
