@@ -248,7 +248,7 @@ int moe_route_topk_q8(const q4moe_matrix* router_q8, const q4moe_bf16* X, int64_
  * moe_route_topk with a routing rule (see q4moe_routing): logits of the rows
  * X bf16 [T][hidden] through rule->router or rule->router_q8 in fp32, as
  * moe_route_topk and moe_route_topk_q8 compute them, then the rule.  Writes ids
- * int32 [T][top_k] and weights fp32 [T][top_k].  Needs Q4MOE_OP_ROUTE_RULE
+ * int32 [T][top_k] and weights fp32 [T][top_k]; T up to 2^26.  Needs Q4MOE_OP_ROUTE_RULE
  * workspace (n_experts; T), zero-filled before its first use and used by moe_route
  * alone: up to four rows run as one launch whose last workgroup selects, by an
  * arrival count that each call leaves at zero again.  Calls that share a workspace
@@ -400,7 +400,7 @@ size_t i8_gemm_workspace_bytes(const q4moe_i8_matrix* W, int64_t m);
  * in slot order, the shared expert last.  With a bf16 Y the integer sums of the down
  * product may be rounded to 11 significant bits before that (fp16, scaled by a power
  * of two): by 2^-11 of each summand at most, next to the output's own 2^-8.
- * Results do not depend on which tokens share a call, except for those roundings.
+ * Other tokens of the call move a token's result by such roundings alone.
  * X bf16 [T][hidden], Y fp32 or bf16 [T][hidden], not overlapping X, ids or weights;
  * hidden and inter multiples of 64 up to 16384, n_experts up to 1024, top_k up to 32
  * (not bounded by n_experts).  Needs a workspace of moe_experts_i8_workspace_bytes.

@@ -129,6 +129,7 @@ int rule_check(const q4moe_routing* R, q4moe::RouteRule* r) {
   return Q4MOE_OK;
 }
 
+constexpr int64_t kMaxTiles = 1 << 22;  // workgroups of 512 threads in a grid
 constexpr int64_t kMaxI8K = 65536;      // 127 * 128 * k stays below 2^31
 constexpr int64_t kMaxExpertK = 16384;  // hidden and intermediate sizes of the 8-bit experts
 
@@ -143,9 +144,9 @@ bool i8_shape(const q4moe_i8_matrix& W, int64_t count, int64_t n, int64_t k) {
 
 int i8_gemm_check(const q4moe_i8_matrix* W, int64_t m) {
   if (!i8_matrix_ok(W) || m < 0) return Q4MOE_EINVAL;
-  // rows and channels are 32-bit in the kernels, and so is the grid of 64 x 64 tiles
+  // rows and channels are 32-bit in the kernels; a grid of 256 x 256 tiles holds 2^22 of them
   if (W->k > kMaxI8K || W->count > kMaxRows32 || W->n > kMaxRows32 || W->count * W->n > kMaxRows32 ||
-      m > kMaxRows32 || (m / 64 + 9) * (W->count * W->n / 64 + 1) > kMaxRows32)
+      m > kMaxRows32 || (m / 256 + 1) * (W->count * W->n / 256 + 1) > kMaxTiles)
     return Q4MOE_EUNSUPPORTED;
   return Q4MOE_OK;
 }
@@ -449,7 +450,8 @@ int moe_route(const q4moe_routing* rule, const q4moe_bf16* X, int64_t T, int32_t
       return Q4MOE_EINVAL;
     if (!X || !aligned(X, 16) || !ids || !aligned(ids, 4) || !weights || !aligned(weights, 4) || T < 0)
       return Q4MOE_EINVAL;
-    if (rule->hidden > kMaxGemvK || T > kMaxRows32 || T * r.top_k > kMaxRows32) return Q4MOE_EUNSUPPORTED;
+    // (2^26 rows: the grid of the logits)
+    if (rule->hidden > kMaxGemvK || T > (1 << 26) || T * r.top_k > kMaxRows32) return Q4MOE_EUNSUPPORTED;
     if (T == 0) return Q4MOE_OK;
     if (!workspace || workspace_bytes < q4moe::route_rule_workspace_bytes(T, r.n_experts) || !aligned(workspace, 256))
       return Q4MOE_EWORKSPACE;

@@ -28,19 +28,18 @@ __device__ __forceinline__ uint16_t i8_bf16(float f) {
 
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 
-// One wave per row; bound by the row's bytes.
+// One wave per row; bound by the row's bytes: 8192 x 4096 in 26-31 us, 100 MB (3.2-3.9 TB/s).
 template <typename In, int kHeld>
 __global__ __launch_bounds__(256) void i8_quantize_kernel(const In* __restrict__ X, int64_t rows, int K,
                                                           int8_t* __restrict__ codes, float* __restrict__ scales) {
-  const int64_t r = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave;
-  if (r >= rows) return;
-  i8_quantize_row<kHeld>(X + r * K, K, codes + r * K, scales + r);
+  for (int64_t r = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave; r < rows; r += (int64_t)gridDim.x * 4)
+    i8_quantize_row<kHeld>(X + r * K, K, codes + r * K, scales + r);
 }
 
 template <typename In>
 hipError_t launch_quantize(const In* X, int64_t rows, int K, int8_t* codes, float* scales, hipStream_t stream) {
   if (rows <= 0) return hipSuccess;
-  const dim3 grid((unsigned)((rows + 3) / 4)), threads(256);
+  const dim3 grid((unsigned)std::min<int64_t>((rows + 3) / 4, 1 << 20)), threads(256);
   if (K <= 512)
     hipLaunchKernelGGL((i8_quantize_kernel<In, 1>), grid, threads, 0, stream, X, rows, K, codes, scales);
   else if (K <= 2048)
@@ -81,6 +80,15 @@ __device__ __forceinline__ void each_stage(F f, std::integer_sequence<int, St...
   (f(std::integral_constant<int, St>{}), ...);
 }
 
+// Measured (MI355X; a large copy moves 5.1 TB/s, the library's int8 product of 8192^3 runs at
+// 2.1 POP/s): 8192 x 8192 x 4096 in 250 us, 2.2 POP/s; its matrix instructions alone take 177
+// us on this data, so what is left is the loads' and the turn's share that they do not cover.
+// Grouped, 16,384 rows over 256 experts of 2048 x 512 and 2,048 of the shared one: gate/up
+// 131 us for 541 MB of weights (4.1 TB/s), down 80 us for 270 MB of weights and 75 MB of sums
+// (4.3 TB/s): bound by the weights' bytes, and by the last of 4.25 rounds of workgroups.
+// Operand tiles of 64 x 64 per wave were taken for them over 128 x 64 (139 and 86 us: half
+// the waves) and over two smaller workgroups a compute unit (285 us a layer against 263).
+//
 // Workgroup = WM x WN waves, each FM x FN blocks of 32 x 32 (v_mfma_i32_32x32x32_i8).  Each
 // 128-column K step of both operands goes through LDS by 16-byte DMA loads (8 lanes read a
 // row's whole line) in kStages stages; inside a row the eight 16-byte pieces are
@@ -378,6 +386,8 @@ __global__ __launch_bounds__(WM* WN* kWave) void i8_tile_kernel(I8GemmArgs p) {
   i8_tile_body<WM, WN, FM, FN, kStages, EPI>(p);
 }
 
+constexpr int64_t kMaxThreads = 0xFFFFFFFFll;  // of a grid
+
 template <int WM, int WN, int FM, int FN, int kStages, int EPI>
 hipError_t launch_tiles(I8GemmArgs p, int64_t tiles, hipStream_t stream) {
   constexpr int kCols = WN * FN * 32 / (EPI == kEpiSwiglu ? 2 : 1);
@@ -386,12 +396,14 @@ hipError_t launch_tiles(I8GemmArgs p, int64_t tiles, hipStream_t stream) {
   const int64_t blocks = p.tiles ? (tiles + kXcds - 1) / kXcds * kXcds * p.n_slices
                                  : (tiles * p.n_slices + kXcds - 1) / kXcds * kXcds;
   if (blocks <= 0) return hipSuccess;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (blocks * (WM * WN * kWave) > kMaxThreads) return hipErrorInvalidValue;  // bounded by the callers
   hipLaunchKernelGGL((i8_tile_kernel<WM, WN, FM, FN, kStages, EPI>), dim3((unsigned)blocks), dim3(WM * WN * kWave), 0,
                      stream, p);
   return hipGetLastError();
 }
 
+// Bound by the sums' bytes, written just before: 2,048 tokens of 9 slots and 2,048 columns in
+// 24 us, 84 MB beside the channels' scales from the L2.
 // y[t] = sum_i w_i (sums of slot i * its row's scale * the channel's scale) + shared, in slot
 // order, the shared expert last; slots whose id names no expert add nothing.
 template <typename Part>
@@ -527,7 +539,9 @@ hipError_t run_i8_gemm(const I8Mat& W, int64_t n, int K, const uint16_t* X, int6
   // on 2048 x 2048 take 32, 21 and 13 us with it.
   const int64_t cus = device_cu_count();
   auto rounds = [&](int64_t t, int64_t at_once) {
-    return (double)(((m + t - 1) / t * ((n + t - 1) / t) + cus * at_once - 1) / (cus * at_once));
+    const int64_t blocks = (m + t - 1) / t * ((n + t - 1) / t);
+    if (t < 256 && (blocks + kXcds) * 256 > kMaxThreads) return 1e30;  // more than a grid holds
+    return (double)((blocks + cus * at_once - 1) / (cus * at_once));
   };
   const double large = rounds(256, 1) * 1.95, middle = rounds(128, 2) * 1.14, small = rounds(64, 3) * 0.63;
   if (large <= middle && large <= small)

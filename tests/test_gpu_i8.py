@@ -116,6 +116,20 @@ def test_gemm_largest_sums(B, m):
     _check_gemm(B, W, X, B.i8_gemm(_dev(B, W), B.bf16_tensor(X)), B.i8_gemm(_dev(B, W), B.bf16_tensor(X), B.OUT_BF16))
 
 
+@pytest.mark.parametrize("m", [3, 20])
+def test_gemm_weights_past_4gb(B, m):
+    """Code offsets and output rows beyond 32 bits: the last channels of a 4.4 GB matrix."""
+    n, k = 2_100_000, 2112
+    gen = torch.Generator(device="cuda").manual_seed(m)
+    codes = torch.randint(-127, 128, (n, k), generator=gen, device="cuda", dtype=torch.int8)
+    scales = torch.rand(n, generator=gen, device="cuda") * 1e-3
+    X = _rows(m, m, k)
+    y = B.i8_gemm(B.DeviceI8(codes, scales), B.bf16_tensor(X))
+    for at in (slice(0, 70), slice(n // 2, n // 2 + 70), slice(n - 70, n)):
+        ref = orc.i8_gemm(codes[at].cpu().numpy(), scales[at].cpu().numpy(), X)
+        assert (np.abs(to_f64(y[:, at]) - ref) <= 3 * HALF * (1 + 1e-6) * np.abs(ref) + 2.0 ** -149).all()
+
+
 @pytest.mark.parametrize("m", [3, 16, 70])
 def test_gemm_rows_without_values(B, m):
     """A zero row gives zeros, a row with an infinity or a NaN gives NaN, and no other row notices."""

@@ -43,6 +43,7 @@ def test_route_rejects(lib):
     assert g(_rule(n_experts=1024, n_groups=128), A, 10, A2, A2, None) == B.EUNSUPPORTED
     assert g(_rule(n_groups=1, top_groups=1, top_k=33), A, 10, A2, A2, None) == B.EUNSUPPORTED
     assert g(_rule(), A, 1 << 31, A2, A2, None) == B.EUNSUPPORTED
+    assert f(_rule(), A, (1 << 26) + 1, A2, A2, A, 1 << 60, None) == B.EUNSUPPORTED
     assert f(None, A, 10, A2, A2, A, need, None) == B.EINVAL
     for bad in (dict(hidden=100), dict(hidden=0), dict(router=None), dict(router=A + 8)):
         assert f(_rule(**bad), A, 10, A2, A2, A, need, None) == B.EINVAL, bad
@@ -99,6 +100,8 @@ def test_i8_gemm_rejects(lib):
     assert f(W, A, -1, Y, 0, A2, need, None) == B.EINVAL
     assert f(W, A, 100, A + 256, 0, A2, need, None) == B.EINVAL                      # Y over X
     assert f(W, A, 1 << 31, Y, 0, A2, 1 << 60, None) == B.EUNSUPPORTED
+    # more tiles than a grid holds
+    assert f(ctypes.byref(_mat(n=1 << 30)), A, 1 << 20, Y, 0, A2, 1 << 60, None) == B.EUNSUPPORTED
     assert f(W, A, 100, Y, 0, None, need, None) == B.EWORKSPACE
     assert f(W, A, 100, Y, 0, A2, need - 1, None) == B.EWORKSPACE
     assert f(W, A, 100, Y, 0, A2 + 16, need, None) == B.EWORKSPACE
@@ -126,6 +129,8 @@ def test_experts_rejects(lib):
         assert lib.moe_experts_i8_workspace_bytes(ctypes.byref(bad), 10, 2) == 0
     assert f(ctypes.byref(_experts(E=1025)), A, 10, I, Wt, 2, Y, 0, A2, 1 << 40, None) == B.EUNSUPPORTED
     assert f(ctypes.byref(_experts(H=16384 + 64)), A, 10, I, Wt, 2, Y, 0, A2, 1 << 40, None) == B.EUNSUPPORTED
+    # 2^18 tokens of 16,384 columns: the offsets of gathered rows
+    assert f(ctypes.byref(_experts(H=16384)), A, 1 << 18, I, Wt, 2, Y, 0, A2, 1 << 60, None) == B.EUNSUPPORTED
     assert f(good, A, 10, I, Wt, 33, Y, 0, A2, 1 << 40, None) == B.EUNSUPPORTED
     assert f(good, A, 1 << 30, I, Wt, 2, Y, 0, A2, 1 << 60, None) == B.EUNSUPPORTED
     assert f(good, A, 10, I, Wt, 0, Y, 0, A2, need, None) == B.EINVAL
