@@ -250,9 +250,9 @@ int moe_route_topk_q8(const q4moe_matrix* router_q8, const q4moe_bf16* X, int64_
  * moe_route_topk and moe_route_topk_q8 compute them, then the rule.  Writes ids
  * int32 [T][top_k] and weights fp32 [T][top_k]; T up to 2^26.  Needs Q4MOE_OP_ROUTE_RULE
  * workspace (n_experts; T), zero-filled before its first use and used by moe_route
- * alone: up to four rows run as one launch whose last workgroup selects, by an
- * arrival count that each call leaves at zero again.  Calls that share a workspace
- * must not overlap.
+ * alone: few rows run as one launch whose last workgroups select, by arrival
+ * counts in its first 256 bytes that each call leaves at zero again.  Calls that
+ * share a workspace must not overlap.
  */
 int moe_route(const q4moe_routing* rule, const q4moe_bf16* X, int64_t T, int32_t* ids, float* weights,
               void* workspace, size_t workspace_bytes, q4moe_stream stream);

@@ -92,7 +92,7 @@ struct RouteRule {
 };
 hipError_t run_select(const RouteRule& r, const float* logits, int64_t T, int32_t* ids, float* weights,
                       hipStream_t stream);
-// The router's logits, then the selection; ws: an arrival counter that is zero between the
+// The router's logits, then the selection; ws: arrival counts that are zero between the
 // calls, then the logits (route_rule_workspace_bytes).
 size_t route_rule_workspace_bytes(int64_t T, int n_experts);
 hipError_t run_route(const RouteRule& r, const uint16_t* router, const Q4Mat* router_q8, int H, const uint16_t* X,

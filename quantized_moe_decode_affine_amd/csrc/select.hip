@@ -16,6 +16,7 @@
 // about 3 us after the launch; the logits are 2 MB) and 15 us for 4,093 of 512 (issue-bound:
 // eight 64-bit exponentials, a sort and ten rounds a wave).
 #include <algorithm>
+#include <type_traits>
 
 #include "kernels.h"
 #include "topk.h"
@@ -226,19 +227,26 @@ __global__ __launch_bounds__(kSelWaves * kWave) void select_kernel(RouteRule r, 
     select_row<V, false>(r, logits + t * r.n_experts, s_c[wave], ids + t * r.top_k, weights + t * r.top_k);
 }
 
-// Routing of at most kSelWaves tokens in one launch: a wave per expert takes its row of the
-// router once for all tokens, and the last workgroup to finish selects, a wave per token.
-// The launch is bound by latencies (its bytes, 1 MB at 256 experts of 2,048 columns, take
-// 0.2 us): one launch instead of two saves one of each, 9.8 us against 12.8 for one token
-// (and 4 us of the host's time).  `arrived` is zero before the launch and after it.
+// Routing of few tokens in one launch, kSelWaves of them to a group of workgroups: a wave per
+// expert takes its row of the router once for the group's tokens, and the group's last
+// workgroup to finish selects, a wave per token.  The launch is bound by latencies (its
+// bytes, 1 MB at 256 experts of 2,048 columns, take 0.2 us): one launch instead of two saves
+// one of each, 8.2 us against 12.8 for one token (and 4 us of the host's time).  `arrived`,
+// a count per group, is zero before the launch and after it.
 template <int V, bool kQ8>
 __global__ __launch_bounds__(kSelWaves * kWave) void route_few_kernel(RouteRule r, const uint16_t* __restrict__ router,
                                                                       Q4Mat q8, int H, const uint16_t* __restrict__ X,
-                                                                      int T, float* logits, unsigned* arrived,
+                                                                      int rows, float* logits, unsigned* arrived,
                                                                       int32_t* __restrict__ ids,
                                                                       float* __restrict__ weights) {
   __shared__ double s_c[kSelWaves][V * kWave];
   __shared__ bool s_last;
+  const int t0 = blockIdx.y * kSelWaves, T = min(kSelWaves, rows - t0);  // this group's tokens
+  X += (int64_t)t0 * H;
+  logits += (int64_t)t0 * r.n_experts;
+  ids += t0 * r.top_k;
+  weights += t0 * r.top_k;
+  arrived += blockIdx.y;
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int e = blockIdx.x * kSelWaves + wave;
@@ -274,30 +282,34 @@ __global__ __launch_bounds__(kSelWaves * kWave) void route_few_kernel(RouteRule 
       }
     } else {
       constexpr int kAhead = 4;  // pieces of 8 columns in flight per lane: 2,048 columns
-      for (int j0 = 0; j0 < H; j0 += kAhead * kWave * 8) {
-        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-        uint4 w[kAhead];
-        auto piece = [&](const uint16_t* row, int c) {
-          const int j = j0 + (c * kWave + lane) * 8;
-          return j < H ? *reinterpret_cast<const uint4*>(row + j) : zero;
-        };
+      const uint16_t* w_row = router + (int64_t)e * H;
+      auto dots = [&](auto tokens_c) __attribute__((always_inline)) {
+        constexpr int kTokens = decltype(tokens_c)::value;  // loads of a group of fewer repeat its last
+        for (int j0 = 0; j0 < H; j0 += kAhead * kWave * 8) {
+          auto piece = [&](const uint16_t* row, int c) {
+            const int j = j0 + (c * kWave + lane) * 8;
+            return j < H ? *reinterpret_cast<const uint4*>(row + j) : make_uint4(0u, 0u, 0u, 0u);
+          };
+          uint4 w[kAhead], x[kTokens][kAhead];
 #pragma unroll
-        for (int c = 0; c < kAhead; ++c) w[c] = piece(router + (int64_t)e * H, c);
+          for (int c = 0; c < kAhead; ++c) w[c] = piece(w_row, c);
 #pragma unroll
-        for (int t = 0; t < kSelWaves; ++t) {
-          if (t >= T) break;
-          uint4 x[kAhead];
+          for (int t = 0; t < kTokens; ++t)
 #pragma unroll
-          for (int c = 0; c < kAhead; ++c) x[c] = piece(X + (int64_t)t * H, c);
+            for (int c = 0; c < kAhead; ++c) x[t][c] = piece(X + (int64_t)min(t, T - 1) * H, c);
 #pragma unroll
-          for (int c = 0; c < kAhead; ++c) {
-            acc[t] = dot2_bf16(w[c].x, x[c].x, acc[t]);
-            acc[t] = dot2_bf16(w[c].y, x[c].y, acc[t]);
-            acc[t] = dot2_bf16(w[c].z, x[c].z, acc[t]);
-            acc[t] = dot2_bf16(w[c].w, x[c].w, acc[t]);
-          }
+          for (int t = 0; t < kTokens; ++t)
+#pragma unroll
+            for (int c = 0; c < kAhead; ++c) {
+              acc[t] = dot2_bf16(w[c].x, x[t][c].x, acc[t]);
+              acc[t] = dot2_bf16(w[c].y, x[t][c].y, acc[t]);
+              acc[t] = dot2_bf16(w[c].z, x[t][c].z, acc[t]);
+              acc[t] = dot2_bf16(w[c].w, x[t][c].w, acc[t]);
+            }
         }
-      }
+      };
+      if (T == 1) dots(std::integral_constant<int, 1>{});
+      else dots(std::integral_constant<int, kSelWaves>{});
     }
 #pragma unroll
     for (int t = 0; t < kSelWaves; ++t) {
@@ -323,7 +335,8 @@ template <int V>
 hipError_t launch_route_few(const RouteRule& r, const uint16_t* router, const Q4Mat* q8, int H, const uint16_t* X,
                             int T, float* logits, unsigned* arrived, int32_t* ids, float* weights,
                             hipStream_t stream) {
-  const dim3 grid((unsigned)((r.n_experts + kSelWaves - 1) / kSelWaves)), threads(kSelWaves * kWave);
+  const dim3 grid((unsigned)((r.n_experts + kSelWaves - 1) / kSelWaves), (unsigned)((T + kSelWaves - 1) / kSelWaves));
+  const dim3 threads(kSelWaves * kWave);
   if (q8->codes)
     hipLaunchKernelGGL((route_few_kernel<V, true>), grid, threads, 0, stream, r, router, *q8, H, X, T, logits, arrived,
                        ids, weights);
@@ -333,7 +346,13 @@ hipError_t launch_route_few(const RouteRule& r, const uint16_t* router, const Q4
   return hipGetLastError();
 }
 
-constexpr size_t kArrivedBytes = 256;  // the arrival counter, before the logits
+// One launch where its rereading of the router by every group costs less than the second
+// launch: up to 64 rows, and rows x experts up to 5,120 (16 rows of 256 experts 11.4 us against
+// 13.4, 64 of 60 9.5 against 12.2; 37 of 256 18.0 against 13.7), with an 8-bit router up to
+// 8,192 (16 of 256 12.1 against 17.5; 37 of 256 18.0 against 17.9).
+constexpr int64_t kFewTokens = 64, kFewWork = 5120, kFewWorkQ8 = 8192;
+constexpr size_t kArrivedBytes = 256;  // the groups' arrival counts, before the logits
+static_assert(kFewTokens / kSelWaves * sizeof(unsigned) <= kArrivedBytes, "a count per group");
 
 }  // namespace
 
@@ -359,7 +378,7 @@ hipError_t run_route(const RouteRule& r, const uint16_t* router, const Q4Mat* ro
                      int64_t T, int32_t* ids, float* weights, void* ws, hipStream_t stream) {
   unsigned* arrived = static_cast<unsigned*>(ws);
   float* logits = reinterpret_cast<float*>(static_cast<char*>(ws) + kArrivedBytes);
-  if (T <= kSelWaves) {
+  if (T <= kFewTokens && T * r.n_experts <= (router_q8->codes ? kFewWorkQ8 : kFewWork)) {
     if (r.n_experts <= kWave)
       return launch_route_few<1>(r, router, router_q8, H, X, (int)T, logits, arrived, ids, weights, stream);
     if (r.n_experts <= 4 * kWave)

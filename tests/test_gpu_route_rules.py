@@ -104,7 +104,8 @@ def _grid(seed, shape, std, step, most):
 
 
 @pytest.mark.parametrize("T,E,H,k", [(1, 256, 2048, 8), (2, 16, 64, 4), (3, 60, 1088, 6), (4, 1000, 576, 9), (4, 257, 4096, 3), (15, 256, 128, 8), (16, 512, 320, 10),
-                                     (17, 512, 2048, 10), (33, 1024, 192, 32), (64, 8, 256, 2), (130, 257, 448, 5),
+                                     (17, 512, 2048, 10), (33, 1024, 192, 32),
+                                     (64, 60, 2048, 6), (63, 81, 2112, 7), (5, 1024, 64, 3), (13, 250, 4160, 8), (64, 8, 256, 2), (130, 257, 448, 5),
                                      (2048, 256, 2048, 8)])
 def test_route_bf16_router(B, T, E, H, k):
     R, X = _grid(E + H, (E, H), 0.02, 2.0 ** -10, 255), _grid(T, (T, H), 1.0, 2.0 ** -3, 40)
@@ -117,7 +118,7 @@ def test_route_bf16_router(B, T, E, H, k):
     _check(ids[some], w[some], *ref)
 
 
-@pytest.mark.parametrize("T,E,H,k", [(1, 256, 2048, 8), (2, 7, 64, 3), (3, 600, 1088, 8), (4, 60, 192, 6), (5, 60, 192, 6), (16, 100, 320, 4), (37, 512, 1088, 10),
+@pytest.mark.parametrize("T,E,H,k", [(1, 256, 2048, 8), (2, 7, 64, 3), (3, 600, 1088, 8), (4, 60, 192, 6), (5, 60, 192, 6), (64, 128, 320, 6), (63, 60, 2112, 6), (16, 100, 320, 4), (37, 512, 1088, 10),
                                      (1111, 509, 448, 7), (2100, 256, 128, 3)])
 def test_route_q8_router(B, T, E, H, k):
     rng = np.random.default_rng(E + T)
@@ -162,7 +163,7 @@ def test_one_workspace_for_many_calls(B, E, H, q8):
     r = B.Routing(router, 7, score="sigmoid")
     ws = B.moe_route_workspace(r, 50)
     side = torch.cuda.Stream()
-    for n, T in enumerate((1, 4, 50, 2, 5, 3, 1, 1)):
+    for n, T in enumerate((1, 4, 50, 2, 17, 5, 49, 3, 1, 1)):
         X = B.bf16_tensor(_grid(n, (T, H), 1.0, 2.0 ** -3, 40))
         want = B.moe_route(r, X)
         torch.cuda.synchronize()
@@ -170,7 +171,7 @@ def test_one_workspace_for_many_calls(B, E, H, q8):
             got = B.moe_route(r, X, ws=ws)
         torch.cuda.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
-        assert not ws[:4].any()
+        assert not ws[:256].any()
 
 
 def test_empty_batch_and_refusals(B):
@@ -194,7 +195,7 @@ def test_empty_batch_and_refusals(B):
     assert e.value.status == B.EWORKSPACE
 
 
-@pytest.mark.parametrize("T", [1, 3, 40])
+@pytest.mark.parametrize("T", [1, 3, 40, 100])
 def test_captured_route_replays(B, T):
     R = B.bf16_tensor(_grid(1, (64, 256), 0.02, 2.0 ** -10, 255))
     r = B.Routing(R, 6, score="sigmoid", bias=torch.linspace(-0.1, 0.1, 64, device="cuda"), n_groups=4, top_groups=2)
