@@ -323,6 +323,60 @@ def test_route_then_experts(B, T):
         assert torch.equal(B.moe_experts_i8(ex, X, i2, w2), y)
 
 
+def test_two_graphs_share_workspaces(B):
+    """Two captured steps of different sizes on the same workspaces, replayed in turn between eager
+    calls on them: each leaves them ready for the other."""
+    E, H, I, k = 16, 256, 128, 4
+    layer = _layer(21, E, H, I, True)
+    ex = _experts(B, layer)
+    r = B.Routing(B.bf16_tensor(_rows(22, E, H)), k, score="sigmoid")
+    ws, wr = B.moe_experts_i8_workspace(ex, 90, k), B.moe_route_workspace(r, 90)
+
+    def step(X, out):
+        ids, w = B.moe_route(r, X, ws=wr)
+        return B.moe_experts_i8(ex, X, ids, w, out=out, ws=ws)
+
+    parts = []
+    for T in (2, 90):
+        X = B.bf16_tensor(_rows(T, T, H))
+        Y = torch.empty(T, H, device="cuda")
+        step(X, Y)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step(X, Y)
+        parts.append((X, Y, graph))
+    for n in range(3):
+        for X, Y, graph in parts:
+            X.copy_(B.bf16_tensor(_rows(30 + n, X.shape[0], H)))
+            Y.zero_()
+            graph.replay()
+            got = Y.clone()
+            want = step(X, torch.empty_like(Y))
+            torch.cuda.synchronize()
+            assert torch.equal(got, want)
+
+
+def test_experts_on_two_streams(B):
+    """Calls in flight together on one set of weights, each with a workspace of its own."""
+    layer = _layer(23, 12, 256, 192, True)
+    ex = _experts(B, layer)
+    args = []
+    for T in (1, 6, 40, 200):
+        ids, w = _ids(T, T, 12, 3, 0.1)
+        args.append((B.bf16_tensor(_rows(T, T, 256)), torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda()))
+    want = [B.moe_experts_i8(ex, *a) for a in args]
+    streams = [torch.cuda.Stream() for _ in args]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for a, s in zip(args, streams):
+            with torch.cuda.stream(s):
+                got.append(B.moe_experts_i8(ex, *a))
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
 def test_refusals(B):
     W = _dev(B, _weights(1, 64, 128))
     X = torch.zeros(3, 128, dtype=torch.bfloat16, device="cuda")
