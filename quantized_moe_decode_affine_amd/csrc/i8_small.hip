@@ -316,19 +316,31 @@ __global__ __launch_bounds__(kSmallWaves* kWave) void i8_slots_up_kernel(I8Exper
 }
 
 // Down and the weighted sum: a workgroup per (token, 16 output columns), a wave per slot
-// (in turn).
+// (in turn).  kHalves: 8 output columns, their rows twice in the operand's 16, with the lower
+// half of K and with the upper; the codes' halves stand as two tokens, and a sum is row r of
+// the one plus row r + 8 of the other.  That puts one token's step on twice as many compute
+// units: with hidden 2048 (128 workgroups of 16 columns) a step takes 12.6 us instead of 13.0.
+// It is for one token whose blocks of 16 are fewer than the compute units, and intermediate
+// sizes whose halves are whole batches of loads.
+template <bool kHalves>
 __global__ void i8_slots_down_kernel(I8Experts L, int T, int k, const int32_t* __restrict__ ids,
                                      const float* __restrict__ weights, int shared, const float* __restrict__ act,
                                      void* __restrict__ Y, int out_bf16) {
-  extern __shared__ __align__(16) uint8_t s_dyn[];  // [waves] images of one row, then [slots][16] parts
+  extern __shared__ __align__(16) uint8_t s_dyn[];  // [waves] images of one row, then [slots][kCols] parts
+  constexpr int kCols = kHalves ? 8 : 16;
+  constexpr int kLoads = kHalves ? kBatch / 2 : kBatch;  // 64 columns each
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), waves = blockDim.x / kWave;
   const int H = L.hidden, I = L.inter, P = T * k, slots = k + shared;
   const int t = blockIdx.y;
-  const int n0 = blockIdx.x * 16;
+  const int n0 = blockIdx.x * kCols;
   const int Kpad = (I + kBatchCols - 1) / kBatchCols * kBatchCols;
+  const int K = kHalves ? I / 2 : I;  // columns that a lane's operand row covers (halves: a multiple of 256)
   uint8_t* image = s_dyn + (size_t)wave * Kpad;
   float* s_part = reinterpret_cast<float*>(s_dyn + (size_t)waves * Kpad);
+  const int a = lane & 15, g = (lane >> 4) * 16;
+  const int w_row = a % kCols, w_col = kHalves ? (a / kCols) * K : 0;  // this lane's weight row and first column
+  const uint8_t* codes = image + (kHalves ? (lane & 1) * K : 0) + g;   // and its codes (one row: column c at c)
   for (int s = wave; s < slots; s += waves) {
     const bool sh = s >= k;
     const int e = sh ? 0 : ids[t * k + s];
@@ -337,36 +349,51 @@ __global__ void i8_slots_down_kernel(I8Experts L, int T, int k, const int32_t* _
     if (there) {
       const I8Mat down = sh ? L.sh_down : L.down;
       const int64_t r0 = (int64_t)e * H + n0;
-      const int8_t* row = down.codes + (r0 + (lane & 15)) * I;
+      const int8_t* row = down.codes + (r0 + w_row) * I + w_col;
       const int64_t slot = sh ? P + t : t * k + s;
-      i32x4_t w[kBatch];
+      const int out_row = (lane >> 4) * 4 % kCols;  // output columns out_row .. + 3 of this lane
+      i32x4_t w[kLoads];
+      auto load = [&](int c) {
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j)
+          w[j] = *reinterpret_cast<const i32x4_t*>(row + min(c + j * 64 + g, K - 16));
+      };
       float sw[4], f = 1.0f;
       const float scale = quantize_row<1>(
           act + slot * I, I, Kpad, image, 0, 1, 0, 1,
           [&] {
-            load_batch(row, 0, I, w);
+            load(0);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sw[i] = down.scales[r0 + (lane >> 4) * 4 + i];
+            for (int i = 0; i < 4; ++i) sw[i] = down.scales[r0 + out_row + i];
             if (!sh) f = weights[t * k + s];
           },
           [](uint32_t most) { return most; });
       __builtin_amdgcn_wave_barrier();
-      i32x4acc_t acc = mul_batch(w, image, 0, 1, i32x4acc_t{});
-      for (int c = kBatchCols; c < I; c += kBatchCols) {
-        load_batch(row, c, I, w);
-        acc = mul_batch(w, image, c, 1, acc);
+      i32x4acc_t acc = {};
+      for (int c = 0; c < K; c += kLoads * 64) {
+        if (c > 0) load(c);
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j)
+          acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[j], *reinterpret_cast<const i32x4_t*>(codes + c + j * 64), acc,
+                                                      0, 0, 0);
+      }
+      if constexpr (kHalves) {
+        // rows 0..7 of token 0 lie in lanes 0 and 16, rows 8..15 of token 1 in lanes 33 and 49
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] += __shfl(acc[i], lane + 33, kWave);
       }
       f *= scale;
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = (float)acc[i] * f * sw[i];
       __builtin_amdgcn_wave_barrier();  // the image is read before the next slot's replaces it
     }
-    if ((lane & 15) == 0) *reinterpret_cast<float4*>(s_part + s * 16 + (lane >> 4) * 4) = make_float4(v[0], v[1], v[2], v[3]);
+    if (a == 0 && (lane >> 4) * 4 < kCols)
+      *reinterpret_cast<float4*>(s_part + s * kCols + (lane >> 4) * 4) = make_float4(v[0], v[1], v[2], v[3]);
   }
   __syncthreads();
-  if (threadIdx.x < 16) {
+  if (threadIdx.x < kCols) {
     float y = 0.f;
-    for (int s = 0; s < slots; ++s) y += s_part[s * 16 + threadIdx.x];
+    for (int s = 0; s < slots; ++s) y += s_part[s * kCols + threadIdx.x];
     const int64_t at = (int64_t)t * H + n0 + threadIdx.x;
     if (out_bf16) static_cast<uint16_t*>(Y)[at] = small_bf16(y);
     else static_cast<float*>(Y)[at] = y;
@@ -401,8 +428,13 @@ hipError_t run_i8_few_slots(const I8Experts& L, const uint16_t* X, int T, const 
   if (e != hipSuccess) return e;
   const int waves = down_waves(L.inter, k + shared);
   const size_t lds = (size_t)waves * ((L.inter + kBatchCols - 1) / kBatchCols * kBatchCols) + (size_t)(k + shared) * 64;
-  hipLaunchKernelGGL(i8_slots_down_kernel, dim3(L.hidden / 16, T), dim3(waves * kWave), lds, stream, L, T, k, ids,
-                     weights, shared, act, Y, out_bf16);
+  const dim3 threads(waves * kWave);
+  if (T == 1 && L.inter % kBatchCols == 0 && L.hidden / 16 < device_cu_count())
+    hipLaunchKernelGGL(i8_slots_down_kernel<true>, dim3(L.hidden / 8, T), threads, lds, stream, L, T, k, ids, weights,
+                       shared, act, Y, out_bf16);
+  else
+    hipLaunchKernelGGL(i8_slots_down_kernel<false>, dim3(L.hidden / 16, T), threads, lds, stream, L, T, k, ids, weights,
+                       shared, act, Y, out_bf16);
   return hipGetLastError();
 }
 

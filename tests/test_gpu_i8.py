@@ -213,7 +213,7 @@ def _check_experts(B, layer, X, ids, w, ex=None):
 
 
 @pytest.mark.parametrize("T,E,H,I,k,shared", [
-    (1, 8, 64, 64, 1, False), (1, 256, 256, 128, 8, True), (1, 16, 2048, 512, 8, True), (2, 4, 128, 192, 4, False),
+    (1, 8, 64, 64, 1, False), (1, 256, 256, 128, 8, True), (1, 16, 2048, 512, 8, True), (1, 8, 192, 1024, 3, True), (1, 8, 4160, 512, 2, False), (2, 4, 128, 192, 4, False),
     (3, 60, 1088, 704, 4, True), (5, 16, 192, 64, 2, True), (8, 32, 512, 256, 8, True), (16, 8, 256, 320, 2, False),
     (17, 16, 256, 128, 4, True), (40, 5, 320, 64, 3, False), (129, 3, 128, 128, 1, True), (300, 2, 192, 64, 2, True),
     (64, 1, 128, 256, 1, False), (33, 40, 64, 1088, 32, False)])
