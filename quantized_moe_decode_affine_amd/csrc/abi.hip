@@ -129,7 +129,7 @@ int rule_check(const q4moe_routing* R, q4moe::RouteRule* r) {
   return Q4MOE_OK;
 }
 
-constexpr int64_t kMaxTiles = 1 << 22;  // workgroups of 512 threads in a grid
+constexpr int64_t kMaxTiles = (1 << 23) - 64;  // workgroups of 512 threads in a grid of 2^32
 constexpr int64_t kMaxI8K = 65536;      // 127 * 128 * k stays below 2^31
 constexpr int64_t kMaxExpertK = 16384;  // hidden and intermediate sizes of the 8-bit experts
 
@@ -144,7 +144,7 @@ bool i8_shape(const q4moe_i8_matrix& W, int64_t count, int64_t n, int64_t k) {
 
 int i8_gemm_check(const q4moe_i8_matrix* W, int64_t m) {
   if (!i8_matrix_ok(W) || m < 0) return Q4MOE_EINVAL;
-  // rows and channels are 32-bit in the kernels; a grid of 256 x 256 tiles holds 2^22 of them
+  // rows and channels are 32-bit in the kernels; a grid holds kMaxTiles of 256 x 256
   if (W->k > kMaxI8K || W->count > kMaxRows32 || W->n > kMaxRows32 || W->count * W->n > kMaxRows32 ||
       m > kMaxRows32 || (m / 256 + 1) * (W->count * W->n / 256 + 1) > kMaxTiles)
     return Q4MOE_EUNSUPPORTED;
@@ -162,7 +162,8 @@ int i8_experts_check(const q4moe_i8_experts* L, int64_t T, int64_t top_k, q4moe:
     return Q4MOE_EINVAL;
   // sorted positions, the tiles' grid and the offsets of gathered rows are 32-bit
   const int64_t rows = T > kMaxRows32 ? kMaxRows32 : T * (top_k + 1);
-  if (T > kMaxRows32 || rows > kMaxRows32 || T * H > 0xFFF00000ll || (rows / 64 + 2 * E + 8) * (std::max(H, I) / 64 + 1) > kMaxRows32)
+  if (T > kMaxRows32 || rows > kMaxRows32 || T * H > 0xFFF00000ll ||
+      (rows / 128 + 2 * E + 16) * (std::max(H / 256, I / 128) + 1) > kMaxTiles)
     return Q4MOE_EUNSUPPORTED;
   auto mat = [](const q4moe_i8_matrix& W) { return q4moe::I8Mat{W.codes, W.scales}; };
   const q4moe::I8Mat none{nullptr, nullptr};

@@ -58,7 +58,7 @@ struct I8GemmArgs {
   const int32_t* row_src;  // grouped: row of A of each sorted position (null: the position itself)
   const int4* tiles;       // grouped: {expert (-1 shared, -2 none), first position, rows, 0}; null: dense
   int64_t rows;            // dense: rows of A
-  uint32_t a_rows;         // gathered: rows of A (a_rows * K below 2^32)
+  uint32_t a_rows;         // gathered: rows of A (a_rows * K at most 2^32 - 2^20)
   int64_t P;               // grouped: routed positions; position P + t is token t's for the shared expert
   int K, N;                // N output columns (SwiGLU: gate columns, as many up columns)
   I8Mat W, W2;             // weights (stacked by expert), SwiGLU: gate and up
@@ -71,6 +71,7 @@ struct I8GemmArgs {
 
 constexpr int kStepBytes = 128;  // columns of a K step, one cache line of every operand row
 constexpr int kXcds = 8;
+// Tile rows of a band: the 32 workgroups that an XCD runs at a time then cover 4 x 8 tiles.
 constexpr int kBand = 4;
 
 __device__ __forceinline__ int row_swz(int r) { return (r >> 1) & 7; }
@@ -99,13 +100,11 @@ template <int WM, int WN, int FM, int FN, int kStages, int EPI>
 __device__ __forceinline__ void i8_tile_body(const I8GemmArgs& p) {
   constexpr int TM = WM * FM * 32, TN = WN * FN * 32, kWaves = WM * WN;
   constexpr int kOps = (TM + TN) / 8 / kWaves;  // DMA loads per wave and step, 8 rows each
-  static_assert((TM + TN) / 8 % kWaves == 0 && kStages >= 2 && kStages <= 6, "whole blocks of 8 rows per wave");
+  static_assert((TM + TN) / 8 % kWaves == 0 && (kStages == 2 || kStages == 3), "whole blocks of 8 rows per wave");
   constexpr int kStageBytes = (TM + TN) * kStepBytes;
   // one array per stage, so that the compiler can tell a stage's reads from the loads
   // still filling another
-  constexpr auto size = [](int st) { return st < kStages ? kStageBytes : 16; };
-  __shared__ __align__(16) uint8_t s_st0[size(0)], s_st1[size(1)], s_st2[size(2)], s_st3[size(3)], s_st4[size(4)],
-      s_st5[size(5)];
+  __shared__ __align__(16) uint8_t s_st0[kStageBytes], s_st1[kStageBytes], s_st2[kStages > 2 ? kStageBytes : 16];
   constexpr bool kSwiglu = EPI == kEpiSwiglu;
   constexpr int kCols = kSwiglu ? TN / 2 : TN;  // output columns of a tile
   const int lane = lane_id();
@@ -192,9 +191,7 @@ __device__ __forceinline__ void i8_tile_body(const I8GemmArgs& p) {
   const __amdgpu_buffer_rsrc_t ra =
       rsrc(p.row_src ? p.A : p.A + first * p.K, (p.row_src ? p.a_rows : (uint32_t)rows) * (uint32_t)p.K);
   const __amdgpu_buffer_rsrc_t rw = rsrc(w.codes + w_off, w_bytes), ru = rsrc(w2.codes + w_off, w_bytes);
-  auto stage = [&](int st) -> uint8_t* {
-    return st == 0 ? s_st0 : st == 1 ? s_st1 : st == 2 ? s_st2 : st == 3 ? s_st3 : st == 4 ? s_st4 : s_st5;
-  };
+  auto stage = [&](int st) -> uint8_t* { return st == 0 ? s_st0 : st == 1 ? s_st1 : s_st2; };
   const int steps = (p.K + kStepBytes - 1) / kStepBytes;
   // steps past the last load it again and are not computed
   auto issue_op = [&](int i, int st, int j) __attribute__((always_inline)) {
@@ -295,13 +292,15 @@ __device__ __forceinline__ void i8_tile_body(const I8GemmArgs& p) {
 #pragma unroll
     for (int j = 0; j < (st + 1 < kStages ? kOps : kOps / 2); ++j) issue_op(st, st, j);
   // grouped tiles are often part full: only the 32-row blocks that hold rows are multiplied
-  constexpr bool kPart = EPI != kEpiF32 && EPI != kEpiBf16;
-  const int nf = kPart ? max(0, min(FM, (rows - wm * FM * 32 + 31) / 32)) : FM;
-  if (nf == FM) run(std::integral_constant<int, FM>{});
-  else if (FM > 3 && nf == 3) run(std::integral_constant<int, (FM > 3 ? 3 : 0)>{});
-  else if (FM > 2 && nf == 2) run(std::integral_constant<int, (FM > 2 ? 2 : 0)>{});
-  else if (FM > 1 && nf == 1) run(std::integral_constant<int, (FM > 1 ? 1 : 0)>{});
-  else run(std::integral_constant<int, 0>{});
+  if constexpr (EPI == kEpiF32 || EPI == kEpiBf16) {
+    run(std::integral_constant<int, FM>{});
+  } else {
+    static_assert(FM == 2, "none, one or both of a wave's blocks");
+    const int held = rows - wm * FM * 32;
+    if (held > 32) run(std::integral_constant<int, 2>{});
+    else if (held > 0) run(std::integral_constant<int, 1>{});
+    else run(std::integral_constant<int, 0>{});
+  }
   __builtin_amdgcn_s_waitcnt(0);  // the repeated loads of the last steps are still landing
 
   // The weight is the first operand of the products, so that a lane holds sums of one row of

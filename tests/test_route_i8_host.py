@@ -131,6 +131,8 @@ def test_experts_rejects(lib):
     assert f(ctypes.byref(_experts(H=16384 + 64)), A, 10, I, Wt, 2, Y, 0, A2, 1 << 40, None) == B.EUNSUPPORTED
     # 2^18 tokens of 16,384 columns: the offsets of gathered rows
     assert f(ctypes.byref(_experts(H=16384)), A, 1 << 18, I, Wt, 2, Y, 0, A2, 1 << 60, None) == B.EUNSUPPORTED
+    # and the tiles of a grid
+    assert f(ctypes.byref(_experts(I=16384)), A, 1 << 22, I, Wt, 2, Y, 0, A2, 1 << 60, None) == B.EUNSUPPORTED
     assert f(good, A, 10, I, Wt, 33, Y, 0, A2, 1 << 40, None) == B.EUNSUPPORTED
     assert f(good, A, 1 << 30, I, Wt, 2, Y, 0, A2, 1 << 60, None) == B.EUNSUPPORTED
     assert f(good, A, 10, I, Wt, 0, Y, 0, A2, need, None) == B.EINVAL
