@@ -73,7 +73,7 @@ enum {
  * row in byte j%4 of word j/4 (least significant first), same groups and
  * w = scale*q + bias.  q4_gemv and lmhead_argmax take 8-bit matrices, the layer
  * calls an 8-bit router (router_q8) and an 8-bit shared expert, and
- * moe_route_topk_q8 an 8-bit router; the other calls return Q4MOE_EUNSUPPORTED
+ * moe_route_topk_q8 and moe_route an 8-bit router; the other calls return Q4MOE_EUNSUPPORTED
  * for them.
  *
  * codes_gm (optional, 4-bit only): the same codes group-major, as written by
@@ -107,7 +107,7 @@ typedef struct {
  * n_experts x hidden, bits 8: the benchmark checkpoint's affine Q8 router-gate
  * exceptions, "2026-09-02: Lily vs MLX 0.32.2", "Hardware and software"), and
  * `router` may be null.  moe_ffn_decode, moe_ffn_decode_batch and moe_ffn_prefill
- * all take an 8-bit router (the standalone router: moe_route_topk_q8).  The
+ * all take an 8-bit router (the standalone routers: moe_route_topk_q8, moe_route).  The
  * shared expert's three matrices may be 8-bit together (the q4-xl conversion
  * keeps it at 8 bits: "lily-qwen3.8-flash-next" README, "The model"); the layer
  * calls take that form (a mix of 4- and 8-bit shared matrices is
