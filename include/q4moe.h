@@ -397,10 +397,8 @@ size_t i8_gemm_workspace_bytes(const q4moe_i8_matrix* W, int64_t m);
  * 8-bit form per token and expert.  A slot whose id lies outside [0, n_experts) adds
  * nothing (a token all of whose slots do gets the shared expert alone, or zeros); an
  * id may stand in several slots of a token.  The slots' products are summed in fp32
- * in slot order, the shared expert last.  With a bf16 Y the integer sums of the down
- * product may be rounded to 11 significant bits before that (fp16, scaled by a power
- * of two): by 2^-11 of each summand at most, next to the output's own 2^-8.
- * Other tokens of the call move a token's result by such roundings alone.
+ * in slot order, the shared expert last; a bf16 Y is that sum rounded once.  Other
+ * tokens of the call move a token's result by fp32 roundings alone.
  * X bf16 [T][hidden], Y fp32 or bf16 [T][hidden], not overlapping X, ids or weights;
  * hidden and inter multiples of 64 up to 16384, n_experts up to 1024, top_k up to 32
  * (not bounded by n_experts).  Needs a workspace of moe_experts_i8_workspace_bytes.

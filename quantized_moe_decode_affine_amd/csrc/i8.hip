@@ -26,8 +26,6 @@ __device__ __forceinline__ uint16_t i8_bf16(float f) {
   return (uint16_t)(f == f ? f32_to_bf16_bits(f) : 0x7FC0u);
 }
 
-typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
-
 // One wave per row; bound by the row's bytes: 8192 x 4096 in 26-31 us, 100 MB (3.2-3.9 TB/s).
 template <typename In, int kHeld>
 __global__ __launch_bounds__(256) void i8_quantize_kernel(const In* __restrict__ X, int64_t rows, int K,
@@ -50,7 +48,7 @@ hipError_t launch_quantize(const In* X, int64_t rows, int K, int8_t* codes, floa
 }
 
 // ---- tiled product on the i8 matrix cores
-enum { kEpiF32 = 0, kEpiBf16 = 1, kEpiSwiglu = 2, kEpiPartF16 = 3, kEpiPartF32 = 4 };
+enum { kEpiF32 = 0, kEpiBf16 = 1, kEpiSwiglu = 2, kEpiSums = 3 };
 
 struct I8GemmArgs {
   const int8_t* A;         // codes of the rows [.][K]
@@ -65,7 +63,6 @@ struct I8GemmArgs {
   I8Mat S, S2;             // the shared expert's
   int n_slices;            // column slices of a tile
   int64_t tiles_n;         // row tiles
-  float mul;               // kEpiPartF16: power of two that keeps a sum within fp16's range
   void* out;               // [position][N]
 };
 
@@ -308,8 +305,7 @@ __device__ __forceinline__ void i8_tile_body(const I8GemmArgs& p) {
   // from there a column quad of 32 rows would touch 32 cache lines, at a power-of-two
   // distance for most N; so each wave turns 32 rows at a time in LDS and stores whole rows
   // of its columns, 16 bytes a lane.
-  constexpr bool kPartial = EPI == kEpiPartF16 || EPI == kEpiPartF32;
-  constexpr bool kHalf = EPI == kEpiBf16 || EPI == kEpiPartF16;
+  constexpr bool kHalf = EPI == kEpiBf16;
   typedef typename std::conditional<kHalf, uint16_t, float>::type out_t;
   constexpr int kOutF = kSwiglu ? FN / 2 : FN;
   constexpr int kRow = kOutF * 32 * sizeof(out_t), kPitch = kRow + 16;  // the pad spreads the rows over the banks
@@ -324,7 +320,7 @@ __device__ __forceinline__ void i8_tile_body(const I8GemmArgs& p) {
     const int r0 = (wm * FM + fm) * 32;
     if (r0 >= rows) break;
     float sa = 0.f;
-    if constexpr (!kPartial) {
+    if constexpr (EPI != kEpiSums) {
       const int64_t pos = first + min(r0 + m, rows - 1);
       sa = p.sa[p.row_src ? (pos < p.P ? (int64_t)p.row_src[pos] : pos - p.P) : pos];
     }
@@ -342,9 +338,7 @@ __device__ __forceinline__ void i8_tile_body(const I8GemmArgs& p) {
             const float g = d * sa * w.scales[row];
             const float u = (float)acc[fm][fn + FN / 2][4 * q + j] * sa * w2.scales[row];
             o[j] = g / (1.0f + expf(-g)) * u;
-          } else if constexpr (EPI == kEpiPartF16) {
-            o[j] = __builtin_bit_cast(uint16_t, (_Float16)(d * p.mul));
-          } else if constexpr (EPI == kEpiPartF32) {
+          } else if constexpr (EPI == kEpiSums) {
             o[j] = d;
           } else if constexpr (EPI == kEpiBf16) {
             o[j] = i8_bf16(d * sa * w.scales[row]);
@@ -401,13 +395,13 @@ hipError_t launch_tiles(I8GemmArgs p, int64_t tiles, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Bound by the sums' bytes, written just before: 2,048 tokens of 9 slots and 2,048 columns in
-// 24 us, 84 MB beside the channels' scales from the L2.
+// Bound by the sums' bytes, written just before: 151 MB for 2,048 tokens of 9 slots and 2,048
+// columns, beside the channels' scales from the L2.  The sums stay in fp32 (fp16 ones made the
+// layer 261 us instead of 284, and a bf16 output less exact than its 8 bits where slots cancel).
 // y[t] = sum_i w_i (sums of slot i * its row's scale * the channel's scale) + shared, in slot
 // order, the shared expert last; slots whose id names no expert add nothing.
-template <typename Part>
-__global__ __launch_bounds__(256) void i8_combine_kernel(const Part* __restrict__ part, float unit,
-                                                         const float* __restrict__ sh, const int32_t* __restrict__ inv,
+__global__ __launch_bounds__(256) void i8_combine_kernel(const float* __restrict__ part, const float* __restrict__ sh,
+                                                         const int32_t* __restrict__ inv,
                                                          const int32_t* __restrict__ ids,
                                                          const float* __restrict__ weights, int64_t T, int k, int E,
                                                          int H, int64_t P, const float* __restrict__ sw,
@@ -420,19 +414,11 @@ __global__ __launch_bounds__(256) void i8_combine_kernel(const Part* __restrict_
     const int n = (int)(i - t * per) * 8;
     float y[8] = {};
     auto add = [&](int64_t pos, float f, const float* s) {
-      float v[8], c[8];
-      if constexpr (std::is_same<Part, float>::value) {
-        const float4* q = reinterpret_cast<const float4*>(part + pos * H + n);
-        v[0] = q[0].x; v[1] = q[0].y; v[2] = q[0].z; v[3] = q[0].w;
-        v[4] = q[1].x; v[5] = q[1].y; v[6] = q[1].z; v[7] = q[1].w;
-      } else {
-        const half8_t hv = *reinterpret_cast<const half8_t*>(part + pos * H + n);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = (float)hv[j];
-      }
+      float c[8];
+      const float4* q = reinterpret_cast<const float4*>(part + pos * H + n);
+      const float v[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
 #pragma unroll
       for (int j = 0; j < 8; ++j) c[j] = s[n + j];
-      f *= unit;
 #pragma unroll
       for (int j = 0; j < 8; ++j) y[j] += v[j] * f * c[j];
     };
@@ -481,7 +467,7 @@ struct ExpertsWs {
   float* act;            // [R][I] silu(gate) * up of each sorted position
   int8_t* aq;            // [R][I] its codes
   float* sh;             // [R]
-  void* part;            // [R][H] sums of the down product: fp16 or fp32
+  float* part;           // [R][H] sums of the down product
   size_t total;
 };
 
@@ -503,7 +489,7 @@ ExpertsWs carve(void* base, const I8Experts& L, int64_t T, int k) {
   w.act = reinterpret_cast<float*>(take((size_t)R * L.inter * 4));
   w.aq = reinterpret_cast<int8_t*>(take((size_t)R * L.inter));
   w.sh = reinterpret_cast<float*>(take((size_t)R * 4));
-  w.part = take((size_t)R * L.hidden * 4);
+  w.part = reinterpret_cast<float*>(take((size_t)R * L.hidden * 4));
   w.total = off;
   return w;
 }
@@ -607,27 +593,12 @@ hipError_t run_moe_experts_i8(const I8Experts& L, const uint16_t* X, int64_t T, 
   d.W = d.W2 = L.down;
   d.S = d.S2 = L.sh_down;
   d.out = w.part;
-  // The sums of a bf16 output are stored as fp16, half the bytes of the round trip: 11
-  // significant bits of each summand against the output's 8.  A sum is at most
-  // 127 * 128 * I, so one power of two per layer keeps it within fp16's range, and the
-  // smallest sums (an integer times it) far above its subnormals.
-  float unit = 1.0f;
-  while (127.0f * 128.0f * I > 65504.0f * unit) unit *= 2.0f;
-  d.mul = 1.0f / unit;
-  e = out_bf16 ? launch_tiles<2, 4, 2, 2, 3, kEpiPartF16>(d, max_tiles, stream)
-               : launch_tiles<2, 4, 2, 2, 3, kEpiPartF32>(d, max_tiles, stream);
+  e = launch_tiles<2, 4, 2, 2, 3, kEpiSums>(d, max_tiles, stream);
   if (e != hipSuccess) return e;
 
   const unsigned blocks = (unsigned)std::min<int64_t>((T * (H / 8) + 255) / 256, 65536);
-  const float* sws = extra ? L.sh_down.scales : nullptr;
-  if (out_bf16)
-    hipLaunchKernelGGL(i8_combine_kernel<_Float16>, dim3(blocks), dim3(256), 0, stream,
-                       static_cast<const _Float16*>(w.part), unit, w.sh, w.inv, ids, weights, T, k, E, H, P,
-                       L.down.scales, sws, Y, 1);
-  else
-    hipLaunchKernelGGL(i8_combine_kernel<float>, dim3(blocks), dim3(256), 0, stream,
-                       static_cast<const float*>(w.part), 1.0f, w.sh, w.inv, ids, weights, T, k, E, H, P,
-                       L.down.scales, sws, Y, 0);
+  hipLaunchKernelGGL(i8_combine_kernel, dim3(blocks), dim3(256), 0, stream, w.part, w.sh, w.inv, ids, weights, T, k, E, H,
+                     P, L.down.scales, extra ? L.sh_down.scales : nullptr, Y, out_bf16);
   return hipGetLastError();
 }
 

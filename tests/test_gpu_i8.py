@@ -403,3 +403,16 @@ def test_refusals(B):
     with pytest.raises(ValueError):
         B.DeviceI8Experts(ex.matrices[0], ex.matrices[1], ex.matrices[0])
     assert B.moe_experts_i8(ex, x[:0], ids[:0], w[:0]).shape == (0, 64)
+
+
+# ------------------------------------------------------- one result in every form --
+
+@pytest.mark.parametrize("T,E,H,I,k,shared", [(1, 16, 256, 512, 8, True), (9, 8, 192, 128, 4, False), (17, 16, 256, 128, 4, True),
+                                              (129, 3, 128, 128, 1, True), (300, 2, 192, 64, 2, False),
+                                              (70, 12, 1088, 320, 3, True)])
+def test_experts_bf16_is_the_fp32_output_rounded(B, T, E, H, I, k, shared):
+    """Nothing but the output's own rounding comes with a bfloat16 output, few slots or many."""
+    ex = _experts(B, _layer(T + 40, E, H, I, shared))
+    ids, w = _ids(T, T, E, k, 0.1 if T > 1 else 0.0)
+    args = ex, B.bf16_tensor(_rows(T, T, H)), torch.from_numpy(ids).cuda(), torch.from_numpy(w - 0.4).cuda()
+    np.testing.assert_array_equal(bf16_bits(B.moe_experts_i8(*args, B.OUT_BF16)), bf16_bits_of_f32(B.moe_experts_i8(*args)))
