@@ -397,8 +397,8 @@ size_t i8_gemm_workspace_bytes(const q4moe_i8_matrix* W, int64_t m);
  * 8-bit form per token and expert.  A slot whose id lies outside [0, n_experts) adds
  * nothing (a token all of whose slots do gets the shared expert alone, or zeros); an
  * id may stand in several slots of a token.  The slots' products are summed in fp32
- * in slot order, the shared expert last; a bf16 Y is that sum rounded once.  Other
- * tokens of the call move a token's result by fp32 roundings alone.
+ * in slot order, the shared expert last; a bf16 Y is that sum rounded once.  A
+ * token's result is the same bits whatever other tokens the call has.
  * X bf16 [T][hidden], Y fp32 or bf16 [T][hidden], not overlapping X, ids or weights;
  * hidden and inter multiples of 64 up to 16384, n_experts up to 1024, top_k up to 32
  * (not bounded by n_experts).  Needs a workspace of moe_experts_i8_workspace_bytes.

@@ -335,9 +335,9 @@ __device__ __forceinline__ void i8_tile_body(const I8GemmArgs& p) {
           const float d = (float)acc[fm][fn][4 * q + j];
           const int64_t row = e_row + min(c0 + c + j, p.N - 1);
           if constexpr (kSwiglu) {
-            const float g = d * sa * w.scales[row];
-            const float u = (float)acc[fm][fn + FN / 2][4 * q + j] * sa * w2.scales[row];
-            o[j] = g / (1.0f + expf(-g)) * u;
+            const float g = i8_scaled(d, sa, w.scales[row]);
+            const float u = i8_scaled((float)acc[fm][fn + FN / 2][4 * q + j], sa, w2.scales[row]);
+            o[j] = i8_swiglu(g, u);
           } else if constexpr (EPI == kEpiSums) {
             o[j] = d;
           } else if constexpr (EPI == kEpiBf16) {
@@ -398,7 +398,7 @@ hipError_t launch_tiles(I8GemmArgs p, int64_t tiles, hipStream_t stream) {
 // Bound by the sums' bytes, written just before: 151 MB for 2,048 tokens of 9 slots and 2,048
 // columns, beside the channels' scales from the L2.  The sums stay in fp32 (fp16 ones made the
 // layer 261 us instead of 284, and a bf16 output less exact than its 8 bits where slots cancel).
-// y[t] = sum_i w_i (sums of slot i * its row's scale * the channel's scale) + shared, in slot
+// y[t] = sum_i (sums of slot i * its row's scale * the channel's scale) w_i + shared, in slot
 // order, the shared expert last; slots whose id names no expert add nothing.
 __global__ __launch_bounds__(256) void i8_combine_kernel(const float* __restrict__ part, const float* __restrict__ sh,
                                                          const int32_t* __restrict__ inv,
@@ -413,19 +413,19 @@ __global__ __launch_bounds__(256) void i8_combine_kernel(const float* __restrict
     const int64_t t = i / per;
     const int n = (int)(i - t * per) * 8;
     float y[8] = {};
-    auto add = [&](int64_t pos, float f, const float* s) {
+    auto add = [&](int64_t pos, float scale, float f, const float* s) {
       float c[8];
       const float4* q = reinterpret_cast<const float4*>(part + pos * H + n);
       const float v[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
 #pragma unroll
       for (int j = 0; j < 8; ++j) c[j] = s[n + j];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] += v[j] * f * c[j];
+      for (int j = 0; j < 8; ++j) y[j] = i8_add_slot(y[j], i8_scaled(v[j], scale, c[j]), f);
     };
     for (int s0 = 0; s0 < k; s0 += 4) {  // four slots' loads in flight
       int e[4];
       int64_t pos[4];
-      float f[4];
+      float f[4], scale[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int64_t r = t * k + min(s0 + j, k - 1);
@@ -434,12 +434,12 @@ __global__ __launch_bounds__(256) void i8_combine_kernel(const float* __restrict
         f[j] = weights[r];
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) f[j] *= sh[pos[j] < 0 ? 0 : pos[j]];
+      for (int j = 0; j < 4; ++j) scale[j] = sh[pos[j] < 0 ? 0 : pos[j]];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (pos[j] >= 0) add(pos[j], f[j], sw + (int64_t)e[j] * H);
+        if (pos[j] >= 0) add(pos[j], scale[j], f[j], sw + (int64_t)e[j] * H);
     }
-    if (sw_shared) add(P + t, sh[P + t], sw_shared);
+    if (sw_shared) add(P + t, sh[P + t], 1.0f, sw_shared);
     if (out_bf16) {
       uint4 o;
       o.x = (uint32_t)i8_bf16(y[0]) | ((uint32_t)i8_bf16(y[1]) << 16);

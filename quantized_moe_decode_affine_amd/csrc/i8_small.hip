@@ -309,8 +309,7 @@ __global__ __launch_bounds__(kSmallWaves* kWave) void i8_slots_up_kernel(I8Exper
         u += s_sum[o][((col + kUpCols) / 4) * 16 + tok][col % 4];
       }
       const float sx = s_scale[tok];
-      const float gv = (float)g * sx * sg, uv = (float)u * sx * su;
-      act[(int64_t)slot_of(s0 + tok) * I + n0 + col] = gv / (1.0f + expf(-gv)) * uv;
+      act[(int64_t)slot_of(s0 + tok) * I + n0 + col] = i8_swiglu(i8_scaled((float)g, sx, sg), i8_scaled((float)u, sx, su));
     }
   }
 }
@@ -382,9 +381,8 @@ __global__ void i8_slots_down_kernel(I8Experts L, int T, int k, const int32_t* _
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[i] += __shfl(acc[i], lane + 33, kWave);
       }
-      f *= scale;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = (float)acc[i] * f * sw[i];
+      for (int i = 0; i < 4; ++i) v[i] = i8_scaled((float)acc[i], scale, sw[i]) * f;
       __builtin_amdgcn_wave_barrier();  // the image is read before the next slot's replaces it
     }
     if (a == 0 && (lane >> 4) * 4 < kCols)

@@ -100,4 +100,20 @@ __device__ __forceinline__ void i8_quantize_row(const In* x, int K, int8_t* code
   if (lane == 0) *scale_out = scale;
 }
 
+// The experts' arithmetic on exact integer sums, one rounding an operation and in this order
+// wherever it is done (a fused multiply-add in one kernel and not in another would move the
+// last bit): a token gets the same bits whichever kernels its batch takes.
+__device__ __forceinline__ float i8_scaled(float sum, float row_scale, float channel_scale) {
+#pragma clang fp contract(off)
+  return sum * row_scale * channel_scale;
+}
+__device__ __forceinline__ float i8_swiglu(float g, float u) {
+#pragma clang fp contract(off)
+  return g / (1.0f + expf(-g)) * u;
+}
+__device__ __forceinline__ float i8_add_slot(float y, float out, float weight) {
+#pragma clang fp contract(off)
+  return y + out * weight;
+}
+
 }  // namespace q4moe

@@ -416,3 +416,17 @@ def test_experts_bf16_is_the_fp32_output_rounded(B, T, E, H, I, k, shared):
     ids, w = _ids(T, T, E, k, 0.1 if T > 1 else 0.0)
     args = ex, B.bf16_tensor(_rows(T, T, H)), torch.from_numpy(ids).cuda(), torch.from_numpy(w - 0.4).cuda()
     np.testing.assert_array_equal(bf16_bits(B.moe_experts_i8(*args, B.OUT_BF16)), bf16_bits_of_f32(B.moe_experts_i8(*args)))
+
+
+@pytest.mark.parametrize("E,H,I,k,shared", [(8, 256, 512, 4, True), (40, 1088, 320, 6, True), (5, 192, 64, 3, False),
+                                            (300, 128, 1024, 8, True)])
+def test_experts_token_does_not_depend_on_its_batch(B, E, H, I, k, shared):
+    """The same bits alone, among few and among many tokens."""
+    T = 90
+    ex = _experts(B, _layer(E, E, H, I, shared))
+    ids, w = _ids(E, T, E, k, 0.1)
+    X, ids, w = B.bf16_tensor(_rows(E, T, H)), torch.from_numpy(ids).cuda(), torch.from_numpy(w - 0.4).cuda()
+    for out in (B.OUT_F32, B.OUT_BF16):
+        whole = B.moe_experts_i8(ex, X, ids, w, out)
+        for part in (slice(0, 1), slice(7, 8), slice(3, 5), slice(20, 28), slice(40, 56), slice(50, 90)):
+            assert torch.equal(B.moe_experts_i8(ex, X[part], ids[part], w[part], out), whole[part])
