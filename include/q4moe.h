@@ -249,9 +249,10 @@ int moe_route_topk_q8(const q4moe_matrix* router_q8, const q4moe_bf16* X, int64_
  * X bf16 [T][hidden] through rule->router or rule->router_q8 in fp32, as
  * moe_route_topk and moe_route_topk_q8 compute them, then the rule.  Writes ids
  * int32 [T][top_k] and weights fp32 [T][top_k]; T up to 2^26.  Needs Q4MOE_OP_ROUTE_RULE
- * workspace (n_experts; T), zero-filled before its first use and used by moe_route
- * alone: few rows run as one launch whose last workgroups select, by arrival
- * counts in its first 256 bytes that each call leaves at zero again.  Calls that
+ * workspace (n_experts; T), its first 256 bytes zero-filled before its first use and
+ * used by moe_route alone: few rows run as one launch whose last workgroups select, by
+ * arrival counts in these bytes that each call leaves at zero again.  Counts that were
+ * not zero give id -1 and weight NaN in every slot, until they are zeroed.  Calls that
  * share a workspace must not overlap.
  */
 int moe_route(const q4moe_routing* rule, const q4moe_bf16* X, int64_t T, int32_t* ids, float* weights,

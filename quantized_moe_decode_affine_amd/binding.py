@@ -448,10 +448,14 @@ def _out_type(out_dtype: int) -> torch.dtype:
 
 
 def moe_route_workspace(routing: Routing, T: int) -> torch.Tensor:
-    """A workspace for moe_route on up to T rows, zero-filled as its first call needs it."""
-    return workspace(load_library().q4moe_workspace_bytes(
-        OP_ROUTE_RULE, ctypes.byref(q4moe_layer(routing.hidden, 0, routing.n_experts, routing.top_k)), None, T),
-        routing.device)
+    """A workspace for moe_route on up to T rows, its arrival counts (the first 256 bytes) zeroed
+    as the first call needs them.  moe_route on another buffer whose counts are not zero gives id
+    -1 and weight NaN."""
+    nbytes = load_library().q4moe_workspace_bytes(
+        OP_ROUTE_RULE, ctypes.byref(q4moe_layer(routing.hidden, 0, routing.n_experts, routing.top_k)), None, T)
+    ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=routing.device)
+    ws[:256].zero_()
+    return ws
 
 
 def moe_route(routing: Routing, X: torch.Tensor, ids: Optional[torch.Tensor] = None,

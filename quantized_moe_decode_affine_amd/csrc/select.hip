@@ -227,12 +227,26 @@ __global__ __launch_bounds__(kSelWaves * kWave) void select_kernel(RouteRule r, 
     select_row<V, false>(r, logits + t * r.n_experts, s_c[wave], ids + t * r.top_k, weights + t * r.top_k);
 }
 
+// Arrivals are counted in steps of an odd number (2^32 over the golden ratio), which modulo
+// 2^32 has an inverse: a count that started at zero gives its workgroup's place back, and one
+// that started at anything else (a workspace that was not zeroed: small integers, floats, bytes
+// of ones) gives places far beyond the grid in every workgroup, but for a share of grid / 2^32
+// of the values.  That costs one multiplication.
+constexpr uint32_t kArrival = 0x9E3779B1u;
+constexpr uint32_t inverse_u32(uint32_t a) {  // of an odd a: each step doubles the right bits, 3 at first
+  uint32_t x = a;
+  for (int i = 0; i < 4; ++i) x *= 2u - a * x;
+  return x;
+}
+static_assert(kArrival * inverse_u32(kArrival) == 1u, "the inverse modulo 2^32");
+
 // Routing of few tokens in one launch, kSelWaves of them to a group of workgroups: a wave per
 // expert takes its row of the router once for the group's tokens, and the group's last
 // workgroup to finish selects, a wave per token.  The launch is bound by latencies (its
 // bytes, 1 MB at 256 experts of 2,048 columns, take 0.2 us): one launch instead of two saves
 // one of each, 8.2 us against 12.8 for one token (and 4 us of the host's time).  `arrived`,
-// a count per group, is zero before the launch and after it.
+// a count per group, is zero before the launch and after it; where it was not, the group's
+// slots get id -1 and weight NaN.
 template <int V, bool kQ8>
 __global__ __launch_bounds__(kSelWaves * kWave) void route_few_kernel(RouteRule r, const uint16_t* __restrict__ router,
                                                                       Q4Mat q8, int H, const uint16_t* __restrict__ X,
@@ -240,7 +254,7 @@ __global__ __launch_bounds__(kSelWaves * kWave) void route_few_kernel(RouteRule 
                                                                       int32_t* __restrict__ ids,
                                                                       float* __restrict__ weights) {
   __shared__ double s_c[kSelWaves][V * kWave];
-  __shared__ bool s_last;
+  __shared__ uint32_t s_place;
   const int t0 = blockIdx.y * kSelWaves, T = min(kSelWaves, rows - t0);  // this group's tokens
   X += (int64_t)t0 * H;
   logits += (int64_t)t0 * r.n_experts;
@@ -321,12 +335,19 @@ __global__ __launch_bounds__(kSelWaves * kWave) void route_few_kernel(RouteRule 
   wait_vmem();  // this wave's logits are where every workgroup sees them
   __syncthreads();
   if (threadIdx.x == 0) {
-    const unsigned n = __hip_atomic_fetch_add(arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    s_last = n == gridDim.x - 1;
-    if (s_last) __hip_atomic_store(arrived, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const uint32_t count = __hip_atomic_fetch_add(arrived, kArrival, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    s_place = count * inverse_u32(kArrival);
+    if (s_place == gridDim.x - 1) __hip_atomic_store(arrived, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
   __syncthreads();
-  if (!s_last || wave >= T) return;
+  if (s_place >= gridDim.x) {  // the count did not start at zero
+    for (int i = threadIdx.x; i < T * r.top_k; i += blockDim.x) {
+      ids[i] = -1;
+      weights[i] = __uint_as_float(0x7FC00000u);
+    }
+    return;
+  }
+  if (s_place != gridDim.x - 1 || wave >= T) return;
   select_row<V, true>(r, logits + (int64_t)wave * r.n_experts, s_c[wave], ids + wave * r.top_k,
                       weights + wave * r.top_k);
 }

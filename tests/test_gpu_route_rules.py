@@ -216,3 +216,22 @@ def test_captured_route_replays(B, T):
         want = B.moe_route(r, X)
         torch.cuda.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("T", [1, 4, 10])
+@pytest.mark.parametrize("fill", [1, 2, 15, -1, 2 ** 31 - 1, 0x3F800000])
+def test_workspace_that_was_not_zeroed_shows(B, T, fill):
+    """Arrival counts that do not start at zero give id -1 and weight NaN in every slot, call after
+    call, and not the memory that was there; a zeroed head puts it right."""
+    r = B.Routing(B.bf16_tensor(_grid(1, (64, 256), 0.02, 2.0 ** -10, 255)), 6, score="sigmoid")
+    X = B.bf16_tensor(_grid(2, (T, 256), 1.0, 2.0 ** -3, 40))
+    want = B.moe_route(r, X)
+    ws = B.moe_route_workspace(r, T)
+    ws.view(torch.int32).fill_(fill)
+    ids, w = torch.full_like(want[0], 7), torch.full_like(want[1], 7.0)
+    for _ in range(3):
+        B.moe_route(r, X, ids=ids, weights=w, ws=ws)
+        assert (ids == -1).all() and torch.isnan(w).all()
+    ws[:256].zero_()
+    B.moe_route(r, X, ids=ids, weights=w, ws=ws)
+    assert torch.equal(ids, want[0]) and torch.equal(w, want[1])
