@@ -246,14 +246,16 @@ int moe_route_topk_q8(const q4moe_matrix* router_q8, const q4moe_bf16* X, int64_
 
 /*
  * moe_route_topk with a routing rule (see q4moe_routing): logits of the rows
- * X bf16 [T][hidden] through rule->router or rule->router_q8 in fp32, as
- * moe_route_topk and moe_route_topk_q8 compute them, then the rule.  Writes ids
- * int32 [T][top_k] and weights fp32 [T][top_k]; T up to 2^26.  Needs Q4MOE_OP_ROUTE_RULE
- * workspace (n_experts; T), its first 256 bytes zero-filled before its first use and
- * used by moe_route alone: few rows run as one launch whose last workgroups select, by
- * arrival counts in these bytes that each call leaves at zero again.  Counts that were
- * not zero give id -1 and weight NaN in every slot, until they are zeroed.  Calls that
- * share a workspace must not overlap.
+ * X bf16 [T][hidden] through rule->router or rule->router_q8 in fp32, then the rule.
+ * Rows of one call are summed alike, but few rows (T up to 64) in another order than
+ * more, and than moe_route_topk sums them: where choices lie within such a sum's
+ * rounding of each other, another T or the other call may choose another expert.
+ * Writes ids int32 [T][top_k] and weights fp32 [T][top_k]; T up to 2^26.  Needs
+ * Q4MOE_OP_ROUTE_RULE workspace (n_experts; T), its first 256 bytes zero-filled before
+ * its first use and used by moe_route alone: few rows run as one launch whose last
+ * workgroups select, by arrival counts in these bytes that each call leaves at zero
+ * again.  Counts that were not zero give id -1 and weight NaN in every slot, until they
+ * are zeroed.  Calls that share a workspace must not overlap.
  */
 int moe_route(const q4moe_routing* rule, const q4moe_bf16* X, int64_t T, int32_t* ids, float* weights,
               void* workspace, size_t workspace_bytes, q4moe_stream stream);

@@ -235,3 +235,62 @@ def test_workspace_that_was_not_zeroed_shows(B, T, fill):
     ws[:256].zero_()
     B.moe_route(r, X, ids=ids, weights=w, ws=ws)
     assert torch.equal(ids, want[0]) and torch.equal(w, want[1])
+
+
+def _check_near(ids, w, logits, delta, rule, bias=None):
+    """Ids and weights of logits that are each within `delta` [T][E] of these: every id is chosen as
+    the rule would for some such logits, and every weight is what it would give them."""
+    T, E = logits.shape
+    b = np.zeros(E) if bias is None else bias.astype(np.float64)
+    if rule["score"] == "sigmoid":
+        s, slope = 1.0 / (1.0 + np.exp(-logits)), 0.25
+    else:
+        s = np.exp(logits - logits.max(1, keepdims=True))
+        s, slope = s / s.sum(1, keepdims=True), None
+    for t in range(T):
+        d = delta[t].max()
+        # a sigmoid's slope is 1/4 at most; a softmax score moves by a factor of exp(2 d) at most
+        eps = d * slope if slope else np.expm1(2 * d) * s[t].max()
+        c, chosen = s[t] + b, ids[t]
+        assert len(set(chosen)) == len(chosen) and chosen.min() >= 0 and chosen.max() < E
+        left = np.delete(c, chosen)
+        assert (c[chosen][:-1] >= c[chosen][1:] - 2 * eps).all()
+        assert left.size == 0 or c[chosen].min() >= left.max() - 2 * eps
+        want = s[t][chosen]
+        if rule["renormalise"]:
+            want = want / want.sum()
+        # a score, or its share of the chosen ones' sum, moves by a factor of exp(2 d) at most; the
+        # weight is rounded once
+        bound = want * rule["scale"] * (np.expm1(2 * d) + 2.0 ** -24 * (1 + 2 * d))
+        assert (np.abs(w[t] - want * rule["scale"]) <= bound * (1 + 1e-9)).all()
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("E,H,k", [(256, 2048, 8), (60, 1088, 6), (512, 320, 10)])
+def test_route_of_ordinary_values(B, E, H, k, q8):
+    """Values whose fp32 sums are rounded, through every form of the logits: a row's ids and weights
+    belong to logits within the rounding of the exact ones, in whatever order they are summed."""
+    X = synth.to_bf16_bits(np.random.default_rng(H).standard_normal((1500, H)).astype(np.float32))
+    x = qorc.bf16_to_f64(X)
+    if q8:
+        mat = synth.q8_matrix(71, 0, synth.ROUTER_STREAM, 0, E, H, scale_std=0.02 / 74)
+        router, logits = B.DeviceQ4(*mat), qorc.q4_gemm(*mat, X)
+        s, b = (np.repeat(np.abs(qorc.bf16_to_f64(v)), 64, axis=1) for v in mat[1:])
+        size = np.abs(x) @ (s * mat[0].view(np.uint8).reshape(E, H) + b).T   # of sum(x q) scale and of sum(x) bias
+    else:
+        R = synth.to_bf16_bits((np.random.default_rng(E).standard_normal((E, H)) * 0.02).astype(np.float32))
+        router, logits = B.bf16_tensor(R), qorc.router_logits(R, X)
+        size = np.abs(x) @ np.abs(qorc.bf16_to_f64(R)).T
+    # products of two bfloat16 values (or of one and a code) are exact in fp32; a sum of H of them in any order
+    # takes at most H roundings on a value's way, a folded group 2 more, each half a step, 2^-24, or a whole
+    # one where a matrix core truncates
+    delta = size * (H + 2 * (H // 64)) * 2.0 ** -23
+    bias = (np.random.default_rng(k).standard_normal(E) * 0.05).astype(np.float32)
+    for rule in (dict(top_k=k, score="sigmoid", renormalise=True, scale=2.5), dict(top_k=k, score="softmax", renormalise=True, scale=1.0),
+                 dict(top_k=k, score="softmax", renormalise=False, scale=1.0)):
+        for T in (1, 3, 20, 21, 64, 300, 1500):
+            for b in (None, bias):
+                r = B.Routing(router, bias=None if b is None else torch.from_numpy(b).cuda(), **rule)
+                ids, w = B.moe_route(r, B.bf16_tensor(X[:T]))
+                some = slice(None) if T <= 64 else slice(T % 29, None, 29)
+                _check_near(ids[some].cpu().numpy(), w[some].double().cpu().numpy(), logits[:T][some], delta[:T][some], rule, b)
