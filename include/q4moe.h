@@ -250,7 +250,8 @@ int moe_route_topk_q8(const q4moe_matrix* router_q8, const q4moe_bf16* X, int64_
  * Rows of one call are summed alike, but few rows (T up to 64) in another order than
  * more, and than moe_route_topk sums them: where choices lie within such a sum's
  * rounding of each other, another T or the other call may choose another expert.
- * Writes ids int32 [T][top_k] and weights fp32 [T][top_k]; T up to 2^26.  Needs
+ * Writes ids int32 [T][top_k] and weights fp32 [T][top_k], which overlap neither X nor
+ * each other nor the workspace (Q4MOE_EINVAL); T up to 2^26.  Needs
  * Q4MOE_OP_ROUTE_RULE workspace (n_experts; T), its first 256 bytes zero-filled before
  * its first use and used by moe_route alone: few rows run as one launch whose last
  * workgroups select, by arrival counts in these bytes that each call leaves at zero
@@ -262,7 +263,8 @@ int moe_route(const q4moe_routing* rule, const q4moe_bf16* X, int64_t T, int32_t
 
 /*
  * The rule alone, on logits fp32 [T][n_experts] that the caller has; rule->hidden,
- * router and router_q8 are not read.  No workspace.
+ * router and router_q8 are not read.  ids and weights overlap neither the logits nor
+ * each other (Q4MOE_EINVAL).  No workspace.
  */
 int moe_route_logits(const q4moe_routing* rule, const float* logits, int64_t T, int32_t* ids, float* weights,
                      q4moe_stream stream);
@@ -382,7 +384,7 @@ int i8_quantize(const q4moe_bf16* X, int64_t rows, int64_t k, int8_t* codes, flo
  * product in 8-bit integers next to q4_gemm's fp16 one: the integer sum is exact
  * (int32) and is rounded where it becomes fp32, at each scale, and to Y's type.
  * Y fp32 or bf16 [m][count*n], not overlapping X; k up to 65536.  Needs a workspace
- * of i8_gemm_workspace_bytes.
+ * of i8_gemm_workspace_bytes, which overlaps neither.
  */
 int i8_gemm(const q4moe_i8_matrix* W, const q4moe_bf16* X, int64_t m, void* Y, int out_dtype,
             void* workspace, size_t workspace_bytes, q4moe_stream stream);
@@ -404,7 +406,8 @@ size_t i8_gemm_workspace_bytes(const q4moe_i8_matrix* W, int64_t m);
  * token's result is the same bits whatever other tokens the call has.
  * X bf16 [T][hidden], Y fp32 or bf16 [T][hidden], not overlapping X, ids or weights;
  * hidden and inter multiples of 64 up to 16384, n_experts up to 1024, top_k up to 32
- * (not bounded by n_experts).  Needs a workspace of moe_experts_i8_workspace_bytes.
+ * (not bounded by n_experts).  Needs a workspace of moe_experts_i8_workspace_bytes that
+ * overlaps none of them.
  */
 int moe_experts_i8(const q4moe_i8_experts* experts, const q4moe_bf16* X, int64_t T, const int32_t* ids,
                    const float* weights, int32_t top_k, void* Y, int out_dtype, void* workspace,

@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 #include <new>
 
 namespace q4moe {
@@ -111,6 +112,22 @@ size_t lmhead_ws(int64_t rows, int64_t k, int64_t B) {
 bool overlap(const void* a, size_t an, const void* b, size_t bn) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + bn && y < x + an;
+}
+
+// A call's buffer and its size.
+struct Span {
+  const void* at;
+  size_t bytes;
+};
+// One of `written` shares a byte with another of them or with one of `read`.
+bool clash(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+  for (const Span* w = written.begin(); w != written.end(); ++w) {
+    for (const Span* o = written.begin(); o != w; ++o)
+      if (overlap(w->at, w->bytes, o->at, o->bytes)) return true;
+    for (const Span& r : read)
+      if (overlap(w->at, w->bytes, r.at, r.bytes)) return true;
+  }
+  return false;
 }
 
 // The rule of a routing descriptor (everything but its router).
@@ -454,8 +471,9 @@ int moe_route(const q4moe_routing* rule, const q4moe_bf16* X, int64_t T, int32_t
     // (2^26 rows: the grid of the logits)
     if (rule->hidden > kMaxGemvK || T > (1 << 26) || T * r.top_k > kMaxRows32) return Q4MOE_EUNSUPPORTED;
     if (T == 0) return Q4MOE_OK;
-    if (!workspace || workspace_bytes < q4moe::route_rule_workspace_bytes(T, r.n_experts) || !aligned(workspace, 256))
-      return Q4MOE_EWORKSPACE;
+    const size_t need = q4moe::route_rule_workspace_bytes(T, r.n_experts), sb = (size_t)T * r.top_k * 4;
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return Q4MOE_EWORKSPACE;
+    if (clash({{ids, sb}, {weights, sb}, {workspace, need}}, {{X, (size_t)T * rule->hidden * 2}})) return Q4MOE_EINVAL;
     const Q4Mat m = q8 ? to_mat(rule->router_q8) : Q4Mat{nullptr, nullptr, nullptr};
     return hip_status(q4moe::run_route(r, rule->router, &m, rule->hidden, X, T, ids, weights, workspace,
                                        (hipStream_t)stream));
@@ -474,6 +492,8 @@ int moe_route_logits(const q4moe_routing* rule, const float* logits, int64_t T, 
       return Q4MOE_EINVAL;
     if (T > kMaxRows32 || T * r.top_k > kMaxRows32) return Q4MOE_EUNSUPPORTED;
     if (T == 0) return Q4MOE_OK;
+    const size_t sb = (size_t)T * r.top_k * 4;
+    if (clash({{ids, sb}, {weights, sb}}, {{logits, (size_t)T * r.n_experts * 4}})) return Q4MOE_EINVAL;
     return hip_status(q4moe::run_select(r, logits, T, ids, weights, (hipStream_t)stream));
   } catch (...) {
     return Q4MOE_EHIP;
@@ -488,7 +508,7 @@ int i8_quantize(const q4moe_bf16* X, int64_t rows, int64_t k, int8_t* codes, flo
     if (k > kMaxI8K || rows > kMaxRows32) return Q4MOE_EUNSUPPORTED;
     if (rows == 0) return Q4MOE_OK;
     const size_t n = (size_t)rows * k, s = (size_t)rows * 4;
-    if (overlap(codes, n, X, 2 * n) || overlap(scales, s, X, 2 * n) || overlap(scales, s, codes, n)) return Q4MOE_EINVAL;
+    if (clash({{codes, n}, {scales, s}}, {{X, 2 * n}})) return Q4MOE_EINVAL;
     return hip_status(q4moe::run_i8_quantize(X, rows, (int)k, codes, scales, (hipStream_t)stream));
   } catch (...) {
     return Q4MOE_EHIP;
@@ -507,9 +527,11 @@ int i8_gemm(const q4moe_i8_matrix* W, const q4moe_bf16* X, int64_t m, void* Y, i
     if (!X || !aligned(X, 16) || !out_ok(Y, out_dtype)) return Q4MOE_EINVAL;
     if (m == 0) return Q4MOE_OK;
     const int64_t n = W->count * W->n;
-    if (overlap(Y, (size_t)m * n * (out_dtype == Q4MOE_OUT_F32 ? 4 : 2), X, (size_t)m * W->k * 2)) return Q4MOE_EINVAL;
-    if (!workspace || workspace_bytes < q4moe::i8_gemm_workspace_bytes(m, (int)W->k) || !aligned(workspace, 256))
-      return Q4MOE_EWORKSPACE;
+    const Span y{Y, (size_t)m * n * (out_dtype == Q4MOE_OUT_F32 ? 4 : 2)}, x{X, (size_t)m * W->k * 2};
+    if (clash({y}, {x})) return Q4MOE_EINVAL;
+    const size_t need = q4moe::i8_gemm_workspace_bytes(m, (int)W->k);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return Q4MOE_EWORKSPACE;
+    if (clash({{workspace, need}}, {x, y})) return Q4MOE_EINVAL;
     return hip_status(q4moe::run_i8_gemm(q4moe::I8Mat{W->codes, W->scales}, n, (int)W->k, X, m, Y,
                                          out_dtype == Q4MOE_OUT_BF16, workspace, (hipStream_t)stream));
   } catch (...) {
@@ -532,11 +554,12 @@ int moe_experts_i8(const q4moe_i8_experts* experts, const q4moe_bf16* X, int64_t
     if (!X || !aligned(X, 16) || !ids || !aligned(ids, 4) || !weights || !aligned(weights, 4) || !out_ok(Y, out_dtype))
       return Q4MOE_EINVAL;
     if (T == 0) return Q4MOE_OK;
-    const size_t yb = (size_t)T * d.hidden * (out_dtype == Q4MOE_OUT_F32 ? 4 : 2), sb = (size_t)T * top_k * 4;
-    if (overlap(Y, yb, X, (size_t)T * d.hidden * 2) || overlap(Y, yb, ids, sb) || overlap(Y, yb, weights, sb))
-      return Q4MOE_EINVAL;
-    if (!workspace || workspace_bytes < q4moe::experts_i8_workspace_bytes(d, T, top_k) || !aligned(workspace, 256))
-      return Q4MOE_EWORKSPACE;
+    const Span y{Y, (size_t)T * d.hidden * (out_dtype == Q4MOE_OUT_F32 ? 4 : 2)}, x{X, (size_t)T * d.hidden * 2};
+    const Span i{ids, (size_t)T * top_k * 4}, w{weights, (size_t)T * top_k * 4};
+    if (clash({y}, {x, i, w})) return Q4MOE_EINVAL;
+    const size_t need = q4moe::experts_i8_workspace_bytes(d, T, top_k);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return Q4MOE_EWORKSPACE;
+    if (clash({{workspace, need}}, {x, i, w, y})) return Q4MOE_EINVAL;
     return hip_status(q4moe::run_moe_experts_i8(d, X, T, ids, weights, top_k, Y, out_dtype == Q4MOE_OUT_BF16,
                                                 workspace, (hipStream_t)stream));
   } catch (...) {

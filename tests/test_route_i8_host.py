@@ -186,3 +186,27 @@ def test_structs_match_header(tmp_path):
         assert got[(cname, "size")] == ctypes.sizeof(cls), cname
         for field, _ in cls._fields_:
             assert got[(cname, field)] == getattr(cls, field).offset, (cname, field)
+
+
+def test_outputs_over_inputs_are_refused(lib):
+    """Outputs and workspaces that share bytes with each other or with an input."""
+    r, f, g, T = _rule(), lib.moe_route, lib.moe_route_logits, 10
+    need = lib.q4moe_workspace_bytes(B.OP_ROUTE_RULE, ctypes.byref(B.q4moe_layer(128, 0, 64, 4)), None, T)
+    X, ids, w, ws = A, A + 0x100000, A + 0x200000, A + 0x300000
+    x_bytes, s_bytes = T * 128 * 2, T * 4 * 4
+    for bad in ((X, X, w, ws), (X, ids, X + x_bytes - 4, ws), (X, ids, ids, ws), (X, ids, ids + s_bytes - 4, ws),
+                (X, ws + 512, w, ws), (X, ids, ws, ws), (ws + 256, ids, w, ws)):
+        assert f(r, bad[0], T, bad[1], bad[2], bad[3], need, None) == B.EINVAL, bad
+    l_bytes = T * 64 * 4
+    for bad in ((X, X, w), (X, ids, X), (X, ids, X + l_bytes - 4), (X, X - s_bytes + 4, w), (X, ids, ids)):
+        assert g(r, bad[0], T, bad[1], bad[2], None) == B.EINVAL, bad
+    W = ctypes.byref(_mat())
+    need = lib.i8_gemm_workspace_bytes(W, 100)
+    Y = A + 0x100000
+    for over in (A, A + 256 * 99, Y, Y + 256 * 99):
+        assert lib.i8_gemm(W, A, 100, Y, 0, over, need, None) == B.EINVAL
+    ex = ctypes.byref(_experts())
+    need = lib.moe_experts_i8_workspace_bytes(ex, T, 2)
+    Y, ids, w = A + 0x1000000, A + 0x2000000, A + 0x3000000
+    for over in (A, Y, ids, w):
+        assert lib.moe_experts_i8(ex, A, T, ids, w, 2, Y, 0, over, need, None) == B.EINVAL
