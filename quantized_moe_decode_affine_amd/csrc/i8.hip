@@ -12,6 +12,7 @@
 #include <type_traits>
 #include <utility>
 
+#include "i8_tiles.h"
 #include "int8.h"
 #include "kernels.h"
 
@@ -67,7 +68,6 @@ struct I8GemmArgs {
 };
 
 constexpr int kStepBytes = 128;  // columns of a K step, one cache line of every operand row
-constexpr int kXcds = 8;
 // Tile rows of a band: the 32 workgroups that an XCD runs at a time then cover 4 x 8 tiles.
 constexpr int kBand = 4;
 
@@ -379,8 +379,6 @@ __global__ __launch_bounds__(WM* WN* kWave) void i8_tile_kernel(I8GemmArgs p) {
   i8_tile_body<WM, WN, FM, FN, kStages, EPI>(p);
 }
 
-constexpr int64_t kMaxThreads = 0xFFFFFFFFll;  // of a grid
-
 template <int WM, int WN, int FM, int FN, int kStages, int EPI>
 hipError_t launch_tiles(I8GemmArgs p, int64_t tiles, hipStream_t stream) {
   constexpr int kCols = WN * FN * 32 / (EPI == kEpiSwiglu ? 2 : 1);
@@ -517,22 +515,11 @@ hipError_t run_i8_gemm(const I8Mat& W, int64_t n, int K, const uint16_t* X, int6
   p.N = (int)n;
   p.W = p.W2 = p.S = p.S2 = W;
   p.out = Y;
-  // The tile by the time that its rounds of workgroups take, in microseconds per 128 columns
-  // of K (measured on 8192 x 8192 x 4096): 256 x 256, one workgroup on a compute unit, 1.95;
-  // 128 x 128, two, 1.14; 64 x 64, three, 0.63.  The large tile moves the fewest bytes (that
-  // product takes 250, 292 and 430 us), a small one spreads few rows over the chip: 512 rows
-  // on 2048 x 2048 take 32, 21 and 13 us with it.
-  const int64_t cus = device_cu_count();
-  auto rounds = [&](int64_t t, int64_t at_once) {
-    const int64_t blocks = (m + t - 1) / t * ((n + t - 1) / t);
-    if (t < 256 && (blocks + kXcds) * 256 > kMaxThreads) return 1e30;  // more than a grid holds
-    return (double)((blocks + cus * at_once - 1) / (cus * at_once));
-  };
-  const double large = rounds(256, 1) * 1.95, middle = rounds(128, 2) * 1.14, small = rounds(64, 3) * 0.63;
-  if (large <= middle && large <= small)
+  const int tile = i8_dense_tile(m, n, device_cu_count());
+  if (tile == 256)
     return out_bf16 ? launch_tiles<2, 4, 4, 2, 2, kEpiBf16>(p, (m + 255) / 256, stream)
                     : launch_tiles<2, 4, 4, 2, 2, kEpiF32>(p, (m + 255) / 256, stream);
-  if (middle <= small)
+  if (tile == 128)
     return out_bf16 ? launch_tiles<2, 2, 2, 2, 2, kEpiBf16>(p, (m + 127) / 128, stream)
                     : launch_tiles<2, 2, 2, 2, 2, kEpiF32>(p, (m + 127) / 128, stream);
   return out_bf16 ? launch_tiles<2, 2, 1, 1, 3, kEpiBf16>(p, (m + 63) / 64, stream)

@@ -430,3 +430,54 @@ def test_experts_token_does_not_depend_on_its_batch(B, E, H, I, k, shared):
         whole = B.moe_experts_i8(ex, X, ids, w, out)
         for part in (slice(0, 1), slice(7, 8), slice(3, 5), slice(20, 28), slice(40, 56), slice(50, 90)):
             assert torch.equal(B.moe_experts_i8(ex, X[part], ids[part], w[part], out), whole[part])
+
+
+# ------------------------------------------------------------ loops and large tiles --
+
+@pytest.mark.parametrize("m,n,k", [(4090, 4093, 448), (4096, 4096, 64), (3850, 4090, 1088), (3900, 4100, 1088)])
+def test_gemm_large_tiles(B, m, n, k):
+    """Tiles of 256 x 256 with whole and ragged edges, and the 128 x 128 ones (the last shape) over
+    more steps of K than a tile has stages (tests/test_route_i8_host.py has each shape's tile)."""
+    W, X = _weights(m + n, n, k), _rows(k + m, m, k)
+    d, x = _dev(B, W), B.bf16_tensor(X)
+    _check_gemm(B, W, X, B.i8_gemm(d, x), B.i8_gemm(d, x, B.OUT_BF16))
+
+
+@pytest.mark.parametrize("T,E,H,I,k,shared", [(70, 12, 1088, 320, 3, True), (40, 16, 2048, 512, 4, True), (150, 6, 832, 192, 2, False),
+                                              (300, 2, 1088, 1088, 2, True)])
+def test_experts_grouped_long_rows(B, T, E, H, I, k, shared):
+    """More slots than the few-slots form takes, over more steps of K than the tiles have stages."""
+    assert T * k > 64
+    _check_experts(B, _layer(T + E, E, H, I, shared), _rows(T, T, H), *_ids(T, T, E, k, 0.1))
+
+
+@pytest.mark.parametrize("full", [16, 17, 33, 64])
+def test_experts_many_slots_of_one(B, full):
+    """16 tokens, `full` of their 64 slots on one expert: up to four passes of 16 over its rows."""
+    layer = _layer(13, 6, 192, 128, True)
+    ids, w = _ids(14, 16, 5, 4)
+    flat = ids.reshape(-1)
+    flat[np.random.default_rng(full).permutation(64)[:full]] = 5
+    _check_experts(B, layer, _rows(15, 16, 192), ids, w - 0.5)
+
+
+@pytest.mark.parametrize("T,E,H,I,k", [(1, 40, 256, 128, 32), (2, 40, 192, 320, 32), (1, 40, 128, 512, 32), (1, 10, 128, 8192, 9),
+                                       (2, 8, 64, 16384, 8), (1, 8, 64, 16384, 8)])
+def test_experts_more_slots_than_waves(B, T, E, H, I, k):
+    """A wave of the down product takes several slots: more than 16 of them, or activations so long
+    that fewer waves fit a workgroup."""
+    _check_experts(B, _layer(T + I, E, H, I, True), _rows(T, T, H), *_ids(T, T, E, k))
+
+
+def test_experts_gathered_rows_past_2gb(B):
+    """Offsets of the tokens' codes between 2^31 and 2^32."""
+    T, E, H, I = 135_001, 3, 16384, 64
+    layer = _layer(17, E, H, I, False)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    X = torch.randn(T, H, generator=gen, device="cuda", dtype=torch.bfloat16)
+    ids = torch.randint(-1, E, (T, 1), generator=gen, device="cuda", dtype=torch.int32)
+    w = torch.rand(T, 1, generator=gen, device="cuda")
+    y = B.moe_experts_i8(_experts(B, layer), X, ids, w)
+    some = torch.cat([torch.arange(0, 9), torch.arange(131_067, 131_076), torch.arange(T - 9, T)]).cuda()
+    ref, slack, _ = orc.experts_i8(*layer[:3], bf16_bits(X[some]), ids[some].cpu().numpy(), w[some].cpu().numpy())
+    assert (np.abs(to_f64(y[some]) - ref) <= slack).all()

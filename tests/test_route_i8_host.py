@@ -210,3 +210,31 @@ def test_outputs_over_inputs_are_refused(lib):
     Y, ids, w = A + 0x1000000, A + 0x2000000, A + 0x3000000
     for over in (A, Y, ids, w):
         assert lib.moe_experts_i8(ex, A, T, ids, w, 2, Y, 0, over, need, None) == B.EINVAL
+
+
+def test_dense_tiles_of_the_tested_shapes(tmp_path):
+    """Which tile the rule gives each shape of the GPU tests on 256 compute units: all three are met,
+    the large ones by several shapes."""
+    import shutil
+    import subprocess
+
+    import tests.test_gpu_i8 as gpu
+
+    cc = shutil.which("g++") or shutil.which("c++")
+    if cc is None:
+        pytest.skip("no C++ compiler")
+
+    def shapes(test):
+        return [v for mark in test.pytestmark if mark.name == "parametrize" for v in mark.args[1]]
+
+    large = shapes(gpu.test_gemm_large_tiles)
+    asked = large + [(m, n, k) for m, n, k in shapes(gpu.test_gemm_parity) if m > 16] + [(8192, 8192, 4096), (512, 2048, 2048)]
+    src = tmp_path / "tiles.cpp"
+    src.write_text('#include <cstdio>\n#include "i8_tiles.h"\nint main() {\n'
+                   + "\n".join(f'printf("%d\\n", q4moe::i8_dense_tile({m}, {n}, 256));' for m, n, _ in asked) + "\nreturn 0;\n}\n")
+    exe = tmp_path / "tiles"
+    subprocess.run([cc, "-std=c++17", "-I", os.path.join(ROOT, "quantized_moe_decode_affine_amd", "csrc"), str(src), "-o", str(exe)],
+                   check=True)
+    tiles = [int(line) for line in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()]
+    assert tiles[:len(large)] == [256, 256, 256, 128]
+    assert set(tiles[len(large):-2]) == {64, 128} and tiles[-2:] == [256, 64]
