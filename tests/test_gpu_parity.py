@@ -683,3 +683,13 @@ def test_prefill_q8_shared_expert(B, T, H, I, E, k, rbits, gated):
     err, worst = _prefill_check(B, layer, dl, X)
     assert err <= REL_L2_TOL, err
     assert worst <= 2 * REL_L2_TOL
+
+
+def test_prefill_q8_router_more_rows(B):
+    """A chunk whose router runs more workgroups than there are compute units."""
+    T, H, I, E, k = 2080, 576, 64, 256, 4
+    say(f"prefill q8 router T={T} H={H} E={E} k={k}")
+    layer = synth.moe_layer(101, 0, H, I, E, k, router_bits=8)
+    err, worst = _prefill_check(B, layer, B.DeviceLayer(layer), synth.token_rows(101, T, H))
+    assert err <= REL_L2_TOL, err
+    assert worst <= 2 * REL_L2_TOL

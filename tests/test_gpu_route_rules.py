@@ -294,3 +294,25 @@ def test_route_of_ordinary_values(B, E, H, k, q8):
                 ids, w = B.moe_route(r, B.bf16_tensor(X[:T]))
                 some = slice(None) if T <= 64 else slice(T % 29, None, 29)
                 _check_near(ids[some].cpu().numpy(), w[some].double().cpu().numpy(), logits[:T][some], delta[:T][some], rule, b)
+
+
+@pytest.mark.parametrize("T,E,H,k", [(1111, 512, 2048, 8), (1111, 512, 1088, 10), (1111, 512, 576, 7), (2080, 256, 2048, 8),
+                                     (2080, 256, 768, 8)])
+def test_q8_router_over_many_rounds(B, T, E, H, k):
+    """The 8-bit router on a grid of more workgroups than compute units, over enough steps of K that
+    its two stages are refilled: eight, five (of unequal quarters) and three."""
+    rng = np.random.default_rng(E + T + H)
+    codes = rng.integers(0, 256, (E, H), dtype=np.uint8).view(np.uint32)
+    sc = synth.to_bf16_bits((2.0 ** -12 * rng.integers(1, 4, (E, H // 64))).astype(np.float32))
+    bi = synth.to_bf16_bits((-(2.0 ** -5) * rng.integers(1, 4, (E, H // 64))).astype(np.float32))
+    X = _grid(T, (T, H), 0.25, 2.0 ** -3, 4)
+    rule = dict(top_k=k, score="sigmoid")
+    d = B.DeviceQ4(codes, sc, bi)
+    some = slice(T % 23, None, 23)
+    logits = qorc.q4_gemm(codes, sc, bi, X[some])
+    ids, w = B.moe_route(B.Routing(d, **rule), B.bf16_tensor(X))
+    _check(ids[some], w[some], *orc.route_rule(logits, **rule))
+    ids, w = B.moe_route_topk_q8(d, B.bf16_tensor(X), k)
+    ref_ids, ref_w = orc.route_rule(logits, k)
+    np.testing.assert_array_equal(ids[some].cpu().numpy(), ref_ids)
+    np.testing.assert_allclose(w[some].cpu().numpy(), ref_w, rtol=1e-4, atol=1e-6)
