@@ -22,11 +22,6 @@ namespace {
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
-// fp32 -> bf16 bits, nearest even; a NaN stays a NaN (the bare carry could turn it into 0 or infinity).
-__device__ __forceinline__ uint16_t i8_bf16(float f) {
-  return (uint16_t)(f == f ? f32_to_bf16_bits(f) : 0x7FC0u);
-}
-
 // One wave per row; bound by the row's bytes: 8192 x 4096 in 26-31 us, 100 MB (3.2-3.9 TB/s).
 template <typename In, int kHeld>
 __global__ __launch_bounds__(256) void i8_quantize_kernel(const In* __restrict__ X, int64_t rows, int K,

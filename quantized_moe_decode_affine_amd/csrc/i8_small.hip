@@ -17,8 +17,6 @@ namespace q4moe {
 
 namespace {
 
-__device__ __forceinline__ uint16_t small_bf16(float f) { return (uint16_t)(f == f ? f32_to_bf16_bits(f) : 0x7FC0u); }
-
 constexpr int kSmallWaves = 4;
 constexpr int kBatch = 8;                 // weight loads in flight per wave and matrix: 512 columns
 constexpr int kBatchCols = kBatch * 64;
@@ -181,7 +179,7 @@ __global__ __launch_bounds__(kSmallWaves* kWave) void i8_few_rows_kernel(I8Mat W
       for (int i = 0; i < 4; ++i) {
         if (r0 + i >= n) break;
         const float y = (float)acc[i] * sx * W.scales[r0 + i];
-        if constexpr (kBf16) static_cast<uint16_t*>(Y)[t * n + r0 + i] = small_bf16(y);
+        if constexpr (kBf16) static_cast<uint16_t*>(Y)[t * n + r0 + i] = i8_bf16(y);
         else static_cast<float*>(Y)[t * n + r0 + i] = y;
       }
     }
@@ -201,8 +199,8 @@ hipError_t run_i8_few_rows(const I8Mat& W, int64_t n, int K, const uint16_t* X, 
                            hipStream_t stream) {
   const size_t lds = image_bytes(m, K);
   const int64_t blocks = (n + 15) / 16;
-    const int64_t resident = 4 * (int64_t)device_cu_count();
-  const bool split = blocks <= 4 * (int64_t)device_cu_count();
+  const int64_t resident = 4 * (int64_t)device_cu_count();
+  const bool split = blocks <= resident;
   const dim3 grid((unsigned)(split ? blocks : std::min<int64_t>(resident, (blocks + kSmallWaves - 1) / kSmallWaves)));
   const dim3 threads(kSmallWaves * kWave);
   if (split && out_bf16)
@@ -393,7 +391,7 @@ __global__ void i8_slots_down_kernel(I8Experts L, int T, int k, const int32_t* _
     float y = 0.f;
     for (int s = 0; s < slots; ++s) y += s_part[s * kCols + threadIdx.x];
     const int64_t at = (int64_t)t * H + n0 + threadIdx.x;
-    if (out_bf16) static_cast<uint16_t*>(Y)[at] = small_bf16(y);
+    if (out_bf16) static_cast<uint16_t*>(Y)[at] = i8_bf16(y);
     else static_cast<float*>(Y)[at] = y;
   }
 }

@@ -100,6 +100,11 @@ __device__ __forceinline__ void i8_quantize_row(const In* x, int K, int8_t* code
   if (lane == 0) *scale_out = scale;
 }
 
+// fp32 -> bf16 bits, nearest even; a NaN stays a NaN (the bare carry could turn it into 0 or infinity).
+__device__ __forceinline__ uint16_t i8_bf16(float f) {
+  return (uint16_t)(f == f ? f32_to_bf16_bits(f) : 0x7FC0u);
+}
+
 // The experts' arithmetic on exact integer sums, one rounding an operation and in this order
 // wherever it is done (a fused multiply-add in one kernel and not in another would move the
 // last bit): a token gets the same bits whichever kernels its batch takes.
