@@ -144,7 +144,9 @@ typedef struct {
  * The experts of a layer in 8-bit integers: gate and up (count n_experts, inter x
  * hidden), down (count n_experts, hidden x inter); the shared expert, when
  * sh_gate.codes is non-null, has the same shapes with count 1 and is added with
- * weight 1.
+ * weight 1.  (A shared expert with a weight of its own per token, a sigmoid gate say,
+ * goes in as one more of the stacked experts, chosen by every token in a further slot
+ * with that weight.)
  */
 typedef struct {
   int32_t hidden;

@@ -13,8 +13,10 @@
 // 64-bit arithmetic is a few hundred instructions a token.
 //
 // Measured: the selection alone 7.7 us for 2,048 tokens of 256 experts (a wave's chain of
-// about 3 us after the launch; the logits are 2 MB) and 15 us for 4,093 of 512 (issue-bound:
-// eight 64-bit exponentials, a sort and ten rounds a wave).
+// about 3 us after the launch; the logits are 2 MB) and 14 us for 4,093 of 512 (issue-bound:
+// eight 64-bit exponentials, a sort and ten rounds a wave; the sort's conditional swaps hold a
+// mask each, and at 8 and 16 experts a lane 52 and 290 of them move to lanes of vector
+// registers and back).
 #include <algorithm>
 #include <type_traits>
 

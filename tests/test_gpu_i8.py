@@ -481,3 +481,21 @@ def test_experts_gathered_rows_past_2gb(B):
     some = torch.cat([torch.arange(0, 9), torch.arange(131_067, 131_076), torch.arange(T - 9, T)]).cuda()
     ref, slack, _ = orc.experts_i8(*layer[:3], bf16_bits(X[some]), ids[some].cpu().numpy(), w[some].cpu().numpy())
     assert (np.abs(to_f64(y[some]) - ref) <= slack).all()
+
+
+@pytest.mark.parametrize("T", [1, 10, 80])
+def test_experts_gated_shared_as_a_stacked_one(B, T):
+    """A shared expert stacked behind the routed ones and chosen in a last slot: with weight 1 the
+    same bits as the shared form, with a gate's weights the definition's value."""
+    E, H, I, k = 6, 192, 128, 3
+    layer = _layer(31, E, H, I, True)
+    stacked = tuple(tuple(np.concatenate([m[i], s[i]]) for i in (0, 1)) for m, s in zip(layer[:3], layer[3]))
+    X, (ids, w) = _rows(32, T, H), _ids(33, T, E, k, 0.1 if T > 1 else 0.0)
+    ids = np.concatenate([ids, np.full((T, 1), E, np.int32)], 1)
+    ex = _experts(B, (*stacked, None))
+    x, i = B.bf16_tensor(X), torch.from_numpy(ids).cuda()
+    one = torch.from_numpy(np.concatenate([w, np.ones((T, 1), np.float32)], 1)).cuda()
+    want = B.moe_experts_i8(_experts(B, layer), x, i[:, :k].contiguous(), one[:, :k].contiguous())
+    assert torch.equal(B.moe_experts_i8(ex, x, i, one), want)
+    gate = np.random.default_rng(34).random((T, 1)).astype(np.float32)
+    _check_experts(B, (*stacked, None), X, ids, np.concatenate([w, gate], 1), ex)
