@@ -74,13 +74,15 @@ __device__ __forceinline__ void each_stage(F f, std::integer_sequence<int, St...
 }
 
 // Measured (MI355X; a large copy moves 5.1 TB/s, the library's int8 product of 8192^3 runs at
-// 2.1 POP/s): 8192 x 8192 x 4096 in 250 us, 2.2 POP/s; its matrix instructions alone take 177
-// us on this data, so what is left is the loads' and the turn's share that they do not cover.
+// 2.1 POP/s): 8192 x 8192 x 4096 in 233-266 us as the clock goes, 2.1-2.4 POP/s; its matrix
+// instructions are busy 62% of that (177 us of them alone on this data), what is left is the
+// loads' and the turn's share that they do not cover.
 // Grouped, 16,384 rows over 256 experts of 2048 x 512 and 2,048 of the shared one: gate/up
-// 131 us for 541 MB of weights (4.1 TB/s), down 80 us for 270 MB of weights and 75 MB of sums
-// (4.3 TB/s): bound by the weights' bytes, and by the last of 4.25 rounds of workgroups.
-// Operand tiles of 64 x 64 per wave were taken for them over 128 x 64 (139 and 86 us: half
-// the waves) and over two smaller workgroups a compute unit (285 us a layer against 263).
+// 136 us for 541 MB of weights (4.0 TB/s), down 92 us for 270 MB of weights and 151 MB of sums
+// (4.6 TB/s): bound by these bytes, and by the last of 4.25 rounds of workgroups.
+// Operand tiles of 64 x 64 per wave were taken for them over 128 x 64 (139 and 86 us against
+// 131 and 80, half the waves) and over two smaller workgroups a compute unit (285 us a layer
+// against 263), both with sums of two bytes.
 //
 // Workgroup = WM x WN waves, each FM x FN blocks of 32 x 32 (v_mfma_i32_32x32x32_i8).  Each
 // 128-column K step of both operands goes through LDS by 16-byte DMA loads (8 lanes read a
@@ -389,8 +391,9 @@ hipError_t launch_tiles(I8GemmArgs p, int64_t tiles, hipStream_t stream) {
 }
 
 // Bound by the sums' bytes, written just before: 151 MB for 2,048 tokens of 9 slots and 2,048
-// columns, beside the channels' scales from the L2.  The sums stay in fp32 (fp16 ones made the
-// layer 261 us instead of 284, and a bf16 output less exact than its 8 bits where slots cancel).
+// columns in 34 us (4.7 TB/s with the rows written), beside the channels' scales from the L2.
+// The sums stay in fp32: fp16 ones made the layer 261 us instead of 284, and a bf16 output less
+// exact than its 8 bits where slots cancel.
 // y[t] = sum_i (sums of slot i * its row's scale * the channel's scale) w_i + shared, in slot
 // order, the shared expert last; slots whose id names no expert add nothing.
 __global__ __launch_bounds__(256) void i8_combine_kernel(const float* __restrict__ part, const float* __restrict__ sh,

@@ -3,11 +3,13 @@
 write), as short Markdown for the profiles/ directory.
 
     python -m quantized_moe_decode_affine_amd.profsum stats DB --cmd "..."
+    python -m quantized_moe_decode_affine_amd.profsum grids DB --cmd "..."
     python -m quantized_moe_decode_affine_amd.profsum traffic --fetch DB1 --write DB2 \\
         --kernel decode_layer_kernel --copy-bytes N --unit-bytes B --cmd-fetch "..." --cmd-write "..."
     python -m quantized_moe_decode_affine_amd.profsum gemm-traffic --fetch DB1 --write DB2 \\
         --copy-bytes N --cmd-fetch "..." --cmd-write "..."
 
+`grids` lists this library's kernels by launch grid, in the order of their first launch.
 `traffic` scales the kernel's FETCH_SIZE / WRITE_SIZE readings (KiB per
 dispatch) by what the same counters read for a plain device copy of known size
 run in the same process (the largest `copyBuffer` dispatch), and records the
@@ -21,6 +23,7 @@ import hashlib
 import os
 import re
 import sqlite3
+import statistics
 from collections import defaultdict
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -75,6 +78,19 @@ def stats_markdown(db: str, cmd: str) -> str:
         for name, v in (("gate/up (even dispatches)", g[0::2]), ("down (odd dispatches)", g[1::2])):
             if v:
                 lines.append(f"| {name} | {len(v)} | {sum(v) / len(v):.2f} | {min(v):.2f} | {max(v):.2f} |")
+    lines += ["", f"kernel sources sha256: {all_sources_sha256()}"]
+    return "\n".join(lines) + "\n"
+
+
+def grids_markdown(db: str, cmd: str) -> str:
+    out = defaultdict(list)
+    for name, x, y, start, end in sqlite3.connect(db).execute(
+            "select name, grid_x, grid_y, start, end from kernels order by start"):
+        if "q4moe" in name:
+            out[(_short(name).replace("q4moe::", ""), x, y)].append((end - start) / 1000.0)
+    lines = [f"command: `{cmd}`", "", "| kernel | grid (threads) | calls | median us | min us |", "|---|---|---|---|---|"]
+    for (k, x, y), v in out.items():
+        lines.append(f"| `{k}` | {x} x {y} | {len(v)} | {statistics.median(v):.2f} | {min(v):.2f} |")
     lines += ["", f"kernel sources sha256: {all_sources_sha256()}"]
     return "\n".join(lines) + "\n"
 
@@ -157,6 +173,9 @@ def main():
     a = sub.add_parser("stats")
     a.add_argument("db")
     a.add_argument("--cmd", required=True)
+    r = sub.add_parser("grids")
+    r.add_argument("db")
+    r.add_argument("--cmd", required=True)
     t = sub.add_parser("traffic")
     t.add_argument("--fetch", required=True)
     t.add_argument("--write", required=True)
@@ -176,6 +195,8 @@ def main():
         print(gemm_traffic_markdown(args.fetch, args.write, args.copy_bytes, args.cmd_fetch, args.cmd_write), end="")
     elif args.what == "stats":
         print(stats_markdown(args.db, args.cmd), end="")
+    elif args.what == "grids":
+        print(grids_markdown(args.db, args.cmd), end="")
     else:
         print(traffic_markdown(args.fetch, args.write, args.kernel, args.copy_bytes, args.unit_bytes,
                                args.cmd_fetch, args.cmd_write), end="")
