@@ -391,8 +391,34 @@ int i8_quantize(const q4moe_bf16* X, int64_t rows, int64_t k, int8_t* codes, flo
 int i8_gemm(const q4moe_i8_matrix* W, const q4moe_bf16* X, int64_t m, void* Y, int out_dtype,
             void* workspace, size_t workspace_bytes, q4moe_stream stream);
 
+/*
+ * i8_gemm on rows that are in 8-bit form already: codes int8 [m][k] (16-byte aligned) and
+ * scales fp32 [m], as i8_quantize and rms_norm write them; the results are i8_gemm's bits
+ * on the rows that these came from.  For several products of the same rows, and after a
+ * norm.  Y overlaps neither.  No workspace.
+ */
+int i8_gemm_rows(const q4moe_i8_matrix* W, const int8_t* codes, const float* scales, int64_t m, void* Y,
+                 int out_dtype, q4moe_stream stream);
+
 /* Workspace bytes of i8_gemm on m rows; 0 for invalid arguments. */
 size_t i8_gemm_workspace_bytes(const q4moe_i8_matrix* W, int64_t m);
+
+/*
+ * Root-mean-square norm of bf16 rows X[rows][k], after the residual's addition:
+ *   t = bf16(X + residual)  (or X, where residual and total are null)
+ *   y = t / sqrt(sum_j t_j^2 / k + eps) * weight
+ * total bf16 [rows][k] receives t, the residual stream that the next addition takes; it
+ * may be X or residual itself.  The result goes to y as bf16 [rows][k] (rounded once from
+ * fp32 that is within 2^-22 of it), or in i8_quantize's 8-bit form to codes int8 [rows][k]
+ * and scales fp32 [rows], or to both: codes and scales are those of the unrounded y
+ * (scales[r] the fp32 nearest to max|y| / 127, codes computed in fp64), so that a product
+ * takes them with one rounding less than a bf16 y would bring.  y is null, or codes and
+ * scales are.  A row that holds an infinity or a NaN (in t, or in weight) gives scale NaN and
+ * codes 0; its y is what the formula gives.  weight bf16 [k]; k a multiple of 8 up to
+ * 65536; eps at least 1.2e-38 and finite.  Buffers overlap no other (but total as said).
+ */
+int rms_norm(const q4moe_bf16* X, const q4moe_bf16* residual, const q4moe_bf16* weight, int64_t rows, int64_t k,
+             double eps, q4moe_bf16* total, q4moe_bf16* y, int8_t* codes, float* scales, q4moe_stream stream);
 
 /*
  * T tokens through the 8-bit experts that a router chose for them: with ids int32

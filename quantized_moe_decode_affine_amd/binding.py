@@ -25,6 +25,7 @@ EXPORTS = ("q4_gemv", "q4_gemm", "moe_route_topk", "moe_route_topk_q8", "moe_per
            "moe_ffn_decode_batch",
            "moe_route", "moe_route_logits", "i8_quantize", "i8_gemm", "i8_gemm_workspace_bytes",
            "moe_experts_i8", "moe_experts_i8_workspace_bytes",
+           "i8_gemm_rows", "rms_norm",
            "moe_ffn_prefill", "lmhead_argmax", "q4moe_pack_group_major", "q4moe_workspace_bytes", "q4moe_strerror")
 
 
@@ -98,6 +99,8 @@ def load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
         "moe_route_logits": [ctypes.POINTER(q4moe_routing), vp, i64, vp, vp, vp],
         "i8_quantize": [vp, i64, i64, vp, vp, vp],
         "i8_gemm": [ctypes.POINTER(q4moe_i8_matrix), vp, i64, vp, ctypes.c_int, vp, sz, vp],
+        "i8_gemm_rows": [ctypes.POINTER(q4moe_i8_matrix), vp, vp, i64, vp, ctypes.c_int, vp],
+        "rms_norm": [vp, vp, vp, i64, i64, ctypes.c_double, vp, vp, vp, vp, vp],
         "moe_experts_i8": [ctypes.POINTER(q4moe_i8_experts), vp, i64, vp, vp, i32, vp, ctypes.c_int, vp, sz, vp],
     }
     for name, args in sigs.items():
@@ -610,6 +613,59 @@ def i8_gemm(W: DeviceI8, X: torch.Tensor, out_dtype: int = OUT_F32, out: Optiona
         _call("i8_gemm", dev, ctypes.byref(W.struct), X.data_ptr(), m, Y.data_ptr(), out_dtype, ws.data_ptr(),
               ws.numel())
     return Y
+
+
+def i8_gemm_rows(W: DeviceI8, codes: torch.Tensor, scales: torch.Tensor, out_dtype: int = OUT_F32,
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """i8_gemm on rows in 8-bit form: codes int8 [m][k] and scales fp32 [m] (i8_quantize, rms_norm_i8)."""
+    m, dev = codes.shape[0], W.codes.device
+    _need("codes", codes, torch.int8, (m, W.k), dev)
+    _need("scales", scales, torch.float32, (m,), dev)
+    Y = _result("out", out, (m, W.count * W.n), _out_type(out_dtype), dev)
+    if m:
+        _call("i8_gemm_rows", dev, ctypes.byref(W.struct), codes.data_ptr(), scales.data_ptr(), m, Y.data_ptr(),
+              out_dtype)
+    return Y
+
+
+def _norm(X, weight, eps, residual, total, y, codes, scales):
+    rows, k = X.shape
+    dev = X.device
+    _need("X", X, torch.bfloat16, (rows, k))
+    _need("weight", weight, torch.bfloat16, (k,), dev)
+    if residual is not None:
+        _need("residual", residual, torch.bfloat16, (rows, k), dev)
+        total = _result("total", total, (rows, k), torch.bfloat16, dev)
+    elif total is not None:
+        raise ValueError("total: only with a residual")
+    if rows:
+        _call("rms_norm", dev, X.data_ptr(), _ptr(residual), weight.data_ptr(), rows, k, eps, _ptr(total), _ptr(y),
+              _ptr(codes), _ptr(scales))
+    return total
+
+
+def rms_norm(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
+             total: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
+    """The root-mean-square norm of bfloat16 rows X [rows][k], as bfloat16.  With a residual the norm
+    is of total = bf16(X + residual), which is returned too (and may be written over X or the
+    residual): (y, total)."""
+    y = _result("out", out, tuple(X.shape), torch.bfloat16, X.device)
+    total = _norm(X, weight, eps, residual, total, y, None, None)
+    return y if residual is None else (y, total)
+
+
+def rms_norm_i8(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
+                total: Optional[torch.Tensor] = None, codes: Optional[torch.Tensor] = None,
+                scales: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
+    """rms_norm with its result in 8-bit form, for i8_gemm_rows: codes int8 [rows][k] and scales fp32
+    [rows], then total with a residual.  `out`: a bfloat16 tensor that receives the result in bfloat16
+    as well (a router's input, say)."""
+    codes = _result("codes", codes, tuple(X.shape), torch.int8, X.device)
+    scales = _result("scales", scales, (X.shape[0],), torch.float32, X.device)
+    if out is not None:
+        _need("out", out, torch.bfloat16, tuple(X.shape), X.device)
+    total = _norm(X, weight, eps, residual, total, out, codes, scales)
+    return (codes, scales) if residual is None else (codes, scales, total)
 
 
 def moe_experts_i8_workspace(experts: DeviceI8Experts, T: int, top_k: int) -> torch.Tensor:

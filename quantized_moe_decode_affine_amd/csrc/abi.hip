@@ -148,6 +148,7 @@ int rule_check(const q4moe_routing* R, q4moe::RouteRule* r) {
 
 constexpr int64_t kMaxTiles = (1 << 23) - 64;  // workgroups of 512 threads in a grid of 2^32
 constexpr int64_t kMaxI8K = 65536;      // 127 * 128 * k stays below 2^31
+constexpr int64_t kMaxNormK = 65536;    // 16 waves hold a row
 constexpr int64_t kMaxExpertK = 16384;  // hidden and intermediate sizes of the 8-bit experts
 
 bool i8_matrix_ok(const q4moe_i8_matrix* W) {
@@ -534,6 +535,46 @@ int i8_gemm(const q4moe_i8_matrix* W, const q4moe_bf16* X, int64_t m, void* Y, i
     if (clash({{workspace, need}}, {x, y})) return Q4MOE_EINVAL;
     return hip_status(q4moe::run_i8_gemm(q4moe::I8Mat{W->codes, W->scales}, n, (int)W->k, X, m, Y,
                                          out_dtype == Q4MOE_OUT_BF16, workspace, (hipStream_t)stream));
+  } catch (...) {
+    return Q4MOE_EHIP;
+  }
+}
+
+int i8_gemm_rows(const q4moe_i8_matrix* W, const int8_t* codes, const float* scales, int64_t m, void* Y, int out_dtype,
+                 q4moe_stream stream) {
+  try {
+    const int st = i8_gemm_check(W, m);
+    if (st != Q4MOE_OK) return st;
+    if (!codes || !aligned(codes, 16) || !scales || !aligned(scales, 4) || !out_ok(Y, out_dtype)) return Q4MOE_EINVAL;
+    if (m == 0) return Q4MOE_OK;
+    const int64_t n = W->count * W->n;
+    if (clash({{Y, (size_t)m * n * (out_dtype == Q4MOE_OUT_F32 ? 4 : 2)}}, {{codes, (size_t)m * W->k}, {scales, (size_t)m * 4}}))
+      return Q4MOE_EINVAL;
+    return hip_status(q4moe::run_i8_gemm_rows(q4moe::I8Mat{W->codes, W->scales}, n, (int)W->k, codes, scales, m, Y,
+                                              out_dtype == Q4MOE_OUT_BF16, (hipStream_t)stream));
+  } catch (...) {
+    return Q4MOE_EHIP;
+  }
+}
+
+int rms_norm(const q4moe_bf16* X, const q4moe_bf16* residual, const q4moe_bf16* weight, int64_t rows, int64_t k,
+             double eps, q4moe_bf16* total, q4moe_bf16* y, int8_t* codes, float* scales, q4moe_stream stream) {
+  try {
+    if (!X || !aligned(X, 16) || !weight || !aligned(weight, 16) || rows < 0 || k < 8 || k % 8) return Q4MOE_EINVAL;
+    if (!residual != !total || !codes != !scales || (!y && !codes)) return Q4MOE_EINVAL;
+    if (!aligned(residual, 16) || !aligned(total, 16) || !aligned(y, 16) || !aligned(codes, 16) || !aligned(scales, 4))
+      return Q4MOE_EINVAL;
+    if (!std::isfinite(eps) || eps < 1.2e-38) return Q4MOE_EINVAL;
+    if (k > kMaxNormK || rows > kMaxRows32) return Q4MOE_EUNSUPPORTED;
+    if (rows == 0) return Q4MOE_OK;
+    const size_t n = (size_t)rows * k;
+    const Span x{X, 2 * n}, r{residual, residual ? 2 * n : 0}, w{weight, (size_t)k * 2}, t{total, total ? 2 * n : 0};
+    const Span o{y, y ? 2 * n : 0}, c{codes, codes ? n : 0}, s{scales, scales ? (size_t)rows * 4 : 0};
+    if (clash({o, c, s}, {x, r, w, t}) || clash({t}, {w})) return Q4MOE_EINVAL;
+    // a row is read before its total is written, by the same threads
+    if (total && ((total != X && clash({t}, {x})) || (total != residual && clash({t}, {r})))) return Q4MOE_EINVAL;
+    return hip_status(q4moe::run_rms_norm(X, residual, weight, rows, (int)k, eps, total, y, codes, scales,
+                                          (hipStream_t)stream));
   } catch (...) {
     return Q4MOE_EHIP;
   }

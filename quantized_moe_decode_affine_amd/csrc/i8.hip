@@ -498,13 +498,11 @@ hipError_t run_i8_quantize(const uint16_t* X, int64_t rows, int K, int8_t* codes
 
 size_t i8_gemm_workspace_bytes(int64_t m, int K) { return align256((size_t)m * K) + align256((size_t)m * 4); }
 
-hipError_t run_i8_gemm(const I8Mat& W, int64_t n, int K, const uint16_t* X, int64_t m, void* Y, int out_bf16, void* ws,
-                       hipStream_t stream) {
-  if (i8_few_rows(m, K)) return run_i8_few_rows(W, n, K, X, (int)m, Y, out_bf16, stream);
-  int8_t* xq = static_cast<int8_t*>(ws);
-  float* sx = reinterpret_cast<float*>(static_cast<char*>(ws) + align256((size_t)m * K));
-  hipError_t e = launch_quantize(X, m, K, xq, sx, stream);
-  if (e != hipSuccess) return e;
+namespace {
+
+// The dense product of rows that are codes already.
+hipError_t launch_dense(const I8Mat& W, int64_t n, int K, const int8_t* xq, const float* sx, int64_t m, void* Y,
+                        int out_bf16, hipStream_t stream) {
   I8GemmArgs p{};
   p.A = xq;
   p.sa = sx;
@@ -522,6 +520,24 @@ hipError_t run_i8_gemm(const I8Mat& W, int64_t n, int K, const uint16_t* X, int6
                     : launch_tiles<2, 2, 2, 2, 2, kEpiF32>(p, (m + 127) / 128, stream);
   return out_bf16 ? launch_tiles<2, 2, 1, 1, 3, kEpiBf16>(p, (m + 63) / 64, stream)
                   : launch_tiles<2, 2, 1, 1, 3, kEpiF32>(p, (m + 63) / 64, stream);
+}
+
+}  // namespace
+
+hipError_t run_i8_gemm(const I8Mat& W, int64_t n, int K, const uint16_t* X, int64_t m, void* Y, int out_bf16, void* ws,
+                       hipStream_t stream) {
+  if (i8_few_rows(m, K)) return run_i8_few_rows(W, n, K, X, (int)m, Y, out_bf16, stream);
+  int8_t* xq = static_cast<int8_t*>(ws);
+  float* sx = reinterpret_cast<float*>(static_cast<char*>(ws) + align256((size_t)m * K));
+  const hipError_t e = launch_quantize(X, m, K, xq, sx, stream);
+  if (e != hipSuccess) return e;
+  return launch_dense(W, n, K, xq, sx, m, Y, out_bf16, stream);
+}
+
+hipError_t run_i8_gemm_rows(const I8Mat& W, int64_t n, int K, const int8_t* codes, const float* scales, int64_t m,
+                            void* Y, int out_bf16, hipStream_t stream) {
+  if (i8_few_rows(m, K)) return run_i8_few_rows(W, n, K, codes, scales, (int)m, Y, out_bf16, stream);
+  return launch_dense(W, n, K, codes, scales, m, Y, out_bf16, stream);
 }
 
 size_t experts_i8_workspace_bytes(const I8Experts& L, int64_t T, int k) {

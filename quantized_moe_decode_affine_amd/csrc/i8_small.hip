@@ -98,6 +98,20 @@ __device__ __forceinline__ void quantize_rows(Row row, int m, int K, int Kpad, u
   lds_sync();
 }
 
+// Rows that are codes already into the image, by the workgroup.
+__device__ __forceinline__ void copy_rows(const int8_t* X, const float* Xs, int m, int K, int Kpad, uint8_t* image,
+                                          float* s_scale) {
+  const int per = Kpad / 16;  // pieces of a row
+  for (int i = threadIdx.x; i < m * per; i += kSmallWaves * kWave) {
+    const int r = i / per, col = (i - r * per) * 16;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (col < K) v = *reinterpret_cast<const uint4*>(X + (int64_t)r * K + col);
+    *reinterpret_cast<uint4*>(image + image_at(col, r, m)) = v;
+  }
+  if (threadIdx.x < (unsigned)m) s_scale[threadIdx.x] = Xs[threadIdx.x];
+  lds_sync();
+}
+
 // A batch of weight pieces of one row per lane: columns c0 + 64 j + 16 * (lane / 16), clamped to the row.
 __device__ __forceinline__ void load_batch(const int8_t* row, int c0, int K, i32x4_t (&w)[kBatch]) {
   const int g = (lane_id() >> 4) * 16;
@@ -127,9 +141,11 @@ __device__ __forceinline__ i32x4acc_t mul_batch(const i32x4_t (&w)[kBatch], cons
 // Split: a workgroup per 16 weight rows, its waves share the columns (few rows: every
 // compute unit gets some).  Otherwise each wave takes whole blocks of 16 rows in turn, with
 // the next batch's loads in flight while one is multiplied.
-template <bool kSplit, bool kBf16>
+// In: bf16 rows (uint16_t), or codes (int8_t) whose scales are sx.
+template <bool kSplit, bool kBf16, typename In>
 __global__ __launch_bounds__(kSmallWaves* kWave) void i8_few_rows_kernel(I8Mat W, int64_t n, int K,
-                                                                         const uint16_t* __restrict__ X, int m,
+                                                                         const In* __restrict__ X,
+                                                                         const float* __restrict__ Xs, int m,
                                                                          void* __restrict__ Y) {
   extern __shared__ __align__(16) uint8_t s_image[];
   __shared__ float s_scale[16];
@@ -147,9 +163,15 @@ __global__ __launch_bounds__(kSmallWaves* kWave) void i8_few_rows_kernel(I8Mat W
 
   // the first weights are on their way while the rows are quantized
   i32x4_t w[kBatch];
-  quantize_rows<4>([&](int r) { return X + (int64_t)r * K; }, m, K, Kpad, s_image, s_scale, s_most, [&] {
+  auto weights = [&] {
     if (first < blocks && b0 < batches) load_batch(row_of(first), b0 * kBatchCols, K, w);
-  });
+  };
+  if constexpr (sizeof(In) == 1) {
+    weights();
+    copy_rows(X, Xs, m, K, Kpad, s_image, s_scale);
+  } else {
+    quantize_rows<4>([&](int r) { return X + (int64_t)r * K; }, m, K, Kpad, s_image, s_scale, s_most, weights);
+  }
 
   const int t = lane & 15;
   const float sx = s_scale[min(t, m - 1)];
@@ -195,7 +217,10 @@ size_t image_bytes(int64_t m, int K) { return (size_t)m * ((K + kBatchCols - 1) 
 
 bool i8_few_rows(int64_t m, int K) { return m <= 16 && image_bytes(m, K) <= kSmallLds; }
 
-hipError_t run_i8_few_rows(const I8Mat& W, int64_t n, int K, const uint16_t* X, int m, void* Y, int out_bf16,
+namespace {
+
+template <typename In>
+hipError_t launch_few_rows(const I8Mat& W, int64_t n, int K, const In* X, const float* Xs, int m, void* Y, int out_bf16,
                            hipStream_t stream) {
   const size_t lds = image_bytes(m, K);
   const int64_t blocks = (n + 15) / 16;
@@ -204,14 +229,26 @@ hipError_t run_i8_few_rows(const I8Mat& W, int64_t n, int K, const uint16_t* X, 
   const dim3 grid((unsigned)(split ? blocks : std::min<int64_t>(resident, (blocks + kSmallWaves - 1) / kSmallWaves)));
   const dim3 threads(kSmallWaves * kWave);
   if (split && out_bf16)
-    hipLaunchKernelGGL((i8_few_rows_kernel<true, true>), grid, threads, lds, stream, W, n, K, X, m, Y);
+    hipLaunchKernelGGL((i8_few_rows_kernel<true, true, In>), grid, threads, lds, stream, W, n, K, X, Xs, m, Y);
   else if (split)
-    hipLaunchKernelGGL((i8_few_rows_kernel<true, false>), grid, threads, lds, stream, W, n, K, X, m, Y);
+    hipLaunchKernelGGL((i8_few_rows_kernel<true, false, In>), grid, threads, lds, stream, W, n, K, X, Xs, m, Y);
   else if (out_bf16)
-    hipLaunchKernelGGL((i8_few_rows_kernel<false, true>), grid, threads, lds, stream, W, n, K, X, m, Y);
+    hipLaunchKernelGGL((i8_few_rows_kernel<false, true, In>), grid, threads, lds, stream, W, n, K, X, Xs, m, Y);
   else
-    hipLaunchKernelGGL((i8_few_rows_kernel<false, false>), grid, threads, lds, stream, W, n, K, X, m, Y);
+    hipLaunchKernelGGL((i8_few_rows_kernel<false, false, In>), grid, threads, lds, stream, W, n, K, X, Xs, m, Y);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t run_i8_few_rows(const I8Mat& W, int64_t n, int K, const uint16_t* X, int m, void* Y, int out_bf16,
+                           hipStream_t stream) {
+  return launch_few_rows(W, n, K, X, nullptr, m, Y, out_bf16, stream);
+}
+
+hipError_t run_i8_few_rows(const I8Mat& W, int64_t n, int K, const int8_t* codes, const float* scales, int m, void* Y,
+                           int out_bf16, hipStream_t stream) {
+  return launch_few_rows(W, n, K, codes, scales, m, Y, out_bf16, stream);
 }
 
 // ---- the experts' feed-forward on few slots, two launches

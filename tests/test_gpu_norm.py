@@ -1,0 +1,223 @@
+"""rms_norm and i8_gemm_rows against their 64-bit forms."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import q4moe_oracle as qorc
+from oracle import route_i8_oracle as i8orc
+from oracle import step_oracle as orc
+from quantized_moe_decode_affine_amd import synth
+
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-6
+# y is rounded once to bf16 from fp32 that two products of 2^-24 and a factor's 2^-24 left
+Y_REL = 2.0 ** -8 + 2.0 ** -22
+Y_ABS = 2.0 ** -133  # the last bit of bf16's subnormals
+
+
+@pytest.fixture(scope="module")
+def B():
+    from quantized_moe_decode_affine_amd import binding
+    assert torch.cuda.is_available()
+    binding.load_library()
+    return binding
+
+
+def _rows(seed, m, k, scale=1.0):
+    rng = np.random.default_rng(seed)
+    x = rng.standard_normal((m, k)) * np.exp(0.7 * rng.standard_normal((m, 1))) * scale
+    return synth.to_bf16_bits(x.astype(np.float32))
+
+
+def _bits(t):
+    return t.view(torch.int16).cpu().numpy().view(np.uint16)
+
+
+def _check_y(got, y):
+    g = qorc.bf16_to_f64(_bits(got))
+    assert (np.abs(g - y) <= Y_REL * np.abs(y) + Y_ABS).all(), np.abs(g - y).max()
+
+
+def _check_codes(codes, scales, y):
+    q, s = i8orc.quantize_rows(y)
+    np.testing.assert_array_equal(scales.cpu().numpy(), s)
+    np.testing.assert_array_equal(codes.cpu().numpy(), q)
+
+
+SHAPES = [(1, 8), (3, 64), (5, 200), (1, 512), (7, 520), (600, 1024), (600, 1000), (1, 2048), (700, 2048), (513, 2040),
+          (2, 4096), (515, 4104), (3, 8192), (2, 8200), (1, 16384), (2, 16392), (1, 65536), (2, 50000), (4097, 64)]
+
+
+@pytest.mark.parametrize("rows,k", SHAPES)
+@pytest.mark.parametrize("residual", [False, True])
+def test_norm(B, rows, k, residual):
+    X, w = _rows(rows + k, rows, k), _rows(k, 1, k)[0]
+    R = _rows(rows * 3 + k, rows, k, 3.0) if residual else None
+    t, y = orc.rms_norm(X, w, EPS, R)
+    x, wt = B.bf16_tensor(X), B.bf16_tensor(w)
+    r = B.bf16_tensor(R) if residual else None
+    got = B.rms_norm(x, wt, EPS, residual=r)
+    codes, scales, *more = B.rms_norm_i8(x, wt, EPS, residual=r)
+    both = torch.empty_like(x)
+    codes2, scales2, *_ = B.rms_norm_i8(x, wt, EPS, residual=r, out=both)
+    assert torch.equal(codes, codes2) and torch.equal(scales, scales2)
+    if residual:
+        got, total = got
+        np.testing.assert_array_equal(qorc.bf16_to_f64(_bits(total)), t)
+        assert torch.equal(total, more[0])
+    _check_y(got, y)
+    _check_y(both, y)
+    _check_codes(codes, scales, y)
+
+
+@pytest.mark.parametrize("rows,k", [(3, 2048), (1100, 2048), (2, 20000)])
+def test_total_over_an_input(B, rows, k):
+    """The stream's new state written over X or over the residual: the same bits."""
+    X, R, w = _rows(1, rows, k), _rows(2, rows, k), B.bf16_tensor(_rows(3, 1, k)[0])
+    x, r = B.bf16_tensor(X), B.bf16_tensor(R)
+    y, total = B.rms_norm(x, w, EPS, residual=r)
+    for over in (0, 1):
+        ins = [x.clone(), r.clone()]
+        y2, t2 = B.rms_norm(ins[0], w, EPS, residual=ins[1], total=ins[over])
+        assert t2 is ins[over] and torch.equal(t2, total) and torch.equal(y2, y)
+        assert torch.equal(ins[1 - over], (x, r)[1 - over])
+
+
+def test_extremes(B):
+    k = 256
+    x = np.zeros((12, k))
+    x[1] = 1.0                                    # every value the same
+    x[2, 5] = -3.0                                # a lone value
+    x[3] = 2.0 ** -130 * (np.arange(k) % 7)       # subnormal: eps rules
+    x[4] = 3e38 * (1 - np.arange(k) / 128)        # squares beyond fp32
+    x[5] = 1e-20 * np.arange(k)
+    x[6] = np.where(np.arange(k) % 2, 1e30, 1e-30)
+    x[7] = -1.0
+    w = 1 + 0.5 * np.sin(np.arange(k))
+    w[17] = 0.0
+    X, W = synth.to_bf16_bits(x.astype(np.float32)), synth.to_bf16_bits(w.astype(np.float32))
+    X[8, 9], X[9, 100], X[10, 17], X[11, 17] = 0x7F80, 0xFFC1, 0x7F80, 0x7FC0  # the last two under a zero weight
+    for eps in (1e-6, 1e-30, 1.0):
+        for rows in (slice(0, 8), slice(0, 12)):
+            _, y = orc.rms_norm(X[rows], W, eps)
+            xt, wt = B.bf16_tensor(X[rows]), B.bf16_tensor(W)
+            got = qorc.bf16_to_f64(_bits(B.rms_norm(xt, wt, eps)))
+            fine = np.isfinite(y)
+            assert (np.isnan(got) == np.isnan(y)).all()
+            # rounding to bf16 overflows from its largest value and half a step up
+            want = orc.f64_to_bf16(y)
+            big = fine & np.isinf(want)
+            assert (got[big] == want[big]).all()
+            fine &= ~big
+            assert (np.abs(got - y)[fine] <= Y_REL * np.abs(y[fine]) + Y_ABS).all()
+            codes, scales = B.rms_norm_i8(xt, wt, eps)
+            _check_codes(codes[:8], scales[:8], y[:8])
+            assert np.isnan(scales[8:].cpu().numpy()).all() and not codes[8:].any()
+    # a weight that is not finite reaches every row
+    W[3] = 0x7F80
+    codes, scales = B.rms_norm_i8(B.bf16_tensor(X[:8]), B.bf16_tensor(W))
+    assert torch.isnan(scales).all() and not codes.any()
+
+
+def test_residual_rounding_and_overflow(B):
+    """Ties of the addition go to even, a sum beyond the type becomes infinite, opposite infinities NaN."""
+    k = 64
+    a, r = np.zeros((4, k)), np.zeros((4, k))
+    a[0], r[0] = 256.0 + 2 * np.arange(k), 1.0            # a half step: to the even one
+    a[1], r[1] = -(256.0 + 2 * np.arange(k)), -1.0
+    a[2], r[2] = 3e38, 1e38
+    Xa, Xr = synth.to_bf16_bits(a.astype(np.float32)), synth.to_bf16_bits(r.astype(np.float32))
+    Xa[3, 0], Xr[3, 0] = 0x7F80, 0xFF80
+    w = synth.to_bf16_bits(np.ones(k, np.float32))
+    _, total = B.rms_norm(B.bf16_tensor(Xa), B.bf16_tensor(w), residual=B.bf16_tensor(Xr))
+    t, _ = orc.rms_norm(Xa, w, EPS, Xr)
+    np.testing.assert_array_equal(qorc.bf16_to_f64(_bits(total)), t)
+    codes, scales, _ = B.rms_norm_i8(B.bf16_tensor(Xa), B.bf16_tensor(w), residual=B.bf16_tensor(Xr))
+    assert torch.isnan(scales[2:]).all() and not codes[2:].any() and not torch.isnan(scales[:2]).any()
+
+
+def test_rows_alone_and_in_a_batch(B):
+    """A row's sums depend on how many waves share it: results stay within the one rounding, codes are equal."""
+    X, w = _rows(5, 1500, 2048), B.bf16_tensor(_rows(6, 1, 2048)[0])
+    x = B.bf16_tensor(X)
+    codes, scales = B.rms_norm_i8(x, w)
+    for r in (0, 777, 1499):
+        c1, s1 = B.rms_norm_i8(x[r:r + 1], w)
+        assert torch.equal(c1[0], codes[r]) and torch.equal(s1[0], scales[r])
+
+
+def test_offsets_past_32_bits(B):
+    rows, k = 262200, 8192  # 2^31 columns and more
+    x = torch.zeros((rows, k), dtype=torch.bfloat16, device="cuda")
+    last = B.bf16_tensor(_rows(7, 1, k))
+    x[-1:] = last
+    w = B.bf16_tensor(_rows(8, 1, k)[0])
+    codes, scales = B.rms_norm_i8(x, w)
+    c1, s1 = B.rms_norm_i8(last, w)
+    assert torch.equal(codes[-1], c1[0]) and torch.equal(scales[-1:], s1)
+    assert not codes[:-1].any() and not scales[:-1].any()
+    del codes
+    y = B.rms_norm(x, w)
+    assert torch.equal(y[-1], B.rms_norm(last, w)[0])
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 16, 64), (1, 1024, 2048), (3, 100, 192), (16, 4100, 2048), (17, 70, 320), (200, 513, 1088),
+                                   (16, 64, 8192), (1500, 700, 512)])
+def test_gemm_rows_is_gemm(B, m, n, k):
+    """The product of rows that are codes: the bits of the product that makes them."""
+    rng = np.random.default_rng(m + n + k)
+    W = B.DeviceI8(torch.from_numpy(rng.integers(-127, 128, (n, k), dtype=np.int8)).cuda(),
+                   torch.from_numpy((rng.random(n) * 0.01 + 1e-4).astype(np.float32)).cuda())
+    X = B.bf16_tensor(_rows(m, m, k))
+    for out in (B.OUT_F32, B.OUT_BF16):
+        assert torch.equal(B.i8_gemm_rows(W, *B.i8_quantize(X), out), B.i8_gemm(W, X, out))
+
+
+def test_norm_then_product(B):
+    """A norm's codes through a product, against the 64-bit forms of both."""
+    rows, k, n = 33, 1088, 515
+    rng = np.random.default_rng(9)
+    X, R, w = _rows(1, rows, k), _rows(2, rows, k), _rows(3, 1, k)[0]
+    wc, ws = rng.integers(-127, 128, (n, k), dtype=np.int8), (rng.random(n) * 0.01 + 1e-4).astype(np.float32)
+    codes, scales, _ = B.rms_norm_i8(B.bf16_tensor(X), B.bf16_tensor(w), EPS, residual=B.bf16_tensor(R))
+    Y = B.i8_gemm_rows(B.DeviceI8(torch.from_numpy(wc).cuda(), torch.from_numpy(ws).cuda()), codes, scales)
+    q, s = i8orc.quantize_rows(orc.rms_norm(X, w, EPS, R)[1])
+    ref = (q.astype(np.float64) @ wc.astype(np.float64).T) * s[:, None] * ws.astype(np.float64)
+    # the exact sum becomes fp32, then two scales: three roundings
+    assert (np.abs(Y.double().cpu().numpy() - ref) <= 3.01 * 2.0 ** -24 * np.abs(ref)).all()
+
+
+def test_norm_graph(B):
+    X, R, w = (B.bf16_tensor(_rows(s, 40, 2048)) for s in (1, 2, 3))
+    w = w[0].clone()
+    y, total, codes, scales = torch.empty_like(X), torch.empty_like(X), torch.empty(40, 2048, dtype=torch.int8, device="cuda"), torch.empty(40, device="cuda")
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        B.rms_norm_i8(X, w, residual=R, total=total, codes=codes, scales=scales, out=y)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        B.rms_norm_i8(X, w, residual=R, total=total, codes=codes, scales=scales, out=y)
+    for seed in range(3):
+        X.copy_(B.bf16_tensor(_rows(10 + seed, 40, 2048)))
+        g.replay()
+        y2 = torch.empty_like(X)
+        c2, s2, t2 = B.rms_norm_i8(X, w, residual=R, out=y2)
+        assert torch.equal(y, y2) and torch.equal(total, t2) and torch.equal(codes, c2) and torch.equal(scales, s2)
+
+
+def test_binding_refusals(B):
+    x, w = torch.zeros(2, 64, dtype=torch.bfloat16, device="cuda"), torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    for bad in (lambda: B.rms_norm(x.float(), w), lambda: B.rms_norm(x, w[:32]), lambda: B.rms_norm(x.T, w),
+                lambda: B.rms_norm(x.cpu(), w.cpu()), lambda: B.rms_norm(x, w, residual=x[:1]),
+                lambda: B.rms_norm(x, w, total=x.clone()), lambda: B.rms_norm_i8(x, w, out=x.float()),
+                lambda: B.rms_norm(x, w.cpu())):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: B.rms_norm(x, w, eps=0.0), lambda: B.rms_norm(x, w, out=x),
+                lambda: B.rms_norm(x, w, residual=x.clone(), total=x, out=x)):
+        with pytest.raises(B.Q4Error) as err:
+            bad()
+        assert err.value.status == B.EINVAL
+    assert B.rms_norm(x[:0], w).shape == (0, 64)
