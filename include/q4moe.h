@@ -157,6 +157,35 @@ typedef struct {
   q4moe_i8_matrix sh_gate, sh_up, sh_down;
 } q4moe_i8_experts;
 
+/*
+ * A matrix in microscaled 4-bit floating point (OCP MXFP4), or `count` stacked matrices of
+ * the same shape.  Each 32 consecutive columns of a row share a scale, a power of two held
+ * as its exponent (E8M0): scales uint8 [count][n][k/32], a byte b for 2^(b - 127), 255 for
+ * NaN.  codes uint8 [count][n][k/2]: column 2j of a row in the low four bits of byte j,
+ * column 2j + 1 in the high four; a code is e2m1, a sign (bit 3) and one of 0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6.  w[r][j] = 2^(scale - 127) * code.  mx4_quantize writes this form.
+ * k a multiple of 64; codes 16-byte aligned, scales 2-byte aligned.
+ */
+typedef struct {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  int64_t count;  /* >= 1 */
+  int64_t n;      /* rows per matrix */
+  int64_t k;      /* columns, a multiple of 64 */
+} q4moe_mx4_matrix;
+
+/*
+ * The experts of a layer in microscaled 4-bit floating point, shaped as q4moe_i8_experts.
+ */
+typedef struct {
+  int32_t hidden;
+  int32_t inter;
+  int32_t n_experts;
+  int32_t reserved;  /* 0 */
+  q4moe_mx4_matrix gate, up, down;
+  q4moe_mx4_matrix sh_gate, sh_up, sh_down;  /* codes null: no shared expert */
+} q4moe_mx4_experts;
+
 /* Scores of q4moe_routing. */
 enum { Q4MOE_SCORE_SOFTMAX = 0, Q4MOE_SCORE_SIGMOID = 1 };
 
@@ -443,6 +472,54 @@ int moe_experts_i8(const q4moe_i8_experts* experts, const q4moe_bf16* X, int64_t
 
 /* Workspace bytes of moe_experts_i8 on T tokens of top_k slots; 0 for invalid arguments. */
 size_t moe_experts_i8_workspace_bytes(const q4moe_i8_experts* experts, int64_t T, int32_t top_k);
+
+/*
+ * Microscaled 4-bit form (see q4moe_mx4_matrix) of bf16 rows X[rows][k].  A block's scale is
+ * 2^(floor(log2(max|x|)) - 2), at least 2^-127, and its codes are x / scale rounded to the
+ * nearest of e2m1's values (ties to the even code; beyond 6 to 6).  A block of zeros gets
+ * scale byte 0; a block that holds an infinity or a NaN gets scale byte 255 and codes 0, so
+ * products with it are NaN.  The load-time step for weights, and what mx4_gemm does to its
+ * activations.  k a multiple of 64 up to 65536; X and codes 16-byte aligned, scales 2-byte
+ * aligned; no buffer overlaps another.
+ */
+int mx4_quantize(const q4moe_bf16* X, int64_t rows, int64_t k, uint8_t* codes, uint8_t* scales, q4moe_stream stream);
+
+/*
+ * The values of a matrix (all count * n rows) as bf16 [count*n][k], exact: magnitudes of 2^128
+ * and more, which mx4_quantize does not write, become infinite.  Y overlaps neither input.
+ */
+int mx4_dequantize(const q4moe_mx4_matrix* W, q4moe_bf16* Y, q4moe_stream stream);
+
+/*
+ * Y[m][r] = sum_j xq[m][j] w[r][j] for bf16 rows X[m][k], with xq the microscaled 4-bit form
+ * of X's rows (mx4_quantize), taken inside the call.  The product in 4-bit floating point
+ * next to i8_gemm's in integers, on the matrix cores that take the blocks' scales: each
+ * product is exact, sums are fp32 (rows of one call alike, few rows in another order than
+ * more).  Y fp32 or bf16 [m][count*n], not overlapping X; k up to 65536.  Needs a workspace
+ * of mx4_gemm_workspace_bytes, which overlaps neither.
+ */
+int mx4_gemm(const q4moe_mx4_matrix* W, const q4moe_bf16* X, int64_t m, void* Y, int out_dtype, void* workspace,
+             size_t workspace_bytes, q4moe_stream stream);
+
+/* Workspace bytes of mx4_gemm on m rows; 0 for invalid arguments. */
+size_t mx4_gemm_workspace_bytes(const q4moe_mx4_matrix* W, int64_t m);
+
+/*
+ * moe_experts_i8 with experts in microscaled 4-bit floating point: x in that form per token,
+ * silu(gate x) * up x (fp32) per token and expert, both products mx4_gemm's.  Ids, weights,
+ * empty and repeated slots, the order of the sum and the shared expert as there.  X bf16
+ * [T][hidden], Y fp32 or bf16 [T][hidden], not overlapping X, ids or weights; hidden and
+ * inter multiples of 64 up to 16384, n_experts up to 1024, top_k up to 32 (not bounded by
+ * n_experts).  A token's result may differ in its sums' last bits, and in an activation next
+ * to a border between two codes, with the number of tokens in the call.  Needs a workspace of
+ * moe_experts_mx4_workspace_bytes that overlaps none of them.
+ */
+int moe_experts_mx4(const q4moe_mx4_experts* experts, const q4moe_bf16* X, int64_t T, const int32_t* ids,
+                    const float* weights, int32_t top_k, void* Y, int out_dtype, void* workspace,
+                    size_t workspace_bytes, q4moe_stream stream);
+
+/* Workspace bytes of moe_experts_mx4 on T tokens of top_k slots; 0 for invalid arguments. */
+size_t moe_experts_mx4_workspace_bytes(const q4moe_mx4_experts* experts, int64_t T, int32_t top_k);
 
 /*
  * Greedy LM head: logits[b][r] = W[r] . X[b] in fp32 for b < B (1 <= B <= 8),

@@ -25,7 +25,8 @@ EXPORTS = ("q4_gemv", "q4_gemm", "moe_route_topk", "moe_route_topk_q8", "moe_per
            "moe_ffn_decode_batch",
            "moe_route", "moe_route_logits", "i8_quantize", "i8_gemm", "i8_gemm_workspace_bytes",
            "moe_experts_i8", "moe_experts_i8_workspace_bytes",
-           "i8_gemm_rows", "rms_norm",
+           "i8_gemm_rows", "rms_norm", "mx4_quantize", "mx4_dequantize", "mx4_gemm", "mx4_gemm_workspace_bytes",
+           "moe_experts_mx4", "moe_experts_mx4_workspace_bytes",
            "moe_ffn_prefill", "lmhead_argmax", "q4moe_pack_group_major", "q4moe_workspace_bytes", "q4moe_strerror")
 
 
@@ -59,6 +60,18 @@ class q4moe_i8_experts(ctypes.Structure):
                 ("reserved", ctypes.c_int32),
                 ("gate", q4moe_i8_matrix), ("up", q4moe_i8_matrix), ("down", q4moe_i8_matrix),
                 ("sh_gate", q4moe_i8_matrix), ("sh_up", q4moe_i8_matrix), ("sh_down", q4moe_i8_matrix)]
+
+
+class q4moe_mx4_matrix(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("count", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64)]
+
+
+class q4moe_mx4_experts(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_int32), ("inter", ctypes.c_int32),
+                ("n_experts", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("gate", q4moe_mx4_matrix), ("up", q4moe_mx4_matrix), ("down", q4moe_mx4_matrix),
+                ("sh_gate", q4moe_mx4_matrix), ("sh_up", q4moe_mx4_matrix), ("sh_down", q4moe_mx4_matrix)]
 
 
 class q4moe_routing(ctypes.Structure):
@@ -101,6 +114,10 @@ def load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
         "i8_gemm": [ctypes.POINTER(q4moe_i8_matrix), vp, i64, vp, ctypes.c_int, vp, sz, vp],
         "i8_gemm_rows": [ctypes.POINTER(q4moe_i8_matrix), vp, vp, i64, vp, ctypes.c_int, vp],
         "rms_norm": [vp, vp, vp, i64, i64, ctypes.c_double, vp, vp, vp, vp, vp],
+        "mx4_quantize": [vp, i64, i64, vp, vp, vp],
+        "mx4_dequantize": [ctypes.POINTER(q4moe_mx4_matrix), vp, vp],
+        "mx4_gemm": [ctypes.POINTER(q4moe_mx4_matrix), vp, i64, vp, ctypes.c_int, vp, sz, vp],
+        "moe_experts_mx4": [ctypes.POINTER(q4moe_mx4_experts), vp, i64, vp, vp, i32, vp, ctypes.c_int, vp, sz, vp],
         "moe_experts_i8": [ctypes.POINTER(q4moe_i8_experts), vp, i64, vp, vp, i32, vp, ctypes.c_int, vp, sz, vp],
     }
     for name, args in sigs.items():
@@ -113,6 +130,10 @@ def load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
     lib.i8_gemm_workspace_bytes.restype = sz
     lib.moe_experts_i8_workspace_bytes.argtypes = [ctypes.POINTER(q4moe_i8_experts), i64, i32]
     lib.moe_experts_i8_workspace_bytes.restype = sz
+    lib.mx4_gemm_workspace_bytes.argtypes = [ctypes.POINTER(q4moe_mx4_matrix), i64]
+    lib.mx4_gemm_workspace_bytes.restype = sz
+    lib.moe_experts_mx4_workspace_bytes.argtypes = [ctypes.POINTER(q4moe_mx4_experts), i64, i32]
+    lib.moe_experts_mx4_workspace_bytes.restype = sz
     lib.q4moe_strerror.argtypes = [ctypes.c_int]
     lib.q4moe_strerror.restype = ctypes.c_char_p
     _lib = lib
@@ -299,6 +320,55 @@ class DeviceI8Experts:
             if (m.count, m.n, m.k) != (count, n, k):
                 raise ValueError(f"experts: a matrix of shape {(m.count, m.n, m.k)} where {(count, n, k)} is wanted")
         self.struct = q4moe_i8_experts(self.hidden, self.inter, self.n_experts, 0, *(m.struct for m in self.matrices))
+
+    @property
+    def nbytes(self) -> int:
+        return sum(m.nbytes for m in self.matrices)
+
+
+class DeviceMx4:
+    """A matrix in microscaled 4-bit floating point (or a stack of them) on the device: codes uint8
+    [n][k/2] or [count][n][k/2], two to a byte (the lower column in the low bits), and scales uint8
+    [..][k/32], exponents of the blocks of 32 columns.  See q4moe_mx4_matrix in include/q4moe.h."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
+        if codes.dim() == 2:
+            codes, scales = codes[None], scales[None]
+        self.count, self.n, half = codes.shape
+        self.k = half * 2
+        _need("codes", codes, torch.uint8, (self.count, self.n, half))
+        _need("scales", scales, torch.uint8, (self.count, self.n, half // 16), codes.device)
+        self.codes, self.scales = codes, scales
+        self.struct = q4moe_mx4_matrix(codes.data_ptr(), scales.data_ptr(), self.count, self.n, self.k)
+
+    @classmethod
+    def quantize(cls, weight: torch.Tensor) -> "DeviceMx4":
+        """The 4-bit form of bfloat16 weights [n][k] or [count][n][k]."""
+        k = weight.shape[-1]
+        codes, scales = mx4_quantize(weight.reshape(-1, k))
+        return cls(codes.view(*weight.shape[:-1], k // 2), scales.view(*weight.shape[:-1], k // 32))
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.scales.numel()
+
+
+class DeviceMx4Experts:
+    """The experts of a layer in microscaled 4-bit floating point: gate and up
+    [n_experts][inter][hidden], down [n_experts][hidden][inter], and optionally the shared expert's
+    (gate, up, down)."""
+
+    def __init__(self, gate: DeviceMx4, up: DeviceMx4, down: DeviceMx4, shared=None):
+        self.n_experts, self.inter, self.hidden = gate.count, gate.n, gate.k
+        self.matrices = (gate, up, down, *(shared or ()))
+        self.has_shared = shared is not None
+        if len(self.matrices) not in (3, 6) or any(m.codes.device != gate.codes.device for m in self.matrices):
+            raise ValueError("experts: gate, up and down, and as many of the shared expert, on one device")
+        for m, count, n, k in zip(self.matrices, (self.n_experts,) * 3 + (1,) * 3, (self.inter, self.inter, self.hidden) * 2,
+                                  (self.hidden, self.hidden, self.inter) * 2):
+            if (m.count, m.n, m.k) != (count, n, k):
+                raise ValueError(f"experts: a matrix of shape {(m.count, m.n, m.k)} where {(count, n, k)} is wanted")
+        self.struct = q4moe_mx4_experts(self.hidden, self.inter, self.n_experts, 0, *(m.struct for m in self.matrices))
 
     @property
     def nbytes(self) -> int:
@@ -688,5 +758,73 @@ def moe_experts_i8(experts: DeviceI8Experts, X: torch.Tensor, ids: torch.Tensor,
     if T:
         ws = _scratch(ws, lambda: load_library().moe_experts_i8_workspace_bytes(ctypes.byref(experts.struct), T, k), dev)
         _call("moe_experts_i8", dev, ctypes.byref(experts.struct), X.data_ptr(), T, ids.data_ptr(),
+              weights.data_ptr(), k, Y.data_ptr(), out_dtype, ws.data_ptr(), ws.numel())
+    return Y
+
+
+def mx4_quantize(X: torch.Tensor):
+    """Microscaled 4-bit codes uint8 [rows][k/2] and scales uint8 [rows][k/32] of bfloat16 rows."""
+    rows, k = X.shape
+    _need("X", X, torch.bfloat16, (rows, k))
+    codes = torch.empty((rows, k // 2), dtype=torch.uint8, device=X.device)
+    scales = torch.empty((rows, k // 32), dtype=torch.uint8, device=X.device)
+    if rows:
+        _call("mx4_quantize", X.device, X.data_ptr(), rows, k, codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The bfloat16 values [..][k] of codes [..][k/2] and scales [..][k/32]."""
+    shape = (*codes.shape[:-1], codes.shape[-1] * 2)
+    dev = codes.device
+    _need("codes", codes, torch.uint8, codes.shape)
+    _need("scales", scales, torch.uint8, (*shape[:-1], shape[-1] // 32), dev)
+    Y = _result("out", out, shape, torch.bfloat16, dev)
+    if codes.numel():
+        rows = codes.numel() // codes.shape[-1]
+        _call("mx4_dequantize", dev, ctypes.byref(q4moe_mx4_matrix(codes.data_ptr(), scales.data_ptr(), 1, rows, shape[-1])),
+              Y.data_ptr())
+    return Y
+
+
+def mx4_gemm_workspace(W: DeviceMx4, m: int) -> torch.Tensor:
+    """A workspace for mx4_gemm on up to m rows."""
+    return torch.empty(max(256, load_library().mx4_gemm_workspace_bytes(ctypes.byref(W.struct), m)),
+                       dtype=torch.uint8, device=W.codes.device)
+
+
+def mx4_gemm(W: DeviceMx4, X: torch.Tensor, out_dtype: int = OUT_F32, out: Optional[torch.Tensor] = None,
+             ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y = X W^T in microscaled 4-bit floating point: the rows of X (bfloat16) are quantized inside the call."""
+    m, dev = X.shape[0], W.codes.device
+    _need("X", X, torch.bfloat16, (m, W.k), dev)
+    Y = _result("out", out, (m, W.count * W.n), _out_type(out_dtype), dev)
+    if m:
+        ws = _scratch(ws, lambda: load_library().mx4_gemm_workspace_bytes(ctypes.byref(W.struct), m), dev)
+        _call("mx4_gemm", dev, ctypes.byref(W.struct), X.data_ptr(), m, Y.data_ptr(), out_dtype, ws.data_ptr(),
+              ws.numel())
+    return Y
+
+
+def moe_experts_mx4_workspace(experts: DeviceMx4Experts, T: int, top_k: int) -> torch.Tensor:
+    """A workspace for moe_experts_mx4 on up to T tokens of top_k slots."""
+    return torch.empty(max(256, load_library().moe_experts_mx4_workspace_bytes(ctypes.byref(experts.struct), T, top_k)),
+                       dtype=torch.uint8, device=experts.matrices[0].codes.device)
+
+
+def moe_experts_mx4(experts: DeviceMx4Experts, X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
+                    out_dtype: int = OUT_F32, out: Optional[torch.Tensor] = None,
+                    ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The rows of X through the 4-bit experts of ids [T][top_k] (others than 0..n_experts-1 add
+    nothing), weighted by weights [T][top_k], plus the shared expert."""
+    T, dev = X.shape[0], experts.matrices[0].codes.device
+    _need("X", X, torch.bfloat16, (T, experts.hidden), dev)
+    k = ids.shape[1] if ids.dim() == 2 else 0
+    _need("ids", ids, torch.int32, (T, k), dev)
+    _need("weights", weights, torch.float32, (T, k), dev)
+    Y = _result("out", out, (T, experts.hidden), _out_type(out_dtype), dev)
+    if T:
+        ws = _scratch(ws, lambda: load_library().moe_experts_mx4_workspace_bytes(ctypes.byref(experts.struct), T, k), dev)
+        _call("moe_experts_mx4", dev, ctypes.byref(experts.struct), X.data_ptr(), T, ids.data_ptr(),
               weights.data_ptr(), k, Y.data_ptr(), out_dtype, ws.data_ptr(), ws.numel())
     return Y

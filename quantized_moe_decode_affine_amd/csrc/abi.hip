@@ -191,6 +191,52 @@ int i8_experts_check(const q4moe_i8_experts* L, int64_t T, int64_t top_k, q4moe:
   return Q4MOE_OK;
 }
 
+bool mx4_matrix_ok(const q4moe_mx4_matrix* W) {
+  return W && W->codes && W->scales && W->count >= 1 && W->n >= 1 && W->k >= 64 && W->k % 64 == 0 &&
+         aligned(W->codes, 16) && aligned(W->scales, 2);
+}
+
+bool mx4_shape(const q4moe_mx4_matrix& W, int64_t count, int64_t n, int64_t k) {
+  return mx4_matrix_ok(&W) && W.count == count && W.n == n && W.k == k;
+}
+
+q4moe::Mx4Mat to_mx4(const q4moe_mx4_matrix& W) { return q4moe::Mx4Mat{W.codes, W.scales}; }
+
+// Rows of a stack, or -1 beyond what the kernels count.
+int64_t mx4_rows(const q4moe_mx4_matrix& W) {
+  return W.count > kMaxRows32 || W.n > kMaxRows32 || W.count * W.n > kMaxRows32 ? -1 : W.count * W.n;
+}
+
+int mx4_gemm_check(const q4moe_mx4_matrix* W, int64_t m) {
+  if (!mx4_matrix_ok(W) || m < 0) return Q4MOE_EINVAL;
+  // a grid holds kMaxTiles of 256 x 256
+  if (W->k > kMaxI8K || mx4_rows(*W) < 0 || m > kMaxRows32 || (m / 256 + 1) * (mx4_rows(*W) / 256 + 1) > kMaxTiles)
+    return Q4MOE_EUNSUPPORTED;
+  return Q4MOE_OK;
+}
+
+int mx4_experts_check(const q4moe_mx4_experts* L, int64_t T, int64_t top_k, q4moe::Mx4Experts* d) {
+  if (!L || T < 0 || top_k < 1) return Q4MOE_EINVAL;
+  if (L->hidden < 64 || L->hidden % 64 || L->inter < 64 || L->inter % 64 || L->n_experts < 1) return Q4MOE_EINVAL;
+  if (L->hidden > kMaxExpertK || L->inter > kMaxExpertK || L->n_experts > 1024 || top_k > 32) return Q4MOE_EUNSUPPORTED;
+  const int64_t E = L->n_experts, H = L->hidden, I = L->inter;
+  if (!mx4_shape(L->gate, E, I, H) || !mx4_shape(L->up, E, I, H) || !mx4_shape(L->down, E, H, I)) return Q4MOE_EINVAL;
+  const bool shared = L->sh_gate.codes != nullptr;
+  if (shared && (!mx4_shape(L->sh_gate, 1, I, H) || !mx4_shape(L->sh_up, 1, I, H) || !mx4_shape(L->sh_down, 1, H, I)))
+    return Q4MOE_EINVAL;
+  // sorted positions, the tiles' grid and the offsets of gathered rows are 32-bit
+  const int64_t rows = T > kMaxRows32 ? kMaxRows32 : T * (top_k + 1);
+  if (T > kMaxRows32 || rows > kMaxRows32 || T * H / 2 > 0xFFF00000ll ||
+      (rows / 128 + 2 * E + 16) * (std::max(H / 256, I / 128) + 1) > kMaxTiles)
+    return Q4MOE_EUNSUPPORTED;
+  const q4moe::Mx4Mat none{nullptr, nullptr};
+  *d = q4moe::Mx4Experts{L->hidden,       L->inter,       L->n_experts,
+                         to_mx4(L->gate), to_mx4(L->up),  to_mx4(L->down),
+                         shared ? to_mx4(L->sh_gate) : none, shared ? to_mx4(L->sh_up) : none,
+                         shared ? to_mx4(L->sh_down) : none};
+  return Q4MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -603,6 +649,86 @@ int moe_experts_i8(const q4moe_i8_experts* experts, const q4moe_bf16* X, int64_t
     if (clash({{workspace, need}}, {x, i, w, y})) return Q4MOE_EINVAL;
     return hip_status(q4moe::run_moe_experts_i8(d, X, T, ids, weights, top_k, Y, out_dtype == Q4MOE_OUT_BF16,
                                                 workspace, (hipStream_t)stream));
+  } catch (...) {
+    return Q4MOE_EHIP;
+  }
+}
+
+int mx4_quantize(const q4moe_bf16* X, int64_t rows, int64_t k, uint8_t* codes, uint8_t* scales, q4moe_stream stream) {
+  try {
+    if (!X || !aligned(X, 16) || !codes || !aligned(codes, 16) || !scales || !aligned(scales, 2) || rows < 0)
+      return Q4MOE_EINVAL;
+    if (k < 64 || k % 64) return Q4MOE_EINVAL;
+    if (k > kMaxI8K || rows > kMaxRows32) return Q4MOE_EUNSUPPORTED;
+    if (rows == 0) return Q4MOE_OK;
+    const size_t n = (size_t)rows * k;
+    if (clash({{codes, n / 2}, {scales, n / 32}}, {{X, 2 * n}})) return Q4MOE_EINVAL;
+    return hip_status(q4moe::run_mx4_quantize(X, rows, (int)k, codes, scales, (hipStream_t)stream));
+  } catch (...) {
+    return Q4MOE_EHIP;
+  }
+}
+
+int mx4_dequantize(const q4moe_mx4_matrix* W, q4moe_bf16* Y, q4moe_stream stream) {
+  try {
+    if (!mx4_matrix_ok(W) || !Y || !aligned(Y, 16)) return Q4MOE_EINVAL;
+    const int64_t rows = mx4_rows(*W);
+    if (rows < 0 || W->k > kMaxI8K) return Q4MOE_EUNSUPPORTED;
+    const size_t n = (size_t)rows * W->k;
+    if (clash({{Y, 2 * n}}, {{W->codes, n / 2}, {W->scales, n / 32}})) return Q4MOE_EINVAL;
+    return hip_status(q4moe::run_mx4_dequantize(W->codes, W->scales, rows, (int)W->k, Y, (hipStream_t)stream));
+  } catch (...) {
+    return Q4MOE_EHIP;
+  }
+}
+
+size_t mx4_gemm_workspace_bytes(const q4moe_mx4_matrix* W, int64_t m) {
+  return mx4_gemm_check(W, m) == Q4MOE_OK ? q4moe::mx4_gemm_workspace_bytes(m, (int)W->k) : 0;
+}
+
+int mx4_gemm(const q4moe_mx4_matrix* W, const q4moe_bf16* X, int64_t m, void* Y, int out_dtype, void* workspace,
+             size_t workspace_bytes, q4moe_stream stream) {
+  try {
+    const int st = mx4_gemm_check(W, m);
+    if (st != Q4MOE_OK) return st;
+    if (!X || !aligned(X, 16) || !out_ok(Y, out_dtype)) return Q4MOE_EINVAL;
+    if (m == 0) return Q4MOE_OK;
+    const int64_t n = mx4_rows(*W);
+    const Span y{Y, (size_t)m * n * (out_dtype == Q4MOE_OUT_F32 ? 4 : 2)}, x{X, (size_t)m * W->k * 2};
+    if (clash({y}, {x})) return Q4MOE_EINVAL;
+    const size_t need = q4moe::mx4_gemm_workspace_bytes(m, (int)W->k);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return Q4MOE_EWORKSPACE;
+    if (clash({{workspace, need}}, {x, y})) return Q4MOE_EINVAL;
+    return hip_status(q4moe::run_mx4_gemm(to_mx4(*W), n, (int)W->k, X, m, Y, out_dtype == Q4MOE_OUT_BF16, workspace,
+                                          (hipStream_t)stream));
+  } catch (...) {
+    return Q4MOE_EHIP;
+  }
+}
+
+size_t moe_experts_mx4_workspace_bytes(const q4moe_mx4_experts* experts, int64_t T, int32_t top_k) {
+  q4moe::Mx4Experts d;
+  return mx4_experts_check(experts, T, top_k, &d) == Q4MOE_OK ? q4moe::experts_mx4_workspace_bytes(d, T, top_k) : 0;
+}
+
+int moe_experts_mx4(const q4moe_mx4_experts* experts, const q4moe_bf16* X, int64_t T, const int32_t* ids,
+                    const float* weights, int32_t top_k, void* Y, int out_dtype, void* workspace,
+                    size_t workspace_bytes, q4moe_stream stream) {
+  try {
+    q4moe::Mx4Experts d;
+    const int st = mx4_experts_check(experts, T, top_k, &d);
+    if (st != Q4MOE_OK) return st;
+    if (!X || !aligned(X, 16) || !ids || !aligned(ids, 4) || !weights || !aligned(weights, 4) || !out_ok(Y, out_dtype))
+      return Q4MOE_EINVAL;
+    if (T == 0) return Q4MOE_OK;
+    const Span y{Y, (size_t)T * d.hidden * (out_dtype == Q4MOE_OUT_F32 ? 4 : 2)}, x{X, (size_t)T * d.hidden * 2};
+    const Span i{ids, (size_t)T * top_k * 4}, w{weights, (size_t)T * top_k * 4};
+    if (clash({y}, {x, i, w})) return Q4MOE_EINVAL;
+    const size_t need = q4moe::experts_mx4_workspace_bytes(d, T, top_k);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return Q4MOE_EWORKSPACE;
+    if (clash({{workspace, need}}, {x, i, w, y})) return Q4MOE_EINVAL;
+    return hip_status(q4moe::run_moe_experts_mx4(d, X, T, ids, weights, top_k, Y, out_dtype == Q4MOE_OUT_BF16,
+                                                 workspace, (hipStream_t)stream));
   } catch (...) {
     return Q4MOE_EHIP;
   }

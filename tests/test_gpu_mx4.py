@@ -1,0 +1,388 @@
+"""mx4_quantize, mx4_dequantize, mx4_gemm and moe_experts_mx4 against their 64-bit forms."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import q4moe_oracle as qorc
+from oracle import step_oracle as orc
+from quantized_moe_decode_affine_amd import synth
+
+pytestmark = pytest.mark.gpu
+
+HALF = 2.0 ** -24       # half a step of fp32 at most, relative
+HALF_BF16 = 2.0 ** -8   # and of bfloat16
+
+
+@pytest.fixture(scope="module")
+def B():
+    from quantized_moe_decode_affine_amd import binding
+    assert torch.cuda.is_available()
+    binding.load_library()
+    return binding
+
+
+def _rows(seed, m, k):
+    rng = np.random.default_rng(seed)
+    x = rng.standard_normal((m, k)) * np.exp(0.7 * rng.standard_normal((m, 1)))
+    return synth.to_bf16_bits(x.astype(np.float32))
+
+
+def _weights(seed, *shape, lo=118, hi=124):
+    rng = np.random.default_rng(seed)
+    codes = rng.integers(0, 256, (*shape[:-1], shape[-1] // 2), dtype=np.uint8)
+    return codes, rng.integers(lo, hi, (*shape[:-1], shape[-1] // 32), dtype=np.uint8)
+
+
+def _dev(B, w):
+    return B.DeviceMx4(torch.from_numpy(w[0]).cuda(), torch.from_numpy(w[1]).cuda())
+
+
+def _bits(t):
+    return t.view(torch.int16).cpu().numpy().view(np.uint16)
+
+
+# ------------------------------------------------------------------- quantize --
+
+def _check_quantize(B, X, v=None):
+    codes, scales = B.mx4_quantize(B.bf16_tensor(X))
+    c, s = orc.mx4_quantize(qorc.bf16_to_f64(X) if v is None else v)
+    np.testing.assert_array_equal(scales.cpu().numpy(), s)
+    np.testing.assert_array_equal(codes.cpu().numpy(), c)
+    back = B.mx4_dequantize(codes, scales)
+    want = orc.f64_to_bf16(orc.mx4_values(c, s))
+    np.testing.assert_array_equal(qorc.bf16_to_f64(_bits(back)), want)
+    return codes, scales
+
+
+@pytest.mark.parametrize("rows,k", [(1, 64), (3, 128), (5, 192), (4, 2048), (1030, 320), (2, 16384), (1, 65536), (9001, 64)])
+def test_quantize_exact(B, rows, k):
+    _check_quantize(B, _rows(rows + k, rows, k))
+
+
+def test_quantize_every_value(B):
+    """Every finite bfloat16 in blocks whose largest value is at, above and far above it."""
+    bits = np.arange(0x8000, dtype=np.uint16)
+    bits = bits[bits < 0x7F80]
+    exps = np.arange(0, 0x7F80, 0x80, dtype=np.uint16)
+    rows = []
+    for up in (0, 1, 2, 3, 4, 5, 9):  # the block's largest: exponent + up, some mantissa
+        top = np.minimum((bits & 0x7F80).astype(np.int64) + 0x80 * up + (bits.astype(np.int64) * 37 & 0x7F), 0x7F7F)
+        block = np.zeros((bits.size, 32), dtype=np.uint16)
+        block[:, 0] = bits
+        block[:, 7] = bits | 0x8000
+        block[:, 31] = np.maximum(top, bits) | (bits & 1) << 15
+        rows.append(block.reshape(-1, 64))
+    block = np.zeros((exps.size * 128, 32), dtype=np.uint16)  # every mantissa among the same exponent's
+    block[:, :] = (np.repeat(exps, 128) + np.tile(np.arange(128, dtype=np.uint16), exps.size))[:, None]
+    block[:, 1] = np.repeat(exps, 128)
+    rows.append(block.reshape(-1, 64))
+    _check_quantize(B, np.concatenate(rows))
+
+
+def test_quantize_blocks_that_are_not_finite(B):
+    X = _rows(3, 6, 256)
+    X[0, 5], X[1, 70], X[2, 31], X[2, 32], X[3, 255] = 0x7F80, 0xFF80, 0x7FC0, 0xFFFF, 0x7F81
+    X[4] = 0
+    X[5] = 0x8000
+    v = qorc.bf16_to_f64(X)
+    codes, scales = _check_quantize(B, X, v)
+    s = scales.cpu().numpy()
+    assert (s[0] == 255).tolist() == [True] + [False] * 7 and s[2, 0] == s[2, 1] == 255 and (s[4:] == 0).all()
+    y = B.mx4_dequantize(codes, scales)
+    assert torch.isnan(y[0, :32]).all() and not torch.isnan(y[0, 32:]).any()
+
+
+def test_dequantize_every_code_and_scale(B):
+    codes = np.tile(np.arange(256, dtype=np.uint8)[None, :], (256, 1))   # 512 columns, 16 blocks
+    scales = np.tile(np.arange(256, dtype=np.uint8)[:, None], (1, 16))
+    y = B.mx4_dequantize(torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda())
+    np.testing.assert_array_equal(qorc.bf16_to_f64(_bits(y)), orc.f64_to_bf16(orc.mx4_values(codes, scales)))
+
+
+def test_quantize_offsets_past_32_bits(B):
+    rows, k = 34000, 65536  # 2^31 columns and more
+    x = torch.zeros((rows, k), dtype=torch.bfloat16, device="cuda")
+    x[-1:] = last = B.bf16_tensor(_rows(7, 1, k))
+    codes, scales = B.mx4_quantize(x)
+    c1, s1 = B.mx4_quantize(last)
+    assert torch.equal(codes[-1:], c1) and torch.equal(scales[-1:], s1)
+    assert not codes[:-1].any() and not scales[:-1].any()
+    x.fill_(1.0)
+    y = B.mx4_dequantize(codes, scales, out=x)
+    assert torch.equal(y[-1:], B.mx4_dequantize(c1, s1)) and not y[:-1].any()
+
+
+# ----------------------------------------------------------------------- gemm --
+
+def _exact_case(seed, m, n, k):
+    """Rows and weights whose every sum of products is exact in fp32: two scales, a bit apart, on
+    either side, so that all products are multiples of a quarter of the smallest and sums stay
+    below 2^24 of them (144 * 4 * k)."""
+    rng = np.random.default_rng(seed)
+    assert 576 * k < 2 ** 24
+    w = _weights(seed, n, k, lo=126, hi=128)
+    xc = rng.integers(0, 256, (m, k // 2), dtype=np.uint8)
+    xc[:, ::16] |= 0x66  # a 4 or a 6 in each block: its scale is then the one that it was made with
+    xs = rng.integers(126, 128, (m, k // 32), dtype=np.uint8)
+    v = orc.mx4_values(xc, xs)
+    X = synth.to_bf16_bits(v.astype(np.float32))
+    assert (orc.mx4_round(v) == v).all()
+    return X, v, w
+
+
+GEMM = [(1, 16, 64), (1, 1, 64), (2, 5, 128), (3, 33, 192), (1, 1024, 2048), (5, 20, 8192), (16, 100, 576), (16, 17000, 256),
+        (9, 16400, 704), (17, 16, 64), (17, 40, 128), (40, 70, 192), (64, 64, 256), (65, 129, 320), (33, 1027, 832), (16, 96, 28672),
+        (381, 1027, 832), (300, 250, 8192), (128, 2048, 512), (1000, 3, 448), (2100, 2300, 384), (4200, 4300, 320), (16, 200, 16384)]
+
+
+@pytest.mark.parametrize("m,n,k", GEMM)
+def test_gemm_exact(B, m, n, k):
+    X, v, w = _exact_case(m * 7 + n + k, m, n, k)
+    W, x = _dev(B, w), B.bf16_tensor(X)
+    dev = torch.from_numpy(orc.mx4_values(*w)).cuda()
+    ref = (torch.from_numpy(v).cuda() @ dev.T)
+    y = B.mx4_gemm(W, x)
+    assert torch.equal(y.double(), ref), (y.double() - ref).abs().max()
+    assert torch.equal(B.mx4_gemm(W, x, B.OUT_BF16), ref.float().bfloat16())
+
+
+@pytest.mark.parametrize("m,n,k", [(256, 256, 256), (256, 512, 16384), (200, 130, 28608)])
+def test_gemm_tiles_over_many_steps(B, m, n, k):
+    """The scale buffers and stages taken in turn many times, each tile size (chosen by rows)."""
+    X, v, w = _exact_case(k, m, n, k)
+    y = B.mx4_gemm(_dev(B, w), B.bf16_tensor(X))
+    assert torch.equal(y.double(), torch.from_numpy(v).cuda() @ torch.from_numpy(orc.mx4_values(*w)).cuda().T)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 100, 2048), (16, 50, 832), (100, 130, 2048), (700, 600, 1088)])
+def test_gemm_random(B, m, n, k):
+    """Scales over their range: a chain of k fp32 additions errs by k 2^-24 of the terms' sum at most."""
+    X, w = _rows(m + n, m, k), _weights(k, n, k, lo=100, hi=140)
+    q, wv = orc.mx4_round(qorc.bf16_to_f64(X)), orc.mx4_values(*w)
+    ref, size = q @ wv.T, np.abs(q) @ np.abs(wv).T
+    y = B.mx4_gemm(_dev(B, w), B.bf16_tensor(X)).double().cpu().numpy()
+    assert (np.abs(y - ref) <= k * HALF * size).all()
+
+
+def test_gemm_extreme_scales_and_nan(B):
+    """The smallest scales against the largest; blocks with NaN scales and rows that are not finite reach
+    their own rows and columns alone."""
+    for m in (4, 40, 300):
+        k, n = 448, 70
+        rng = np.random.default_rng(m)
+        X = synth.to_bf16_bits((rng.standard_normal((m, k)) * 2.0 ** 60).astype(np.float32))
+        w = _weights(5, n, k, lo=0, hi=9)
+        w[1][7, 13] = 255       # a column's last block
+        w[1][9, 0] = 255
+        X[2, 447], X[3, 0] = 0x7F80, 0xFFC0
+        q = orc.mx4_round(qorc.bf16_to_f64(X))
+        wv = orc.mx4_values(*w)
+        with np.errstate(invalid="ignore"):
+            ref, size = q @ wv.T, np.abs(q) @ np.abs(wv).T
+        y = B.mx4_gemm(_dev(B, w), B.bf16_tensor(X)).double().cpu().numpy()
+        nan = np.zeros((m, n), bool)
+        nan[:, [7, 9]] = nan[[2, 3]] = True
+        assert (np.isnan(y) == nan).all()
+        assert (np.abs(y - ref)[~nan] <= k * HALF * size[~nan] + 2.0 ** -149 * k).all()
+
+
+def test_gemm_stack_and_row_of_neighbours(B):
+    """A stack of matrices is its rows; results do not depend on what lies behind the operands."""
+    m, n, k = 50, 24, 320
+    X, v, w = _exact_case(1, m, 3 * n, k)
+    stack = B.DeviceMx4(torch.from_numpy(w[0].reshape(3, n, k // 2)).cuda(), torch.from_numpy(w[1].reshape(3, n, -1)).cuda())
+    y = B.mx4_gemm(stack, B.bf16_tensor(X))
+    assert torch.equal(y, B.mx4_gemm(_dev(B, w), B.bf16_tensor(X)))
+    for rows in (3, 50):  # NaN rows of X and of the weight right behind
+        big = np.full((m + 8, k), 0x7FC0, np.uint16)
+        big[:rows] = X[:rows]
+        wide = torch.full((3 * n + 8, k // 2), 0xFF, dtype=torch.uint8, device="cuda")
+        sc = torch.full((3 * n + 8, k // 32), 0xFF, dtype=torch.uint8, device="cuda")
+        wide[:3 * n], sc[:3 * n] = torch.from_numpy(w[0]).cuda(), torch.from_numpy(w[1]).cuda()
+        got = B.mx4_gemm(B.DeviceMx4(wide[:3 * n], sc[:3 * n]), B.bf16_tensor(big)[:rows])
+        assert torch.equal(got, y[:rows])
+
+
+def test_gemm_leaves_rows_behind(B):
+    X, v, w = _exact_case(2, 300, 77, 128)
+    for m in (5, 40, 300):
+        out = torch.full((m + 4, 77), 7.0, device="cuda")
+        B.mx4_gemm(_dev(B, w), B.bf16_tensor(X[:m]), out=out[:m])
+        assert (out[m:] == 7.0).all()
+
+
+def test_gemm_weights_past_32_bits(B):
+    """Codes beyond 4 GB: the last columns of a large matrix."""
+    n, k = 270000, 32768
+    codes = torch.zeros((n, k // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.full((n, k // 32), 127, dtype=torch.uint8, device="cuda")
+    tail = _weights(4, 40, k, lo=126, hi=128)
+    codes[-40:], scales[-40:] = torch.from_numpy(tail[0]).cuda(), torch.from_numpy(tail[1]).cuda()
+    for m in (2, 20):
+        X = _rows(m, m, k)
+        y = B.mx4_gemm(B.DeviceMx4(codes, scales), B.bf16_tensor(X))
+        small = B.mx4_gemm(_dev(B, tail), B.bf16_tensor(X))
+        size = np.abs(orc.mx4_round(qorc.bf16_to_f64(X))) @ np.abs(orc.mx4_values(*tail)).T
+        assert (np.abs((y[:, -40:] - small).cpu().numpy()) <= 2 * k * HALF * size).all()
+        assert not y[:, :-40].any()
+
+
+# -------------------------------------------------------------------- experts --
+
+def _code_range(h, err):
+    """The lowest and highest value that a block's element can round to when each of h is off by up to err."""
+    g, d = h.reshape(*h.shape[:-1], -1, 32), err.reshape(*h.shape[:-1], -1, 32)
+    out = []
+    tops = (np.maximum(np.abs(g) - d, 0).max(-1, keepdims=True), (np.abs(g) + d).max(-1, keepdims=True))
+    for top in tops:
+        e = np.maximum(np.frexp(np.maximum(top, 2.0 ** -125))[1] - 3, -127)
+        for v in (g - d, g + d):
+            a = np.ldexp(np.abs(v), -e)
+            step = np.where(a < 2, 0.5, np.where(a < 4, 1.0, 2.0))
+            out.append(np.ldexp(np.copysign(np.minimum(np.rint(a / step) * step, 6.0), v), e))
+    return np.minimum.reduce(out).reshape(h.shape), np.maximum.reduce(out).reshape(h.shape)
+
+
+def _experts_ref(X, ids, weights, mats, shared):
+    """y and how far a result computed in fp32 may be from it, by the formula in 64 bits."""
+    q = orc.mx4_round(qorc.bf16_to_f64(X))
+    T, H = q.shape
+    y, tol = np.zeros((T, H)), np.zeros((T, H))
+
+    def add(rows, w, g, u, d):
+        a, b = q[rows] @ g.T, q[rows] @ u.T
+        ea, eb = (H * HALF * (np.abs(q[rows]) @ np.abs(m).T) for m in (g, u))
+        s = a / (1 + np.exp(-a))
+        h = s * b
+        # silu's slope is at most 1.1; expf, the sum, the quotient and the products: 8 steps in all
+        err = 1.1 * ea * (np.abs(b) + eb) + np.abs(s) * eb + 8 * HALF * np.abs(h) + 2.0 ** -126
+        lo, hi = _code_range(h, err)
+        mid, off = (lo + hi) / 2, (hi - lo) / 2
+        part = mid @ d.T
+        size = np.maximum(np.abs(lo), np.abs(hi)) @ np.abs(d).T
+        y[rows] += w[:, None] * part
+        tol[rows] += np.abs(w[:, None]) * (off @ np.abs(d).T + (d.shape[1] + 40) * HALF * size)
+
+    gate, up, down = mats
+    for e in range(gate.shape[0]):
+        t, slot = np.nonzero(ids == e)
+        for s in np.unique(slot):
+            rows = t[slot == s]
+            add(rows, weights[rows, s].astype(np.float64), gate[e], up[e], down[e])
+    if shared is not None:
+        add(np.arange(T), np.ones(T), *shared)
+    return y, tol
+
+
+def _experts_case(seed, T, E, H, inter, k, shared, empty=0.1):
+    rng = np.random.default_rng(seed)
+    mats = [_weights(seed + i, E, *s, lo=119, hi=122) for i, s in enumerate(((inter, H), (inter, H), (H, inter)))]
+    sh = [_weights(seed + 9 + i, 1, *s, lo=119, hi=122) for i, s in enumerate(((inter, H), (inter, H), (H, inter)))] if shared else None
+    ids = np.stack([rng.choice(E, k, replace=k > E) for _ in range(T)]).astype(np.int32)
+    ids[rng.random((T, k)) < empty] = rng.choice([-1, E, 2 ** 31 - 1, -2 ** 31])
+    w = rng.random((T, k)).astype(np.float32)
+    return _rows(seed, T, H), ids, w, mats, sh
+
+
+def _run_experts(B, case, out=0):
+    X, ids, w, mats, sh = case
+    ex = B.DeviceMx4Experts(*(_dev(B, m) for m in mats), shared=tuple(_dev(B, m) for m in sh) if sh else None)
+    return B.moe_experts_mx4(ex, B.bf16_tensor(X), torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda(), out)
+
+
+def _values(mats):
+    return [orc.mx4_values(*m) for m in mats]
+
+
+@pytest.mark.parametrize("T,E,H,inter,k,shared", [
+    (1, 4, 64, 64, 2, False), (1, 8, 2048, 512, 8, True), (2, 8, 128, 64, 2, True), (7, 5, 320, 192, 4, False),
+    (16, 3, 704, 128, 4, True), (3, 40, 1088, 704, 20, True), (17, 6, 128, 64, 3, True), (65, 8, 64, 64, 2, False),
+    (40, 60, 1088, 704, 4, True), (333, 7, 320, 448, 5, True), (200, 2, 576, 64, 1, False), (9, 1, 64, 64, 32, True)])
+def test_experts(B, T, E, H, inter, k, shared):
+    case = _experts_case(T + E + H, T, E, H, inter, k, shared)
+    X, ids, w, mats, sh = case
+    y, tol = _experts_ref(X, ids, w, _values(mats), [m[0] for m in _values(sh)] if sh else None)
+    # the range of values that borders leave is narrow: most elements have only one
+    got = _run_experts(B, case).double().cpu().numpy()
+    assert np.isfinite(got).all() and (np.abs(got - y) <= tol).all(), (np.abs(got - y) - tol).max()
+    half = _run_experts(B, case, B.OUT_BF16).double().cpu().numpy()
+    assert (np.abs(half - y) <= tol * (1 + HALF_BF16) + HALF_BF16 * np.abs(y)).all()
+
+
+def test_experts_repeated_and_empty_slots(B):
+    """An id in several slots counts each time; a token without an expert gets the shared one, or zeros."""
+    for T in (4, 90):
+        case = list(_experts_case(3, T, 6, 128, 64, 4, False, empty=0.0))
+        case[1][0] = 2
+        case[1][1] = -1
+        case[1][2, 1:] = 6
+        y, tol = _experts_ref(case[0], case[1], case[2], _values(case[3]), None)
+        got = _run_experts(B, case).double().cpu().numpy()
+        assert (np.abs(got - y) <= tol).all() and not got[1].any()
+        case[4] = [_weights(50 + i, 1, *s, lo=119, hi=122) for i, s in enumerate(((64, 128), (64, 128), (128, 64)))]
+        y, tol = _experts_ref(case[0], case[1], case[2], _values(case[3]), [m[0] for m in _values(case[4])])
+        got = _run_experts(B, case).double().cpu().numpy()
+        assert (np.abs(got - y) <= tol).all() and got[1].any()
+
+
+def test_experts_all_empty(B):
+    for T in (3, 100):
+        X, ids, w, mats, sh = _experts_case(4, T, 5, 128, 64, 3, False)
+        ids[:] = -1
+        assert not _run_experts(B, (X, ids, w, mats, sh)).any()
+
+
+def test_experts_nan_reaches_its_token_alone(B):
+    for T in (5, 120):
+        case = list(_experts_case(6, T, 5, 320, 128, 3, True, empty=0.0))
+        plain = _run_experts(B, case)
+        case[0] = case[0].copy()
+        case[0][2, 70] = 0x7F80
+        got = _run_experts(B, case)
+        assert torch.isnan(got[2]).all()
+        keep = [t for t in range(T) if t != 2]
+        assert torch.equal(got[keep], plain[keep])
+
+
+def test_experts_workspace_of_more_tokens_and_captured(B):
+    """One workspace for calls of every size up to its own, eager and replayed, the inputs changing between."""
+    X, ids, w, mats, sh = _experts_case(8, 150, 12, 320, 192, 4, True)
+    ex = B.DeviceMx4Experts(*(_dev(B, m) for m in mats), shared=tuple(_dev(B, m) for m in sh))
+    ws = B.moe_experts_mx4_workspace(ex, 150, 4)
+    x, i, wt = B.bf16_tensor(X), torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda()
+    for T in (150, 3, 70, 1):
+        ws.fill_(0xA5)
+        got = B.moe_experts_mx4(ex, x[:T].contiguous(), i[:T].contiguous(), wt[:T].contiguous(), ws=ws)
+        assert torch.equal(got, B.moe_experts_mx4(ex, x[:T].contiguous(), i[:T].contiguous(), wt[:T].contiguous()))
+    for T in (6, 150):
+        xs, out = x[:T].clone(), torch.empty((T, 320), device="cuda")
+        ix, wx = i[:T].clone(), wt[:T].clone()
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            B.moe_experts_mx4(ex, xs, ix, wx, out=out, ws=ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            B.moe_experts_mx4(ex, xs, ix, wx, out=out, ws=ws)
+        for seed in range(4):
+            xs.copy_(B.bf16_tensor(_rows(seed, T, 320)))
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, B.moe_experts_mx4(ex, xs, ix, wx))
+
+
+def test_binding_refusals(B):
+    W = _dev(B, _weights(1, 16, 128))
+    x = torch.zeros(2, 128, dtype=torch.bfloat16, device="cuda")
+    for bad in (lambda: B.mx4_gemm(W, x.float()), lambda: B.mx4_gemm(W, x[:, :64]), lambda: B.mx4_gemm(W, x, 2),
+                lambda: B.mx4_gemm(W, x, ws=torch.empty(10, device="cuda")), lambda: B.mx4_quantize(x.half()),
+                lambda: B.DeviceMx4(W.codes, W.scales[:, :, :2]), lambda: B.DeviceMx4(W.codes.cpu(), W.scales),
+                lambda: B.mx4_dequantize(W.codes, W.scales[:, :8])):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(B.Q4Error) as err:
+        B.mx4_gemm(W, x, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    assert err.value.status == B.EWORKSPACE
+    with pytest.raises(B.Q4Error):
+        B.mx4_quantize(torch.zeros(2, 96, dtype=torch.bfloat16, device="cuda"))
+    assert B.mx4_gemm(W, x[:0]).shape == (0, 16) and B.mx4_quantize(x[:0])[0].shape == (0, 64)
