@@ -534,6 +534,36 @@ int lmhead_argmax(const q4moe_matrix* W, const q4moe_bf16* X, int64_t B, int32_t
                   float* max_logit, void* workspace, size_t workspace_bytes, q4moe_stream stream);
 
 /*
+ * The next token of B rows of logits [B][V], drawn by given random numbers u fp32 [B] in
+ * [0, 1): what lmhead_argmax's greedy choice is to one, on logits that a product wrote.
+ * logits_dtype: Q4MOE_OUT_F32 or Q4MOE_OUT_BF16.  Each row has its own parameters (each
+ * array [B], or null for none): temperature fp32, top_k int32, top_p fp32, min_p fp32.
+ *  - temperature t: weights are w_i = exp((l_i - max l) / t).  Where t is not above 0 the
+ *    row is greedy: its largest logit, the filters aside.
+ *  - The filters keep a first part of the tokens in descending order of their logits
+ *    (equal ones: the lower index first).  top_k in 1..V-1: that many tokens (others: all).
+ *    top_p below 1: of these the fewest whose weights sum to at least top_p of theirs, one at
+ *    least.  min_p above 0: of these the ones with w_i >= min_p (1 where it is larger), the
+ *    weight of the likeliest being 1.
+ *  - ids[b] is the first token in the order of the vocabulary with which the kept weights'
+ *    running sum exceeds u times their total; probs[b] (may be null) its weight over the total.
+ * A NaN logit is closed, as -infinity is: never kept.  A row without an open logit gets id -1
+ * and probability 0; of a row with a logit of +infinity these share the weight.  A u outside
+ * [0, 1) counts as the nearest in it, a NaN as 0.  NaN parameters are: a temperature greedy,
+ * a top_p or min_p none.  Weights are taken in fp64 to multiples of 2^-45 of the largest and
+ * added as integers, so a row gets the same token in any batch and on any run.
+ * V up to 262144, B up to 65536; logits aligned to their type; ids and probs overlap no
+ * input, each other or the workspace (Q4MOE_EINVAL).  Needs a workspace of
+ * sample_logits_workspace_bytes; calls that share one must not overlap.
+ */
+int sample_logits(const void* logits, int logits_dtype, int64_t B, int64_t V, const float* u,
+                  const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p, int32_t* ids,
+                  float* probs, void* workspace, size_t workspace_bytes, q4moe_stream stream);
+
+/* Workspace bytes of sample_logits on B rows; 0 for invalid arguments. */
+size_t sample_logits_workspace_bytes(int64_t B, int64_t V);
+
+/*
  * Write the group-major copy of a 4-bit matrix's codes (see q4moe_matrix) to dst:
  * uint32 [count][k/64][n][8] (count*n*k/8 words, 16-byte aligned, device memory the
  * caller owns; it must not overlap W->codes).  A layout step for prefill, done once per

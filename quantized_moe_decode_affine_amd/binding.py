@@ -26,7 +26,7 @@ EXPORTS = ("q4_gemv", "q4_gemm", "moe_route_topk", "moe_route_topk_q8", "moe_per
            "moe_route", "moe_route_logits", "i8_quantize", "i8_gemm", "i8_gemm_workspace_bytes",
            "moe_experts_i8", "moe_experts_i8_workspace_bytes",
            "i8_gemm_rows", "rms_norm", "mx4_quantize", "mx4_dequantize", "mx4_gemm", "mx4_gemm_workspace_bytes",
-           "moe_experts_mx4", "moe_experts_mx4_workspace_bytes",
+           "moe_experts_mx4", "moe_experts_mx4_workspace_bytes", "sample_logits", "sample_logits_workspace_bytes",
            "moe_ffn_prefill", "lmhead_argmax", "q4moe_pack_group_major", "q4moe_workspace_bytes", "q4moe_strerror")
 
 
@@ -118,6 +118,7 @@ def load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
         "mx4_dequantize": [ctypes.POINTER(q4moe_mx4_matrix), vp, vp],
         "mx4_gemm": [ctypes.POINTER(q4moe_mx4_matrix), vp, i64, vp, ctypes.c_int, vp, sz, vp],
         "moe_experts_mx4": [ctypes.POINTER(q4moe_mx4_experts), vp, i64, vp, vp, i32, vp, ctypes.c_int, vp, sz, vp],
+        "sample_logits": [vp, ctypes.c_int, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
         "moe_experts_i8": [ctypes.POINTER(q4moe_i8_experts), vp, i64, vp, vp, i32, vp, ctypes.c_int, vp, sz, vp],
     }
     for name, args in sigs.items():
@@ -134,6 +135,8 @@ def load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
     lib.mx4_gemm_workspace_bytes.restype = sz
     lib.moe_experts_mx4_workspace_bytes.argtypes = [ctypes.POINTER(q4moe_mx4_experts), i64, i32]
     lib.moe_experts_mx4_workspace_bytes.restype = sz
+    lib.sample_logits_workspace_bytes.argtypes = [i64, i64]
+    lib.sample_logits_workspace_bytes.restype = sz
     lib.q4moe_strerror.argtypes = [ctypes.c_int]
     lib.q4moe_strerror.restype = ctypes.c_char_p
     _lib = lib
@@ -828,3 +831,35 @@ def moe_experts_mx4(experts: DeviceMx4Experts, X: torch.Tensor, ids: torch.Tenso
         _call("moe_experts_mx4", dev, ctypes.byref(experts.struct), X.data_ptr(), T, ids.data_ptr(),
               weights.data_ptr(), k, Y.data_ptr(), out_dtype, ws.data_ptr(), ws.numel())
     return Y
+
+
+def sample_logits_workspace(B: int, V: int, device="cuda") -> torch.Tensor:
+    """A workspace for sample_logits on up to B rows of V logits."""
+    return torch.empty(max(256, load_library().sample_logits_workspace_bytes(B, V)), dtype=torch.uint8, device=device)
+
+
+def sample_logits(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch.Tensor] = None,
+                  top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
+                  min_p: Optional[torch.Tensor] = None, ids: Optional[torch.Tensor] = None,
+                  probs: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
+    """The next token of each row of logits [B][V] (float32 or bfloat16), drawn by the random numbers
+    u [B]: ids int32 [B] and their probabilities fp32 [B] among what the filters keep.  Each row has its own
+    temperature, top_k (int32), top_p and min_p, or a filter is None for all."""
+    B, V = logits.shape
+    dev = logits.device
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"logits: float32 or bfloat16 is wanted, got {logits.dtype}")
+    _need("logits", logits, logits.dtype, (B, V))
+    _need("u", u, torch.float32, (B,), dev)
+    for name, t, dtype in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
+                           ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
+        if t is not None:
+            _need(name, t, dtype, (B,), dev)
+    ids = _result("ids", ids, (B,), torch.int32, dev)
+    probs = _result("probs", probs, (B,), torch.float32, dev)
+    if B:
+        ws = _scratch(ws, lambda: load_library().sample_logits_workspace_bytes(B, V), dev)
+        _call("sample_logits", dev, logits.data_ptr(), OUT_F32 if logits.dtype == torch.float32 else OUT_BF16, B, V,
+              u.data_ptr(), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), ids.data_ptr(), probs.data_ptr(),
+              ws.data_ptr(), ws.numel())
+    return ids, probs

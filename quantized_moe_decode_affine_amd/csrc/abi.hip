@@ -237,6 +237,11 @@ int mx4_experts_check(const q4moe_mx4_experts* L, int64_t T, int64_t top_k, q4mo
   return Q4MOE_OK;
 }
 
+int sample_check(int64_t B, int64_t V) {
+  if (B < 0 || V < 1) return Q4MOE_EINVAL;
+  return V > q4moe::kMaxSampleVocab || B > 65536 ? Q4MOE_EUNSUPPORTED : Q4MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -729,6 +734,37 @@ int moe_experts_mx4(const q4moe_mx4_experts* experts, const q4moe_bf16* X, int64
     if (clash({{workspace, need}}, {x, i, w, y})) return Q4MOE_EINVAL;
     return hip_status(q4moe::run_moe_experts_mx4(d, X, T, ids, weights, top_k, Y, out_dtype == Q4MOE_OUT_BF16,
                                                  workspace, (hipStream_t)stream));
+  } catch (...) {
+    return Q4MOE_EHIP;
+  }
+}
+
+size_t sample_logits_workspace_bytes(int64_t B, int64_t V) {
+  return sample_check(B, V) == Q4MOE_OK && B > 0 ? q4moe::sample_workspace_bytes(B, (int)V) : 0;
+}
+
+int sample_logits(const void* logits, int logits_dtype, int64_t B, int64_t V, const float* u, const float* temperature,
+                  const int32_t* top_k, const float* top_p, const float* min_p, int32_t* ids, float* probs,
+                  void* workspace, size_t workspace_bytes, q4moe_stream stream) {
+  try {
+    const int st = sample_check(B, V);
+    if (st != Q4MOE_OK) return st;
+    if (logits_dtype != Q4MOE_OUT_F32 && logits_dtype != Q4MOE_OUT_BF16) return Q4MOE_EINVAL;
+    const size_t each = logits_dtype == Q4MOE_OUT_F32 ? 4 : 2;
+    if (!logits || !aligned(logits, each) || !u || !ids) return Q4MOE_EINVAL;
+    for (const void* p : {(const void*)u, (const void*)temperature, (const void*)top_k, (const void*)top_p,
+                          (const void*)min_p, (const void*)ids, (const void*)probs})
+      if (!aligned(p, 4)) return Q4MOE_EINVAL;
+    if (B == 0) return Q4MOE_OK;
+    const size_t need = q4moe::sample_workspace_bytes(B, (int)V);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return Q4MOE_EWORKSPACE;
+    const size_t row = (size_t)B * 4;
+    auto opt = [&](const void* p) { return Span{p, p ? row : 0}; };
+    if (clash({{ids, row}, opt(probs), {workspace, need}},
+              {{logits, (size_t)B * V * each}, {u, row}, opt(temperature), opt(top_k), opt(top_p), opt(min_p)}))
+      return Q4MOE_EINVAL;
+    return hip_status(q4moe::run_sample(logits, logits_dtype == Q4MOE_OUT_BF16, B, (int)V, u, temperature, top_k, top_p,
+                                        min_p, ids, probs, workspace, (hipStream_t)stream));
   } catch (...) {
     return Q4MOE_EHIP;
   }

@@ -216,4 +216,11 @@ size_t experts_mx4_workspace_bytes(const Mx4Experts& L, int64_t T, int k);
 hipError_t run_moe_experts_mx4(const Mx4Experts& L, const uint16_t* X, int64_t T, const int32_t* ids,
                                const float* weights, int k, void* Y, int out_bf16, void* ws, hipStream_t stream);
 
+// ---- sampling (sample.hip): the filters' arrays and probs may be null
+constexpr int kMaxSampleVocab = 1 << 18;
+size_t sample_workspace_bytes(int64_t B, int V);
+hipError_t run_sample(const void* logits, int is_bf16, int64_t B, int V, const float* u, const float* temperature,
+                      const int32_t* top_k, const float* top_p, const float* min_p, int32_t* ids, float* probs, void* ws,
+                      hipStream_t stream);
+
 }  // namespace q4moe

@@ -12,48 +12,11 @@
 
 #include "int8.h"
 #include "kernels.h"
+#include "wave64.h"
 
 namespace q4moe {
 
 namespace {
-
-__device__ __forceinline__ uint64_t pair64(uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; }
-
-// The sum over the wave, in every lane; both partners of a step add the same two values.
-__device__ __forceinline__ double wave_sum_f64(double v) {
-  auto step = [&](uint32_t lo, uint32_t hi) { v += __longlong_as_double((long long)pair64(lo, hi)); };
-  auto lo = [&] { return (uint32_t)__double_as_longlong(v); };
-  auto hi = [&] { return (uint32_t)(__double_as_longlong(v) >> 32); };
-  step(dpp_u32<kDppQuadXor1>(lo()), dpp_u32<kDppQuadXor1>(hi()));
-  step(dpp_u32<kDppQuadXor2>(lo()), dpp_u32<kDppQuadXor2>(hi()));
-  step(dpp_u32<kDppRowHalfMirror>(lo()), dpp_u32<kDppRowHalfMirror>(hi()));
-  step(dpp_u32<kDppRowMirror>(lo()), dpp_u32<kDppRowMirror>(hi()));
-  auto swapped = [&](auto swap) {
-    uint32_t al, bl, ah, bh;
-    swap(lo(), al, bl);
-    swap(hi(), ah, bh);
-    v = __longlong_as_double((long long)pair64(al, ah)) + __longlong_as_double((long long)pair64(bl, bh));
-  };
-  swapped(swap_rows16);
-  swapped(swap_halves32);
-  return v;
-}
-
-// The largest of the wave, in every lane.
-__device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
-  auto step = [&](uint32_t lo, uint32_t hi) { v = max(v, pair64(lo, hi)); };
-  step(dpp_u32<kDppQuadXor1>((uint32_t)v), dpp_u32<kDppQuadXor1>((uint32_t)(v >> 32)));
-  step(dpp_u32<kDppQuadXor2>((uint32_t)v), dpp_u32<kDppQuadXor2>((uint32_t)(v >> 32)));
-  step(dpp_u32<kDppRowHalfMirror>((uint32_t)v), dpp_u32<kDppRowHalfMirror>((uint32_t)(v >> 32)));
-  step(dpp_u32<kDppRowMirror>((uint32_t)v), dpp_u32<kDppRowMirror>((uint32_t)(v >> 32)));
-  uint32_t al, bl, ah, bh;
-  swap_rows16((uint32_t)v, al, bl);
-  swap_rows16((uint32_t)(v >> 32), ah, bh);
-  v = max(pair64(al, ah), pair64(bl, bh));
-  swap_halves32((uint32_t)v, al, bl);
-  swap_halves32((uint32_t)(v >> 32), ah, bh);
-  return max(pair64(al, ah), pair64(bl, bh));
-}
 
 typedef uint16_t u16x8_t __attribute__((ext_vector_type(8)));
 
