@@ -13,14 +13,15 @@
 //
 // Up to three launches.  peak_kernel reads the logits once for the largest of every 64
 // consecutive ones (a part) and of every chunk.  Where top-k rules, the k-th largest of the
-// parts' maxima is a bound that at least k tokens reach, so draw_kernel, one workgroup for such a
-// row, reads only the parts that reach it, lists their tokens in LDS, and finds the last
-// token kept and the draw in the list.  A top-p without such a top-k needs the whole row's weights:
-// band_kernel sums them by bins of max - l (bins as fine as 2^-7 of the distance) and finds
-// the bin in which the filter ends; draw_kernel, on all chunks, adds up what lies above that
-// bin, lists the bin, and the last workgroup of the row to arrive finds the token.  Without
-// either filter draw_kernel adds up the chunks.  Where a list would overflow (many equal
-// logits) the last workgroup selects from the row itself, digit by digit.
+// parts' maxima is a bound that at least k tokens reach, so one workgroup of front_kernel
+// reads only the parts that reach it, lists their tokens in LDS, and finds the last
+// token kept and the draw in the list.  A top-p without such a top-k needs the whole row's
+// weights: other workgroups of front_kernel add them by bins of (max - l) / t (bins as fine as 2^-8
+// of it) and find the bin in which the filter ends; row_kernel, on all chunks, adds up what
+// lies above that bin for every 1,024 tokens (a step), lists the bin, and the last workgroup of
+// the row to arrive finds the token.  Without either filter row_kernel adds up the steps.
+// Steps whose parts' maxima reach nothing that is kept are not read.  Where a list would
+// overflow (many equal logits) a workgroup selects from the row itself, digit by digit.
 #include <algorithm>
 
 #include "kernels.h"
@@ -30,26 +31,27 @@ namespace q4moe {
 
 namespace {
 
-constexpr int kThreads = 256, kWaves = kThreads / kWave;
 constexpr int kPart = 64;         // tokens of a part
+constexpr int kStep = 1024;       // tokens of a step, one wave's at a time
 constexpr int kMaxChunks = 128;   // of a row
-constexpr int kMaxSteps = 256;    // of a chunk: 64 * kPer tokens each
+constexpr int kMaxSteps = kMaxSampleVocab / kStep;
 constexpr int kList = 2048;       // tokens of a row's list
 constexpr int kTopMost = 1024;    // the largest top-k that goes by parts
-constexpr int kBinBits = 12, kBins = 1 << kBinBits;
+constexpr int kBins = 4096;
+constexpr int kDigits = 2048;     // of a selection's level
 constexpr int kWordBits = 50, kIndexBits = 18;
 constexpr uint64_t kIndexMask = (1ull << kIndexBits) - 1;
-constexpr double kOne = 35184372088832.0;  // 2^45: the largest logit's weight
+constexpr int kOneBits = 45;      // the largest logit's weight is 2^45
 
 static_assert(kMaxSampleVocab == 1 << kIndexBits, "an index fits its bits");
 
 // A row's state between the launches.
 struct RowState {
-  unsigned band_arrived, draw_arrived, listed, pad;
-  unsigned expected;            // tokens in the bins that are listed
-  int b_lo, b_hi;               // these bins; b_lo = kBins: none
-  unsigned c_base;              // tokens in the bins before b_lo
-  uint64_t w_base, total;       // their weight, and the row's
+  unsigned band_arrived, row_arrived, listed, over;  // over: top-k's list overflowed
+  int b_lo, b_hi;               // the bins that are listed; b_lo = kBins: none
+  unsigned c_base;              // top-k: tokens in the bins before b_lo
+  int k;                        // top-k among the tokens that have a weight, 0: none
+  uint64_t w_base, total;       // weight of the bins before b_lo, and the row's
 };
 
 struct SampleArgs {
@@ -62,11 +64,11 @@ struct SampleArgs {
   int32_t* ids;
   float* probs;
   int G, chunk, M;              // chunks of a row, tokens of a chunk, parts of a row
-  uint64_t* peaks;              // [B][G] the chunk's largest word: ordered bits, index inverted
+  uint64_t* peaks;              // [B][G] the chunk's largest word
   float* parts;                 // [B][M]
   uint32_t* counts;             // [B][kBins]
   uint64_t* weights;            // [B][kBins]
-  uint64_t* sums;               // [B][G]
+  uint64_t* sums;               // [B][kMaxSteps]
   uint64_t* list;               // [B][kList]
   RowState* state;              // [B]
 };
@@ -75,7 +77,7 @@ enum Kind { kGreedy, kAll, kTop, kBand, kSum };
 
 struct RowRule {
   Kind kind;
-  double inv_t, p, m;           // m: 0 without min-p
+  double scale, p, m;           // scale: log2(e) / t; m: 0 without min-p
   int k;                        // 0 without top-k
   bool p_on;
 };
@@ -85,16 +87,16 @@ __device__ __forceinline__ RowRule row_rule(const SampleArgs& a, int64_t b) {
   const float t = a.temperature ? a.temperature[b] : 1.0f;
   const int k = a.top_k ? a.top_k[b] : 0;
   const float p = a.top_p ? a.top_p[b] : 1.0f, m = a.min_p ? a.min_p[b] : 0.0f;
-  r.inv_t = 1.0 / (double)t;
+  r.scale = 1.4426950408889634 / (double)t;
   r.k = k > 0 && k < a.V ? k : 0;
   r.p_on = p < 1.0f;
   r.p = p > 0.0f ? (double)p : 0.0;
   r.m = m > 0.0f ? fmin((double)m, 1.0) : 0.0;
-  r.kind = !(t > 0.0f)                                ? kGreedy
-           : a.V <= kList                             ? kAll
-           : r.k && r.k <= min(a.M / 2, kTopMost)     ? kTop
-           : r.k || r.p_on                            ? kBand
-                                                      : kSum;
+  r.kind = !(t > 0.0f)                            ? kGreedy
+           : a.V <= kList                         ? kAll
+           : r.k && r.k <= min(a.M / 2, kTopMost) ? kTop
+           : r.k || r.p_on                        ? kBand
+                                                  : kSum;
   return r;
 }
 
@@ -107,19 +109,19 @@ __device__ __forceinline__ float one_logit(const In* row, int i) {
   else return clean(row[i]);
 }
 
-// 16 bytes of consecutive logits from i on; closed past the row's end.
+// 16 bytes of consecutive logits from i on; closed from `end` on.
 template <typename In>
 struct Logits {
   static constexpr int kPer = 16 / sizeof(In);
   In raw[kPer];
-  __device__ __forceinline__ void load(const In* row, int i, int V) {
-    if (i + kPer <= V) {
+  __device__ __forceinline__ void load(const In* row, int i, int end) {
+    if (i + kPer <= end) {
       __builtin_memcpy(raw, row + i, 16);
     } else {
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
-        if constexpr (sizeof(In) == 2) raw[j] = i + j < V ? row[i + j] : (In)0xFF80;
-        else raw[j] = i + j < V ? row[i + j] : -__builtin_inff();
+        if constexpr (sizeof(In) == 2) raw[j] = i + j < end ? row[i + j] : (In)0xFF80;
+        else raw[j] = i + j < end ? row[i + j] : -__builtin_inff();
       }
     }
   }
@@ -136,36 +138,65 @@ __device__ __forceinline__ uint64_t word_of(float l, int i) {
 __device__ __forceinline__ int index_of(uint64_t word) { return (int)(kIndexMask - (word & kIndexMask)); }
 __device__ __forceinline__ float logit_of(uint64_t word) { return key_float((uint32_t)(word >> kIndexBits)); }
 
-// Bins of the distance from the largest logit, as fine as its exponent and 7 bits from 2^-16
-// to 2^16; they follow the order of the logits.
-__device__ __forceinline__ int bin_of(float l, float top) {
-  const float d = l == top ? 0.0f : top - l;
-  constexpr int kFirst = (127 - 16) << 7;
-  return min(max((int)(__float_as_uint(d) >> 16) - kFirst, 0), kBins - 1);
-}
+// 2^(-j/64), the fractions of the weights' exponential.
+struct Powers {
+  double of[64];
+  __device__ __forceinline__ void fill() {
+    if (threadIdx.x < 64) of[threadIdx.x] = exp2(-(double)threadIdx.x / 64.0);
+  }
+};
 
-// Whether a logit has a weight at all: closed ones and those beyond 2^-46 of the largest have none, and
-// change no filter's end.
-__device__ __forceinline__ bool weighs(float l, float top, double inv_t) {
-  return l == top || ((double)top - (double)l) * inv_t < 32.0;
-}
+// A row's weights.
+struct Weights {
+  const Powers* pow;
+  double top, scale;
+  float top_f, scale_f;
+  __device__ __forceinline__ Weights(const Powers* powers, float top_, double scale_)
+      : pow(powers), top((double)top_), scale(scale_), top_f(top_), scale_f((float)scale_) {}
 
-// A token's weight; 0 where min-p drops it, and beyond 2^-46 of the largest.
-__device__ __forceinline__ uint64_t weight_of(float l, float top, double inv_t, double m) {
-  if (l == top) return (uint64_t)kOne;
-  const double x = ((double)top - (double)l) * inv_t;
-  if (!(x < 32.0)) return 0;  // closed ones among them
-  const double e = exp(-x);
-  if (e < m) return 0;
-  // rounded to an integer by the addition: the low bits of 2^52 + v
-  return (uint64_t)__double_as_longlong(e * kOne + 4503599627370496.0) & ((1ull << 52) - 1);
-}
+  // (max - l) / t in powers of two.
+  __device__ __forceinline__ double distance(float l) const { return l == top_f ? 0.0 : (top - (double)l) * scale; }
+
+  // Closed logits and those beyond 2^-46 of the largest have no weight, and change no
+  // filter's end.
+  __device__ __forceinline__ bool weighs(float l) const { return distance(l) < 46.0; }
+
+  // 0 where min-p drops it, too.  2^-y for y = n / 64 + r: the table's value for n % 64 with n / 64
+  // off its exponent, times exp(-r ln 2) by its series to the fifth power (|r| <= 2^-7: 2^-52 of it is left out).
+  __device__ __forceinline__ uint64_t operator()(float l, double m) const {
+    const double y = distance(l);
+    if (!(y < 46.0)) return 0;
+    constexpr double kMagic = 6755399441055744.0;  // 1.5 * 2^52: the sum's low bits hold the integer
+    const double z = fma(y, 64.0, kMagic);
+    const uint32_t n = (uint32_t)__double_as_longlong(z);
+    const double r = fma(z - kMagic, -1.0 / 64.0, y);
+    constexpr double k1 = -0.69314718055994530942, k2 = k1 * k1 / 2, k3 = k2 * k1 / 3, k4 = k3 * k1 / 4, k5 = k4 * k1 / 5;
+    const double s = fma(fma(fma(fma(fma(k5, r, k4), r, k3), r, k2), r, k1), r, 1.0);
+    const uint64_t t = (uint64_t)__double_as_longlong(pow->of[n & 63]) - ((uint64_t)(n >> 6) << 52);
+    const double e = __longlong_as_double((long long)t) * s;
+    if (e < m) return 0;
+    // rounded to an integer by the addition: the low bits of 2^52 + v
+    constexpr double kOne = (double)(1ull << kOneBits);
+    return (uint64_t)__double_as_longlong(fma(e, kOne, 4503599627370496.0)) & ((1ull << 52) - 1);
+  }
+
+  // Bins of the distance, as fine as its exponent and 8 bits from 2^-10 to 2^6; they follow the
+  // order of the logits.
+  __device__ __forceinline__ int bin(float l) const {
+    const float d = l == top_f ? 0.0f : (top_f - l) * scale_f;
+    constexpr int kFirst = (127 - 10) << 8;
+    return min(max((int)(__float_as_uint(d) >> 15) - kFirst, 0), kBins - 1);
+  }
+};
 
 __device__ __forceinline__ uint64_t ld64(const uint64_t* p) {
   return __hip_atomic_load(const_cast<uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 __device__ __forceinline__ void st64(uint64_t* p, uint64_t v) {
   __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void add64(uint64_t* lds, uint64_t v) {
+  atomicAdd(reinterpret_cast<unsigned long long*>(lds), (unsigned long long)v);
 }
 
 // Whether this is the last of n workgroups to come here; what the others stored or added
@@ -181,11 +212,12 @@ __device__ __forceinline__ bool last_to_arrive(unsigned* count, unsigned n) {
 
 // ---- the largest of every part and chunk
 // Bound by the logits' bytes.  Also clears what the row's other launches count in.
+constexpr int kPeakThreads = 256;
 template <typename In>
-__global__ __launch_bounds__(kThreads) void peak_kernel(SampleArgs a) {
+__global__ __launch_bounds__(kPeakThreads) void peak_kernel(SampleArgs a) {
   constexpr int kPer = Logits<In>::kPer, kLanes = kPart / kPer;  // lanes to a part
-  constexpr int kUnroll = 4;
-  __shared__ uint64_t s_best[kWaves];
+  constexpr int kUnroll = 4, kThreads = kPeakThreads;
+  __shared__ uint64_t s_best[kThreads / kWave];
   const int64_t b = blockIdx.x / a.G;
   const int g = blockIdx.x % a.G;
   const In* row = static_cast<const In*>(a.logits) + b * a.V;
@@ -223,7 +255,7 @@ __global__ __launch_bounds__(kThreads) void peak_kernel(SampleArgs a) {
   __syncthreads();
   if (threadIdx.x == 0) {
 #pragma unroll
-    for (int o = 1; o < kWaves; ++o) w = max(w, s_best[o]);
+    for (int o = 1; o < kThreads / kWave; ++o) w = max(w, s_best[o]);
     a.peaks[b * a.G + g] = w;
     if (g == 0) {
       RowState s{};
@@ -231,7 +263,7 @@ __global__ __launch_bounds__(kThreads) void peak_kernel(SampleArgs a) {
       a.state[b] = s;
     }
   }
-  if (a.counts && row_rule(a, b).kind == kBand) {
+  if (row_rule(a, b).kind == kBand) {
     for (int i = g * kThreads + threadIdx.x; i < kBins; i += a.G * kThreads) {
       a.counts[b * kBins + i] = 0;
       a.weights[b * kBins + i] = 0;
@@ -241,17 +273,20 @@ __global__ __launch_bounds__(kThreads) void peak_kernel(SampleArgs a) {
 
 // The row's largest word; every wave for itself.
 __device__ __forceinline__ uint64_t row_peak(const SampleArgs& a, int64_t b) {
-  uint64_t w = 0;
-  for (int i = lane_id(); i < a.G; i += kWave) w = max(w, a.peaks[b * a.G + i]);
-  return wave_max_u64(w);
+  static_assert(kMaxChunks == 2 * kWave, "two a lane");
+  const int i = lane_id();
+  const uint64_t v = i < a.G ? a.peaks[b * a.G + i] : 0, w = i + kWave < a.G ? a.peaks[b * a.G + i + kWave] : 0;
+  return wave_max_u64(max(v, w));
 }
 
-// Exclusive prefix of (count, weight) over the workgroup's threads, and the totals.
+// Sums before a thread over the workgroup's kThreads, and their total.
 struct Pair {
   uint32_t c;
   uint64_t w;
 };
+template <int kThreads>
 __device__ __forceinline__ Pair block_before(Pair mine, Pair* total) {
+  constexpr int kWaves = kThreads / kWave;
   __shared__ uint32_t s_c[kWaves];
   __shared__ uint64_t s_w[kWaves];
   const int wave = threadIdx.x / kWave;
@@ -275,6 +310,18 @@ __device__ __forceinline__ Pair block_before(Pair mine, Pair* total) {
   *total = all;
   return before;
 }
+template <int kThreads>
+__device__ __forceinline__ uint64_t block_sum(uint64_t mine) {
+  __shared__ uint64_t s_w[kThreads / kWave];
+  mine = wave_sum_u64(mine);
+  __syncthreads();  // an earlier call's are read
+  if (lane_id() == 0) s_w[threadIdx.x / kWave] = mine;
+  __syncthreads();
+  uint64_t all = 0;
+#pragma unroll
+  for (int o = 0; o < kThreads / kWave; ++o) all += s_w[o];
+  return all;
+}
 
 // The least whole number that is at least p z, and 1 at least: a sum reaches p z when it
 // reaches this.
@@ -283,222 +330,7 @@ __device__ __forceinline__ uint64_t share_of(double p, uint64_t z) {
   return v < 1.0 ? 1 : min((uint64_t)v, z);
 }
 
-// ---- weights by bins, for rows whose top-p (or large top-k) ends somewhere in the row
-template <typename In>
-__global__ __launch_bounds__(kThreads) void band_kernel(SampleArgs a) {
-  __shared__ uint64_t s_w[kBins];
-  __shared__ uint32_t s_c[kBins];
-  __shared__ int s_bin;
-  __shared__ Pair s_before;
-  constexpr int kPer = Logits<In>::kPer;
-  const int64_t b = blockIdx.x / a.G;
-  const int g = blockIdx.x % a.G;
-  const RowRule r = row_rule(a, b);
-  if (r.kind != kBand) return;
-  const float top = logit_of(row_peak(a, b));
-  if (top == -__builtin_inff()) return;
-  for (int i = threadIdx.x; i < kBins; i += kThreads) {
-    s_w[i] = 0;
-    s_c[i] = 0;
-  }
-  __syncthreads();
-  const In* row = static_cast<const In*>(a.logits) + b * a.V;
-  const int end = min((g + 1) * a.chunk, a.V);
-  for (int i = g * a.chunk + (int)threadIdx.x * kPer; i < end; i += kThreads * kPer) {
-    Logits<In> v;
-    v.load(row, i, end);
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const float l = v.at(j);
-      const uint64_t w = weight_of(l, top, r.inv_t, 0.0);
-      if (w == 0) continue;  // weightless tokens change no filter's end
-      const int bin = bin_of(l, top);
-      atomicAdd(reinterpret_cast<unsigned long long*>(&s_w[bin]), (unsigned long long)w);
-      atomicAdd(&s_c[bin], 1u);
-    }
-  }
-  __syncthreads();
-  uint32_t* counts = a.counts + b * kBins;
-  uint64_t* weights = a.weights + b * kBins;
-  for (int i = threadIdx.x; i < kBins; i += kThreads) {
-    if (s_c[i] == 0) continue;
-    __hip_atomic_fetch_add(&counts[i], s_c[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __hip_atomic_fetch_add(&weights[i], s_w[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
-  if (!last_to_arrive(&a.state[b].band_arrived, a.G)) return;
-
-  // the row's bins, and the ones in which the filters end
-  for (int i = threadIdx.x; i < kBins; i += kThreads) {
-    s_c[i] = __hip_atomic_load(&counts[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    s_w[i] = ld64(&weights[i]);
-  }
-  __syncthreads();
-  constexpr int kOwn = kBins / kThreads;
-  const int own = threadIdx.x * kOwn;
-  Pair mine{0, 0}, total;
-  for (int i = 0; i < kOwn; ++i) {
-    mine.c += s_c[own + i];
-    mine.w += s_w[own + i];
-  }
-  const Pair before = block_before(mine, &total);
-  // the first bin with which the count or the weight reaches its mark, and what lies before it
-  auto find = [&](uint32_t need_c, uint64_t need_w) {
-    Pair at = before;
-    for (int i = 0; i < kOwn; ++i) {
-      const Pair with{at.c + s_c[own + i], at.w + s_w[own + i]};
-      const bool reached = need_c ? at.c < need_c && with.c >= need_c : at.w < need_w && with.w >= need_w;
-      if (reached) {
-        s_bin = own + i;
-        s_before = at;
-      }
-      at = with;
-    }
-    __syncthreads();
-  };
-  RowState* st = &a.state[b];
-  const bool k_on = r.k && (uint32_t)r.k <= total.c;
-  int lo = kBins, hi = kBins;
-  Pair base = total;
-  uint64_t z = total.w;
-  if (k_on) {
-    find((uint32_t)r.k, 0);
-    lo = hi = s_bin;
-    base = s_before;
-    z = base.w;  // what top-k keeps is at least that
-    __syncthreads();
-  }
-  if (r.p_on && (!k_on || z > 0)) {
-    find(0, share_of(r.p, z));
-    lo = s_bin;
-    base = s_before;
-    if (!k_on) hi = lo;
-    __syncthreads();
-  } else if (r.p_on) {  // the first bin has the end of both
-    lo = 0;
-    base = Pair{0, 0};
-  }
-  Pair in{0, 0};
-  for (int i = 0; i < kOwn; ++i)
-    if (own + i >= lo && own + i <= hi) in.c += s_c[own + i];
-  Pair listed;
-  block_before(in, &listed);
-  if (threadIdx.x == 0) {  // read by the next launch
-    st->expected = listed.c;
-    st->b_lo = lo;
-    st->b_hi = hi;
-    st->c_base = base.c;
-    st->w_base = base.w;
-    st->total = total.w;
-  }
-}
-
-// ---- the draw
-constexpr int kDigits = 2048;
-
-struct DrawShared {
-  uint64_t list[kList];
-  union {
-    struct {
-      uint64_t w[kDigits];
-      uint32_t c[kDigits];
-    } digit;
-    uint32_t bins[kBins];
-    uint16_t parts[kBins];
-  };
-  uint64_t sums[kMaxChunks > kMaxSteps ? kMaxChunks : kMaxSteps];
-  uint64_t w, word;
-  uint32_t c, n;
-  int at, parts_n;
-};
-
-// The word at which the count or the weight of the words from the largest on reaches its mark:
-// need_c words, or need_w of weight.  each(visit) calls visit(word, weight) for this thread's share
-// of the words; `bits` of them are compared, by digits of at most 11.  Returns the lowest
-// word of those kept (its untold bits zero) and, in `with`, what is kept with it.
-template <typename Each>
-__device__ __forceinline__ uint64_t select_word(DrawShared& s, int bits, uint32_t need_c, uint64_t need_w, Each each,
-                                                Pair* with) {
-  uint64_t prefix = 0;
-  Pair above{0, 0};
-  const uint64_t mask = bits < 64 ? (1ull << bits) - 1 : ~0ull;
-  int left = bits;
-  while (true) {
-    const int take = min(left, left > 18 ? 11 : 9);
-    const int rest = left - take;
-    for (int i = threadIdx.x; i < kDigits; i += kThreads) {
-      s.digit.w[i] = 0;
-      s.digit.c[i] = 0;
-    }
-    if (threadIdx.x == 0) s.at = -1;
-    __syncthreads();
-    each([&](uint64_t word, uint64_t w) {
-      word &= mask;
-      if ((left < 64 ? word >> left : 0) != prefix) return;
-      const int d = (int)(word >> rest) & ((1 << take) - 1);
-      atomicAdd(reinterpret_cast<unsigned long long*>(&s.digit.w[d]), (unsigned long long)w);
-      atomicAdd(&s.digit.c[d], 1u);
-    });
-    __syncthreads();
-    // digits from the largest down, eight a thread
-    constexpr int kOwn = kDigits / kThreads;
-    const int own = kDigits - 1 - (int)threadIdx.x * kOwn;
-    Pair mine{0, 0}, total;
-    for (int i = 0; i < kOwn; ++i) {
-      mine.c += s.digit.c[own - i];
-      mine.w += s.digit.w[own - i];
-    }
-    Pair at = block_before(mine, &total);
-    at.c += above.c;
-    at.w += above.w;
-    for (int i = 0; i < kOwn; ++i) {
-      const Pair in{s.digit.c[own - i], s.digit.w[own - i]};
-      const Pair up{at.c + in.c, at.w + in.w};
-      // the mark is reached here, or with the last of the words where it is beyond them all
-      const bool reached = need_c ? at.c < need_c && up.c >= need_c : at.w < need_w && up.w >= need_w;
-      const bool end = in.c && up.c == above.c + total.c && (need_c ? up.c < need_c : up.w < need_w);
-      if (reached || end) {
-        s.at = own - i;
-        s.c = at.c;
-        s.w = at.w;
-      }
-      at = up;
-    }
-    __syncthreads();
-    const int d = s.at;
-    if (d < 0) {  // no word at all
-      *with = above;
-      __syncthreads();
-      return 0;
-    }
-    above = Pair{s.c, s.w};
-    const Pair in{s.digit.c[d], s.digit.w[d]};
-    *with = Pair{above.c + in.c, above.w + in.w};
-    prefix = prefix << take | (uint64_t)d;
-    left = rest;
-    __syncthreads();
-    if (left == 0 || in.c == 1 || (need_c && with->c == need_c)) return prefix << left;
-  }
-}
-
-// The first of n values (n <= 256, in LDS) with which their sum exceeds t, and the sum before it;
-// every thread gets both.
-__device__ __forceinline__ int first_beyond(DrawShared& s, int n, uint64_t t, uint64_t* before) {
-  const int i = threadIdx.x;
-  const Pair mine{0, i < n ? s.sums[i] : 0};
-  Pair total;
-  const Pair at = block_before(mine, &total);
-  if (at.w <= t && at.w + mine.w > t) {
-    s.at = i;
-    s.w = at.w;
-  }
-  __syncthreads();
-  const int found = s.at;
-  *before = s.w;
-  __syncthreads();
-  return found;
-}
-static_assert(kMaxSteps <= kThreads && kMaxChunks <= kThreads, "a thread for each");
-
+// The draw's place among `total` of weight: the chosen token's running sum is the first beyond it.
 __device__ __forceinline__ uint64_t mark_of(const SampleArgs& a, int64_t b, uint64_t total) {
   const float u = a.u[b];
   const double x = u > 0.0f ? fmin((double)u, 1.0) : 0.0;
@@ -510,188 +342,559 @@ __device__ __forceinline__ void answer(const SampleArgs& a, int64_t b, int id, d
   if (a.probs) a.probs[b] = (float)prob;
 }
 
-// The last token that the filters keep, as its word, from a list of n words in LDS: they are all tokens
+// ---- selection among words
+struct Levels {
+  uint64_t w[kDigits];
+  uint32_t c[kDigits];
+  uint64_t found_w;
+  uint32_t found_c;
+  int at;
+};
+
+// The word at which the count or the weight of the words from the largest on reaches its mark:
+// need_c words, or need_w of weight.  each(visit) calls visit(word, weight) for this thread's share
+// of the words; `bits` of them are compared, by digits of at most 11.  Returns a word that
+// all kept ones reach and no others (of those visited), its untold bits zero, and in `with` what is
+// kept.
+template <int kThreads, typename Each>
+__device__ __forceinline__ uint64_t select_word(Levels& s, int bits, uint32_t need_c, uint64_t need_w, Each each,
+                                                Pair* with) {
+  uint64_t prefix = 0;
+  Pair above{0, 0};
+  const uint64_t mask = (1ull << bits) - 1;
+  int left = bits;
+  while (true) {
+    const int take = min(left, left > 18 ? 11 : 9);
+    const int rest = left - take;
+    for (int i = threadIdx.x; i < kDigits; i += kThreads) {
+      s.w[i] = 0;
+      s.c[i] = 0;
+    }
+    if (threadIdx.x == 0) s.at = -1;
+    __syncthreads();
+    each([&](uint64_t word, uint64_t w) {
+      word &= mask;
+      if (word >> left != prefix) return;
+      const int d = (int)(word >> rest) & ((1 << take) - 1);
+      add64(&s.w[d], w);
+      atomicAdd(&s.c[d], 1u);
+    });
+    __syncthreads();
+    // digits from the largest down
+    constexpr int kOwn = kDigits / kThreads;
+    const int own = kDigits - 1 - (int)threadIdx.x * kOwn;
+    Pair mine{0, 0}, total;
+    for (int i = 0; i < kOwn; ++i) {
+      mine.c += s.c[own - i];
+      mine.w += s.w[own - i];
+    }
+    Pair at = block_before<kThreads>(mine, &total);
+    at.c += above.c;
+    at.w += above.w;
+    for (int i = 0; i < kOwn; ++i) {
+      const Pair in{s.c[own - i], s.w[own - i]};
+      const Pair up{at.c + in.c, at.w + in.w};
+      // the mark is reached here, or with the last of the words where it is beyond them all
+      const bool reached = need_c ? at.c < need_c && up.c >= need_c : at.w < need_w && up.w >= need_w;
+      const bool end = in.c && up.c == above.c + total.c && (need_c ? up.c < need_c : up.w < need_w);
+      if (reached || end) {
+        s.at = own - i;
+        s.found_c = at.c;
+        s.found_w = at.w;
+      }
+      at = up;
+    }
+    __syncthreads();
+    const int d = s.at;
+    if (d < 0) {  // no word at all
+      *with = above;
+      __syncthreads();
+      return 0;
+    }
+    above = Pair{s.found_c, s.found_w};
+    const Pair in{s.c[d], s.w[d]};
+    *with = Pair{above.c + in.c, above.w + in.w};
+    prefix = prefix << take | (uint64_t)d;
+    left = rest;
+    __syncthreads();
+    if (left == 0 || in.c == 1 || (need_c && with->c == need_c)) return prefix << left;
+  }
+}
+
+// The last token that the filters keep, as its word among a list of n: all tokens
 // from the one after the first base.c of the order (their weight base.w) on, down to
 // the last that top-k may keep or, without top-k, to the end of the row (z = 0) or of the bin in
 // which top-p ends (z: the row's weight).
-__device__ __forceinline__ uint64_t last_kept(DrawShared& s, int n, const RowRule& r, float top, Pair base, uint64_t z) {
+template <int kThreads>
+__device__ __forceinline__ uint64_t last_kept(Levels& s, const uint64_t* list, int n, int k, bool p_on, double p,
+                                              const Weights& weight, Pair base, uint64_t z) {
   auto each = [&](auto visit) {
-    for (int i = threadIdx.x; i < n; i += kThreads) visit(s.list[i], weight_of(logit_of(s.list[i]), top, r.inv_t, 0.0));
+    for (int i = threadIdx.x; i < n; i += kThreads) visit(list[i], weight(logit_of(list[i]), 0.0));
   };
   uint64_t word = 0;
   Pair with;
-  if (r.k && (uint32_t)r.k < base.c + n) {
-    word = select_word(s, kWordBits, r.k - base.c, 0, each, &with);
+  if (k && (uint32_t)k < base.c + n) {
+    word = select_word<kThreads>(s, kWordBits, k - base.c, 0, each, &with);
     z = base.w + with.w;
-  } else if (r.k || z == 0) {  // all of them
-    Pair mine{0, 0}, total;
-    each([&](uint64_t, uint64_t w) { mine.w += w; });
-    block_before(mine, &total);
-    z = base.w + total.w;
+  } else if (k || z == 0) {  // all of them
+    uint64_t mine = 0;
+    each([&](uint64_t, uint64_t w) { mine += w; });
+    z = base.w + block_sum<kThreads>(mine);
   }
-  if (r.p_on) {
-    const uint64_t need = share_of(r.p, z);
-    word = max(word, select_word(s, kWordBits, 0, need > base.w ? need - base.w : 1, each, &with));
+  if (p_on) {
+    const uint64_t need = share_of(p, z);
+    word = max(word, select_word<kThreads>(s, kWordBits, 0, need > base.w ? need - base.w : 1, each, &with));
   }
   return word;
 }
 
+// ---- the second launch: rows that a list decides, and the bins of those that need them
+constexpr int kFrontThreads = 512, kFrontWaves = kFrontThreads / kWave;
+
+struct BandShared {
+  uint64_t w[kBins];
+  uint32_t c[kBins];
+  Pair before;
+  int bin;
+};
+
+struct PickShared {
+  alignas(16) uint64_t list[kList + 8];
+  union {
+    Levels levels;
+    uint32_t bins[kBins];
+    uint16_t parts[kBins];
+    alignas(16) uint64_t w[kFrontThreads + 8];
+  };
+  uint64_t word[kFrontWaves];
+  unsigned n, parts_n;
+  int at;
+};
+
+// Appends a wave's words to the list; what is beyond its end is counted only.
+template <int kN>
+__device__ __forceinline__ void append(uint64_t* list, unsigned* n, const bool (&want)[kN], const uint64_t (&word)[kN]) {
+  uint64_t ball[kN];
+  uint32_t all = 0;
+#pragma unroll
+  for (int j = 0; j < kN; ++j) {
+    ball[j] = __ballot(want[j]);
+    all += __popcll(ball[j]);
+  }
+  if (all == 0) return;
+  uint32_t base = 0;
+  if (lane_id() == 0) base = atomicAdd(n, all);
+  base = __builtin_amdgcn_readfirstlane(base);
+#pragma unroll
+  for (int j = 0; j < kN; ++j) {
+    const uint32_t at = base + __popcll(ball[j] & ((1ull << lane_id()) - 1ull));
+    if (want[j] && at < kList) list[at] = word[j];
+    base += __popcll(ball[j]);
+  }
+}
+
 // The draw from a list that holds every token kept.
-__device__ __forceinline__ void draw_from_list(DrawShared& s, int n, const SampleArgs& a, int64_t b, const RowRule& r,
-                                               float top) {
+__device__ __forceinline__ void draw_from_list(PickShared& s, int n, const SampleArgs& a, int64_t b, const RowRule& r,
+                                               const Weights& weight) {
+  constexpr int kThreads = kFrontThreads;
   if (n <= kThreads) {
-    // a token a thread: its place and the weight before it by comparison with all
-    const int i = threadIdx.x;
+    // A token a thread: its place and the weight before it by comparison with all, eight at a time.
+    const int i = threadIdx.x, n8 = (n + 7) & ~7;
     const bool here = i < n;
     const uint64_t word = here ? s.list[i] : 0;
-    uint64_t w = here ? weight_of(logit_of(word), top, r.inv_t, 0.0) : 0;
-    s.digit.w[i] = w;
+    uint64_t w = here ? weight(logit_of(word), 0.0) : 0;
+    s.w[i] = w;
+    if (i < 8) s.w[kThreads + i] = 0;
+    if (i < n8 - n) s.list[n + i] = 0;
     __syncthreads();
-    uint32_t place = 0;
-    uint64_t heavier = 0;
+    auto with_each = [&](auto visit) {
+      for (int j = 0; j < n8; j += 8) {
+        ulonglong2 q[4], v[4];
+#pragma unroll
+        for (int o = 0; o < 4; ++o) {
+          q[o] = *reinterpret_cast<const ulonglong2*>(&s.list[j + 2 * o]);
+          v[o] = *reinterpret_cast<const ulonglong2*>(&s.w[j + 2 * o]);
+        }
+#pragma unroll
+        for (int o = 0; o < 4; ++o) {
+          visit(q[o].x, v[o].x);
+          visit(q[o].y, v[o].y);
+        }
+      }
+    };
+    bool kept = here;
+    uint64_t total;
     if (r.k || r.p_on) {
-      for (int j = 0; j < n; ++j) {
-        const bool ahead = s.list[j] > word;
+      uint32_t place = 0;
+      uint64_t heavier = 0;
+      with_each([&](uint64_t other, uint64_t v) {
+        const bool ahead = other > word;
         place += ahead;
-        heavier += ahead ? s.digit.w[j] : 0;
+        heavier += ahead ? v : 0;
+      });
+      if (r.k) kept = kept && place < (uint32_t)r.k;
+      if (r.p_on) {
+        total = block_sum<kThreads>(kept ? w : 0);
+        kept = kept && heavier < share_of(r.p, total);
       }
     }
-    bool kept = here && (!r.k || place < (uint32_t)r.k);
-    Pair total;
-    block_before(Pair{0, kept ? w : 0}, &total);
-    if (r.p_on) kept = kept && heavier < share_of(r.p, total.w);
-    if (r.m > 0.0 && kept) w = weight_of(logit_of(word), top, r.inv_t, r.m);
+    if (r.m > 0.0 && kept) w = weight(logit_of(word), r.m);
     if (!kept) w = 0;
+    total = block_sum<kThreads>(w);  // (its barriers are after the loop's reads)
+    s.w[i] = w;
     __syncthreads();
-    s.digit.w[i] = w;
-    block_before(Pair{0, w}, &total);
-    const uint64_t t = mark_of(a, b, total.w);
+    const uint64_t t = mark_of(a, b, total), mine = word & kIndexMask;
     uint64_t before = 0;
-    for (int j = 0; j < n; ++j) before += index_of(s.list[j]) < index_of(word) ? s.digit.w[j] : 0;
-    if (here && before <= t && before + w > t) answer(a, b, index_of(word), (double)w / (double)total.w);
+    with_each([&](uint64_t other, uint64_t v) { before += (other & kIndexMask) > mine ? v : 0; });
+    if (here && before <= t && before + w > t) answer(a, b, index_of(word), (double)w / (double)total);
     return;
   }
-  Pair with, total;
-  const uint64_t last = last_kept(s, n, r, top, Pair{0, 0}, 0);
-  auto kept = [&](uint64_t word) -> uint64_t { return word >= last ? weight_of(logit_of(word), top, r.inv_t, r.m) : 0; };
-  Pair mine{0, 0};
-  for (int i = threadIdx.x; i < n; i += kThreads) mine.w += kept(s.list[i]);
-  block_before(mine, &total);
+  const uint64_t last = last_kept<kThreads>(s.levels, s.list, n, r.k, r.p_on, r.p, weight, Pair{0, 0}, 0);
+  auto kept = [&](uint64_t word) -> uint64_t { return word >= last ? weight(logit_of(word), r.m) : 0; };
+  uint64_t mine = 0;
+  for (int i = threadIdx.x; i < n; i += kThreads) mine += kept(s.list[i]);
+  const uint64_t total = block_sum<kThreads>(mine);
   // in the vocabulary's order: the inverted index from the largest down
-  const uint64_t mark = mark_of(a, b, total.w) + 1;
-  const uint64_t low = select_word(s, kIndexBits, 0, mark, [&](auto visit) {
+  Pair with;
+  const uint64_t low = select_word<kThreads>(s.levels, kIndexBits, 0, mark_of(a, b, total) + 1, [&](auto visit) {
     for (int i = threadIdx.x; i < n; i += kThreads)
       if (const uint64_t w = kept(s.list[i])) visit(s.list[i], w);
   }, &with);
   // the chosen one is the kept token of the lowest inverted index from `low` on
-  if (threadIdx.x == 0) s.word = kIndexMask;
+  if (threadIdx.x == 0) s.word[0] = kIndexMask;
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += kThreads) {
     const uint64_t at = s.list[i] & kIndexMask;
-    if (at >= low && kept(s.list[i])) atomicMin(reinterpret_cast<unsigned long long*>(&s.word), (unsigned long long)at);
+    if (at >= low && kept(s.list[i])) atomicMin(reinterpret_cast<unsigned long long*>(&s.word[0]), (unsigned long long)at);
   }
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += kThreads)
-    if ((s.list[i] & kIndexMask) == s.word && kept(s.list[i]))
-      answer(a, b, index_of(s.list[i]), (double)kept(s.list[i]) / (double)total.w);
+    if ((s.list[i] & kIndexMask) == s.word[0] && kept(s.list[i]))
+      answer(a, b, index_of(s.list[i]), (double)kept(s.list[i]) / (double)total);
 }
 
-// The draw from a row whose chunks' sums of kept weights are in s.sums: a kept token is one whose
-// word is at least `last`.
 template <typename In>
-__device__ __forceinline__ void draw_from_row(DrawShared& s, const SampleArgs& a, int64_t b, const RowRule& r, float top,
-                                              uint64_t last) {
-  constexpr int kPer = Logits<In>::kPer, kStep = kWave * kPer;
+__device__ __forceinline__ void pick(PickShared& s, Powers& powers, const SampleArgs& a, int64_t b) {
+  constexpr int kThreads = kFrontThreads;
+  constexpr int kOwnParts = kMaxSampleVocab / kPart / kThreads, kOwnAll = kList / kThreads;
   const In* row = static_cast<const In*>(a.logits) + b * a.V;
   const int wave = threadIdx.x / kWave, lane = lane_id();
-  Pair total;
-  block_before(Pair{0, (int)threadIdx.x < a.G ? s.sums[threadIdx.x] : 0}, &total);
-  uint64_t t = mark_of(a, b, total.w), before;
-  const int g = first_beyond(s, a.G, t, &before);
-  t -= before;
-  const int first = g * a.chunk, end = min(first + a.chunk, a.V), steps = (end - first + kStep - 1) / kStep;
-  auto kept = [&](float l, int i) -> uint64_t {
-    return word_of(l, i) >= last ? weight_of(l, top, r.inv_t, r.m) : 0;
-  };
-  for (int o = wave; o < steps; o += kWaves) {
-    const int i = first + o * kStep + lane * kPer;
-    Logits<In> v;
-    v.load(row, i, end);
-    uint64_t w = 0;
+  const bool small = a.V <= kList;
+  // what the row may need is on its way while its rule is read
+  float l[kOwnParts > kOwnAll ? kOwnParts : kOwnAll];
+  if (small) {
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) w += kept(v.at(j), i + j);
-    w = wave_sum_u64(w);
-    if (lane == 0) s.sums[o] = w;
+    for (int o = 0; o < kOwnAll; ++o) {
+      const int i = o * kThreads + threadIdx.x;
+      l[o] = i < a.V ? one_logit(row, i) : -__builtin_inff();
+    }
+  } else {
+#pragma unroll
+    for (int o = 0; o < kOwnParts; ++o) {
+      const int i = o * kThreads + threadIdx.x;
+      l[o] = i < a.M ? a.parts[b * a.M + i] : -__builtin_inff();
+    }
+  }
+  uint64_t peak = small ? 0 : row_peak(a, b);
+  const RowRule r = row_rule(a, b);
+  if (r.kind == kBand || r.kind == kSum) return;
+  powers.fill();
+  if (threadIdx.x == 0) s.n = s.parts_n = 0;
+  if (small) {
+#pragma unroll
+    for (int o = 0; o < kOwnAll; ++o) {
+      const int i = o * kThreads + threadIdx.x;
+      if (i < a.V) peak = max(peak, word_of(l[o], i));
+    }
+    peak = wave_max_u64(peak);
+    if (lane == 0) s.word[wave] = peak;
+    __syncthreads();
+#pragma unroll
+    for (int o = 0; o < kFrontWaves; ++o) peak = max(peak, s.word[o]);
+  }
+  const float top = logit_of(peak);
+  if (r.kind == kGreedy || top == -__builtin_inff()) {
+    const bool open = top != -__builtin_inff();
+    if (threadIdx.x == 0) answer(a, b, open ? index_of(peak) : -1, open ? 1.0 : 0.0);
+    return;
+  }
+  const Weights weight(&powers, top, r.scale);
+
+  if (r.kind == kAll) {
+    __syncthreads();
+    bool want[kOwnAll];
+    uint64_t word[kOwnAll];
+#pragma unroll
+    for (int o = 0; o < kOwnAll; ++o) {
+      const int i = o * kThreads + threadIdx.x;
+      want[o] = i < a.V && weight.weighs(l[o]);
+      word[o] = word_of(l[o], i);
+    }
+    append(s.list, &s.n, want, word);
+    __syncthreads();
+    draw_from_list(s, (int)s.n, a, b, r, weight);
+    return;
+  }
+
+  // the bin of the k-th largest of the parts' maxima
+  int bin[kOwnParts];
+#pragma unroll
+  for (int o = 0; o < kOwnParts; ++o) bin[o] = weight.weighs(l[o]) ? weight.bin(l[o]) : kBins;
+  for (int i = threadIdx.x; i < kBins; i += kThreads) s.bins[i] = 0;
+  if (threadIdx.x == 0) s.at = kBins - 1;  // fewer parts than k hold a token of any weight
+  __syncthreads();
+#pragma unroll
+  for (int o = 0; o < kOwnParts; ++o)
+    if (bin[o] < kBins) atomicAdd(&s.bins[bin[o]], 1u);
+  __syncthreads();
+  constexpr int kOwn = kBins / kThreads;
+  uint32_t in[kOwn];
+  Pair mine{0, 0}, total;
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) mine.c += in[i] = s.bins[threadIdx.x * kOwn + i];
+  uint32_t c = block_before<kThreads>(mine, &total).c;
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    if (c < (uint32_t)r.k && c + in[i] >= (uint32_t)r.k) s.at = threadIdx.x * kOwn + i;
+    c += in[i];
   }
   __syncthreads();
-  const int o = first_beyond(s, steps, t, &before);
-  t -= before;
-  if (wave == 0) {
-    const int i = first + o * kStep + lane * kPer;
+  const int bound = s.at;
+  // the parts that reach it, then their tokens that do
+#pragma unroll
+  for (int o = 0; o < kOwnParts; ++o)
+    if (bin[o] <= bound) s.parts[atomicAdd(&s.parts_n, 1u)] = (uint16_t)(o * kThreads + threadIdx.x);
+  __syncthreads();
+  constexpr int kUnroll = 8;
+  const int n = (int)s.parts_n;
+  for (int o = wave * kUnroll; o < n; o += kFrontWaves * kUnroll) {
+    float v[kUnroll];
+    bool want[kUnroll];
+    uint64_t word[kUnroll];
+    int i[kUnroll];
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j) {
+      i[j] = o + j < n ? s.parts[o + j] * kPart + lane : a.V;
+      v[j] = i[j] < a.V ? one_logit(row, i[j]) : -__builtin_inff();
+    }
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j) {
+      want[j] = weight.weighs(v[j]) && weight.bin(v[j]) <= bound;
+      word[j] = word_of(v[j], i[j]);
+    }
+    append(s.list, &s.n, want, word);
+  }
+  __syncthreads();
+  if (s.n <= kList) draw_from_list(s, (int)s.n, a, b, r, weight);
+  else if (threadIdx.x == 0) a.state[b].over = 1;  // row_kernel's
+}
+
+template <typename In>
+__device__ __forceinline__ void band(BandShared& s, Powers& powers, const SampleArgs& a, int64_t b, int g) {
+  constexpr int kThreads = kFrontThreads, kPer = Logits<In>::kPer;
+  const RowRule r = row_rule(a, b);
+  if (r.kind != kBand) return;
+  const float top = logit_of(row_peak(a, b));
+  if (top == -__builtin_inff()) return;
+  powers.fill();
+  for (int i = threadIdx.x; i < kBins; i += kThreads) {
+    s.w[i] = 0;
+    s.c[i] = 0;
+  }
+  __syncthreads();
+  const Weights weight(&powers, top, r.scale);
+  const In* row = static_cast<const In*>(a.logits) + b * a.V;
+  const int end = min((g + 1) * a.chunk, a.V);
+  for (int i = g * a.chunk + (int)threadIdx.x * kPer; i < end; i += kThreads * kPer) {
     Logits<In> v;
     v.load(row, i, end);
-    uint64_t w[kPer], mine = 0;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) mine += w[j] = kept(v.at(j), i + j);
-    uint64_t at = wave_prefix(mine) - mine;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      if (w[j] && at <= t && at + w[j] > t) answer(a, b, i + j, (double)w[j] / (double)total.w);
-      at += w[j];
+      const float l = v.at(j);
+      const uint64_t w = weight(l, 0.0);
+      if (w == 0) continue;
+      const int bin = weight.bin(l);
+      add64(&s.w[bin], w);
+      if (r.k) atomicAdd(&s.c[bin], 1u);
     }
+  }
+  __syncthreads();
+  uint32_t* counts = a.counts + b * kBins;
+  uint64_t* weights = a.weights + b * kBins;
+  for (int i = threadIdx.x; i < kBins; i += kThreads) {
+    if (s.w[i] == 0) continue;
+    __hip_atomic_fetch_add(&weights[i], s.w[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (r.k) __hip_atomic_fetch_add(&counts[i], s.c[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  if (!last_to_arrive(&a.state[b].band_arrived, a.G)) return;
+
+  // the row's bins, and the ones in which the filters end
+  for (int i = threadIdx.x; i < kBins; i += kThreads) {
+    s.w[i] = ld64(&weights[i]);
+    s.c[i] = r.k ? __hip_atomic_load(&counts[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
+  }
+  __syncthreads();
+  constexpr int kOwn = kBins / kThreads;
+  const int own = threadIdx.x * kOwn;
+  Pair mine{0, 0}, total;
+  for (int i = 0; i < kOwn; ++i) {
+    mine.c += s.c[own + i];
+    mine.w += s.w[own + i];
+  }
+  const Pair before = block_before<kThreads>(mine, &total);
+  // the first bin with which the count or the weight reaches its mark, and what lies before it
+  auto find = [&](uint32_t need_c, uint64_t need_w, Pair* base) {
+    Pair at = before;
+    for (int i = 0; i < kOwn; ++i) {
+      const Pair with{at.c + s.c[own + i], at.w + s.w[own + i]};
+      const bool reached = need_c ? at.c < need_c && with.c >= need_c : at.w < need_w && with.w >= need_w;
+      if (reached) {
+        s.bin = own + i;
+        s.before = at;
+      }
+      at = with;
+    }
+    __syncthreads();
+    const int bin = s.bin;
+    *base = s.before;
+    __syncthreads();
+    return bin;
+  };
+  const int k = r.k && (uint32_t)r.k <= total.c ? r.k : 0;
+  int lo = kBins, hi = kBins;
+  Pair base = total;
+  uint64_t z = total.w;
+  if (k) {
+    lo = hi = find((uint32_t)k, 0, &base);
+    z = base.w;  // what top-k keeps is at least that
+  }
+  if (r.p_on && z > 0) {
+    lo = find(0, share_of(r.p, z), &base);
+    if (!k) hi = lo;
+  } else if (r.p_on) {  // the first bin has the end of both
+    lo = 0;
+    base = Pair{0, 0};
+  }
+  if (threadIdx.x == 0) {  // read by the next launch
+    RowState* st = &a.state[b];
+    st->b_lo = lo;
+    st->b_hi = hi;
+    st->c_base = base.c;
+    st->k = k;
+    st->w_base = base.w;
+    st->total = total.w;
   }
 }
 
-// The draw from a row by this workgroup alone: the last token kept by digits of the row's words, then
-// the chunks' sums.  z: the row's weight, for a top-p without top-k.
+// Workgroups 0 .. rows - 1: a row each; the others: a chunk's bins.
 template <typename In>
-__device__ __noinline__ void draw_alone(DrawShared& s, const SampleArgs& a, int64_t b, const RowRule& r, float top,
-                                        uint64_t z) {
+__global__ __launch_bounds__(kFrontThreads, 2) void front_kernel(SampleArgs a, unsigned rows) {
+  __shared__ union Shared {
+    BandShared band;
+    PickShared pick;
+    __device__ Shared() {}
+  } s;
+  __shared__ Powers powers;
+  if (blockIdx.x < rows) pick<In>(s.pick, powers, a, blockIdx.x);
+  else band<In>(s.band, powers, a, (blockIdx.x - rows) / a.G, (blockIdx.x - rows) % a.G);
+}
+
+// ---- the third launch: rows by the sums of their steps
+constexpr int kRowThreads = 256, kRowWaves = kRowThreads / kWave;
+static_assert(kMaxSteps <= kRowThreads, "a thread for each step's sum");
+
+struct RowShared {
+  uint64_t list[kList];
+  Levels levels;
+  uint64_t sums[kMaxSteps];
+  uint64_t word, found_w;
+  unsigned n, base;
+  int at;
+};
+
+// The draw from a row whose steps' sums of kept weights are in s.sums: a kept token is one whose
+// word is at least `last`.
+template <typename In>
+__device__ __forceinline__ void draw_from_steps(RowShared& s, const SampleArgs& a, int64_t b, const RowRule& r,
+                                                const Weights& weight, uint64_t last) {
+  constexpr int kPer = Logits<In>::kPer, kLoads = kStep / kWave / kPer;
+  const int steps = (a.V + kStep - 1) / kStep, lane = lane_id();
+  const Pair mine{0, (int)threadIdx.x < steps ? s.sums[threadIdx.x] : 0};
+  Pair total;
+  const Pair at = block_before<kRowThreads>(mine, &total);
+  uint64_t t = mark_of(a, b, total.w);
+  if (at.w <= t && at.w + mine.w > t) {
+    s.at = threadIdx.x;
+    s.found_w = at.w;
+  }
+  __syncthreads();
+  if (threadIdx.x >= kWave) return;
+  t -= s.found_w;
+  const In* row = static_cast<const In*>(a.logits) + b * a.V;
+  Logits<In> v[kLoads];
+#pragma unroll
+  for (int o = 0; o < kLoads; ++o) v[o].load(row, s.at * kStep + (o * kWave + lane) * kPer, a.V);
+#pragma unroll
+  for (int o = 0; o < kLoads; ++o) {
+    const int i = s.at * kStep + (o * kWave + lane) * kPer;
+    uint64_t w[kPer], sum = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const float l = v[o].at(j);
+      sum += w[j] = word_of(l, i + j) >= last ? weight(l, r.m) : 0;
+    }
+    uint64_t up = wave_prefix(sum), before = up - sum;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      if (before <= t && before + w[j] > t) answer(a, b, i + j, (double)w[j] / (double)total.w);
+      before += w[j];
+    }
+    up = __shfl(up, kWave - 1, kWave);
+    if (t < up) break;  // uniform
+    t -= up;
+  }
+}
+
+// The draw by this workgroup alone: the last token kept by digits of the row's words, then the steps' sums.
+// z: the row's weight, for a top-p without top-k.
+template <typename In>
+__device__ __noinline__ void draw_alone(RowShared& s, const SampleArgs& a, int64_t b, const RowRule& r, int k,
+                                        const Weights& weight, uint64_t z) {
   const In* row = static_cast<const In*>(a.logits) + b * a.V;
   auto each = [&](auto visit) {
-    for (int i = threadIdx.x; i < a.V; i += kThreads) {
+    for (int i = threadIdx.x; i < a.V; i += kRowThreads) {
       const float l = one_logit(row, i);
-      if (const uint64_t w = weight_of(l, top, r.inv_t, 0.0)) visit(word_of(l, i), w);
+      if (const uint64_t w = weight(l, 0.0)) visit(word_of(l, i), w);
     }
   };
   uint64_t last = 0;
   Pair with;
-  if (r.k) {
-    last = select_word(s, kWordBits, r.k, 0, each, &with);
+  if (k) {
+    last = select_word<kRowThreads>(s.levels, kWordBits, k, 0, each, &with);
     z = with.w;
   }
-  if (r.p_on) last = max(last, select_word(s, kWordBits, 0, share_of(r.p, z), each, &with));
-  for (int g = threadIdx.x; g < a.G; g += kThreads) s.sums[g] = 0;
+  if (r.p_on) last = max(last, select_word<kRowThreads>(s.levels, kWordBits, 0, share_of(r.p, z), each, &with));
+  for (int i = threadIdx.x; i < kMaxSteps; i += kRowThreads) s.sums[i] = 0;
   __syncthreads();
   each([&](uint64_t word, uint64_t w) {
     if (word < last) return;
-    if (r.m > 0.0) w = weight_of(logit_of(word), top, r.inv_t, r.m);
-    atomicAdd(reinterpret_cast<unsigned long long*>(&s.sums[index_of(word) / a.chunk]), (unsigned long long)w);
+    if (r.m > 0.0) w = weight(logit_of(word), r.m);
+    add64(&s.sums[index_of(word) / kStep], w);
   });
   __syncthreads();
-  draw_from_row<In>(s, a, b, r, top, last);
-}
-
-// Appends a wave's words to the list in LDS; false where it is full.
-__device__ __forceinline__ void append(DrawShared& s, bool want, uint64_t word) {
-  const uint64_t ball = __ballot(want);
-  if (!ball) return;
-  uint32_t base = 0;
-  if (lane_id() == 0) base = atomicAdd(&s.n, (uint32_t)__popcll(ball));
-  base = __builtin_amdgcn_readfirstlane(base);
-  const uint32_t at = base + __popcll(ball & ((1ull << lane_id()) - 1ull));
-  if (want && at < kList) s.list[at] = word;
+  draw_from_steps<In>(s, a, b, r, weight, last);
 }
 
 template <typename In>
-__global__ __launch_bounds__(kThreads) void draw_kernel(SampleArgs a) {
-  __shared__ DrawShared s;
-  constexpr int kPer = Logits<In>::kPer, kStep = kWave * kPer;
+__global__ __launch_bounds__(kRowThreads, 3) void row_kernel(SampleArgs a) {
+  __shared__ RowShared s;
+  __shared__ Powers powers;
+  constexpr int kPer = Logits<In>::kPer, kLoads = kStep / kWave / kPer, kParts = kStep / kPart;
   const int64_t b = blockIdx.x / a.G;
   const int g = blockIdx.x % a.G;
   const RowRule r = row_rule(a, b);
-  const bool alone = r.kind == kGreedy || r.kind == kAll || r.kind == kTop;
-  if (alone && g > 0) return;
+  if (r.kind == kGreedy && a.top_k) return;  // front_kernel's
+  if (r.kind == kTop && (g > 0 || !a.state[b].over)) return;
   const uint64_t peak = row_peak(a, b);
   const float top = logit_of(peak);
   if (r.kind == kGreedy || top == -__builtin_inff()) {
@@ -699,190 +902,143 @@ __global__ __launch_bounds__(kThreads) void draw_kernel(SampleArgs a) {
     if (g == 0 && threadIdx.x == 0) answer(a, b, open ? index_of(peak) : -1, open ? 1.0 : 0.0);
     return;
   }
+  powers.fill();
+  if (threadIdx.x == 0) s.n = 0;
+  __syncthreads();
+  const Weights weight(&powers, top, r.scale);
+  if (r.kind == kTop) {
+    draw_alone<In>(s, a, b, r, r.k, weight, 0);
+    return;
+  }
+
+  // steps' sums; of a band's row those above the listed bins
+  const bool banded = r.kind == kBand;
+  const RowState* st = &a.state[b];
+  const int b_lo = banded ? st->b_lo : kBins, b_hi = banded ? st->b_hi : kBins;
   const In* row = static_cast<const In*>(a.logits) + b * a.V;
   const int wave = threadIdx.x / kWave, lane = lane_id();
-  if (threadIdx.x == 0) {
-    s.n = 0;
-    s.parts_n = 0;
-  }
-
-  if (r.kind == kAll) {
-    __syncthreads();
-    for (int i = threadIdx.x; i - lane < a.V; i += kThreads) {
-      const float l = i < a.V ? one_logit(row, i) : -__builtin_inff();
-      append(s, l != -__builtin_inff(), word_of(l, i));
-    }
-    __syncthreads();
-    draw_from_list(s, (int)s.n, a, b, r, top);
-    return;
-  }
-
-  if (r.kind == kTop) {
-    // the bin of the k-th largest of the parts' maxima
-    constexpr int kOwnParts = kMaxSampleVocab / kPart / kThreads;
-    const float* parts = a.parts + b * a.M;
-    int bin[kOwnParts];
-#pragma unroll
-    for (int o = 0; o < kOwnParts; ++o) {
-      const int i = o * kThreads + threadIdx.x;
-      const float l = i < a.M ? parts[i] : -__builtin_inff();
-      bin[o] = weighs(l, top, r.inv_t) ? bin_of(l, top) : kBins;
-    }
-    for (int i = threadIdx.x; i < kBins; i += kThreads) s.bins[i] = 0;
-    if (threadIdx.x == 0) s.at = kBins - 1;  // fewer parts than k hold a token of any weight
-    __syncthreads();
-#pragma unroll
-    for (int o = 0; o < kOwnParts; ++o)
-      if (bin[o] < kBins) atomicAdd(&s.bins[bin[o]], 1u);
-    __syncthreads();
-    constexpr int kOwn = kBins / kThreads;
-    Pair mine{0, 0}, total;
-    for (int i = 0; i < kOwn; ++i) mine.c += s.bins[threadIdx.x * kOwn + i];
-    uint32_t c = block_before(mine, &total).c;
-    for (int i = 0; i < kOwn; ++i) {
-      const uint32_t in = s.bins[threadIdx.x * kOwn + i];
-      if (c < (uint32_t)r.k && c + in >= (uint32_t)r.k) s.at = threadIdx.x * kOwn + i;
-      c += in;
-    }
-    __syncthreads();
-    const int bound = s.at;
-    // the parts that reach it, then their tokens that do
-#pragma unroll
-    for (int o = 0; o < kOwnParts; ++o)
-      if (bin[o] <= bound) s.parts[atomicAdd(&s.parts_n, 1)] = (uint16_t)(o * kThreads + threadIdx.x);
-    __syncthreads();
-    constexpr int kUnroll = 4;
-    const int n = s.parts_n;
-    for (int o = wave * kUnroll; o < n; o += kWaves * kUnroll) {
-      float l[kUnroll];
-      int i[kUnroll];
-#pragma unroll
-      for (int j = 0; j < kUnroll; ++j) {
-        i[j] = o + j < n ? s.parts[o + j] * kPart + lane : a.V;
-        l[j] = i[j] < a.V ? one_logit(row, i[j]) : -__builtin_inff();
-      }
-#pragma unroll
-      for (int j = 0; j < kUnroll; ++j)
-        append(s, weighs(l[j], top, r.inv_t) && bin_of(l[j], top) <= bound, word_of(l[j], i[j]));
-    }
-    __syncthreads();
-    if (s.n <= kList) draw_from_list(s, (int)s.n, a, b, r, top);
-    else draw_alone<In>(s, a, b, r, top, 0);
-    return;
-  }
-
-  // chunks' sums; of a band's row those above the listed bins
-  const RowState st = a.state[b];
-  const int b_lo = r.kind == kBand ? st.b_lo : kBins, b_hi = r.kind == kBand ? st.b_hi : kBins;
-  const bool listed = b_lo < kBins && st.expected <= kList, over = b_lo < kBins && !listed;
-  const int first = g * a.chunk, end = min(first + a.chunk, a.V);
-  uint64_t sum = 0;
-  __syncthreads();
-  if (!over) {
-    for (int i0 = first + wave * kStep; i0 < end; i0 += kWaves * kStep) {
-      const int i = i0 + lane * kPer;
-      Logits<In> v;
-      v.load(row, i, end);
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const float l = v.at(j);
-        const int bin = r.kind == kBand ? bin_of(l, top) : 0;
-        if (bin < b_lo) sum += weight_of(l, top, r.inv_t, r.m);
-        if (listed) append(s, bin >= b_lo && bin <= b_hi && weight_of(l, top, r.inv_t, 0.0), word_of(l, i + j));
+  const int end = min((g + 1) * a.chunk, a.V);
+  for (int i0 = g * a.chunk + wave * kStep; i0 < end; i0 += kRowWaves * kStep) {
+    if (banded || r.m > 0.0) {  // what the step's largest logit does not reach none does
+      const int i = i0 / kPart + lane;
+      float most = lane < kParts && i < a.M ? a.parts[b * a.M + i] : -__builtin_inff();
+      most = fmaxf(most, dpp_f32<kDppQuadXor1>(most));
+      most = fmaxf(most, dpp_f32<kDppQuadXor2>(most));
+      most = fmaxf(most, dpp_f32<kDppRowHalfMirror>(most));
+      most = fmaxf(most, dpp_f32<kDppRowMirror>(most));
+      most = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(most)));
+      // (the list holds what min-p drops, too: the other filters count it)
+      if (b_lo < kBins ? !weight.weighs(most) || weight.bin(most) > b_hi : !weight(most, r.m)) {
+        if (lane == 0) st64(&a.sums[b * kMaxSteps + i0 / kStep], 0);
+        continue;
       }
     }
+    Logits<In> v[kLoads];
+#pragma unroll
+    for (int o = 0; o < kLoads; ++o) v[o].load(row, i0 + (o * kWave + lane) * kPer, end);
+    uint64_t sum = 0;
+#pragma unroll
+    for (int o = 0; o < kLoads; ++o) {
+      if (b_lo == kBins) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) sum += weight(v[o].at(j), r.m);
+      } else {
+        bool want[kPer];
+        uint64_t word[kPer];
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          const float l = v[o].at(j);
+          const int bin = weight.bin(l);
+          if (bin < b_lo) sum += weight(l, r.m);
+          want[j] = bin >= b_lo && bin <= b_hi && weight.weighs(l);
+          word[j] = word_of(l, i0 + (o * kWave + lane) * kPer + j);
+        }
+        append(s.list, &s.n, want, word);
+      }
+    }
+    sum = wave_sum_u64(sum);
+    if (lane == 0) st64(&a.sums[b * kMaxSteps + i0 / kStep], sum);
   }
-  sum = wave_sum_u64(sum);
-  if (lane == 0) s.sums[wave] = sum;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int o = 1; o < kWaves; ++o) sum += s.sums[o];
-    st64(&a.sums[b * a.G + g], sum);
-    s.c = s.n ? __hip_atomic_fetch_add(&a.state[b].listed, s.n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
+  if (b_lo < kBins) {
+    __syncthreads();
+    if (threadIdx.x == 0)
+      s.base = s.n ? __hip_atomic_fetch_add(&a.state[b].listed, s.n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
+    __syncthreads();
+    const unsigned base = s.base;
+    for (unsigned i = threadIdx.x; i < min(s.n, (unsigned)kList) && base + i < kList; i += kRowThreads)
+      st64(&a.list[b * kList + base + i], s.list[i]);
   }
-  __syncthreads();
-  const uint32_t base = s.c;
-  for (uint32_t i = threadIdx.x; i < s.n; i += kThreads) st64(&a.list[b * kList + base + i], s.list[i]);
-  if (!last_to_arrive(&a.state[b].draw_arrived, a.G)) return;
+  if (!last_to_arrive(&a.state[b].row_arrived, a.G)) return;
 
-  RowRule rule = r;
-  if (b_lo == kBins && r.kind == kBand) rule.k = 0;  // fewer tokens have a weight than top-k keeps
-  if (over) {
-    if (rule.k && (uint64_t)rule.k > st.c_base + (uint64_t)st.expected) rule.k = 0;
-    draw_alone<In>(s, a, b, rule, top, st.total);
-    return;
-  }
   uint64_t last = 0;
-  if (listed) {
-    const int n = (int)st.expected;
-    for (int i = threadIdx.x; i < n; i += kThreads) s.list[i] = ld64(&a.list[b * kList + i]);
-    if ((uint64_t)rule.k > st.c_base + (uint64_t)n) rule.k = 0;
-    __syncthreads();
-    last = last_kept(s, n, rule, top, Pair{st.c_base, st.w_base}, st.total);
-    // that word tells the list's tokens apart, the row's others need the last one's own
+  const unsigned n = b_lo < kBins ? __hip_atomic_load(&a.state[b].listed, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
+  if (n > kList) {
+    draw_alone<In>(s, a, b, r, st->k, weight, st->total);
+    return;
+  }
+  const int steps = (a.V + kStep - 1) / kStep;
+  for (int i = threadIdx.x; i < steps; i += kRowThreads) s.sums[i] = ld64(&a.sums[b * kMaxSteps + i]);
+  if (b_lo < kBins) {
+    for (unsigned i = threadIdx.x; i < n; i += kRowThreads) s.list[i] = ld64(&a.list[b * kList + i]);
     if (threadIdx.x == 0) s.word = ~0ull;
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kThreads)
-      if (s.list[i] >= last) atomicMin(reinterpret_cast<unsigned long long*>(&s.word), (unsigned long long)s.list[i]);
+    last = last_kept<kRowThreads>(s.levels, s.list, (int)n, st->k, r.p_on, r.p, weight, Pair{st->c_base, st->w_base}, st->total);
+    // that word tells the list's tokens apart, the row's others need the last one's own
+    for (unsigned i = threadIdx.x; i < n; i += kRowThreads) {
+      const uint64_t word = s.list[i];
+      if (word < last) continue;
+      atomicMin(reinterpret_cast<unsigned long long*>(&s.word), (unsigned long long)word);
+      if (const uint64_t w = weight(logit_of(word), r.m)) add64(&s.sums[index_of(word) / kStep], w);
+    }
     __syncthreads();
     last = s.word;
   }
-  for (int i = threadIdx.x; i < a.G; i += kThreads) s.sums[i] = ld64(&a.sums[b * a.G + i]);
   __syncthreads();
-  if (listed) {
-    const int n = (int)st.expected;
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-      const uint64_t word = s.list[i];
-      const uint64_t w = word >= last ? weight_of(logit_of(word), top, r.inv_t, r.m) : 0;
-      if (w) atomicAdd(reinterpret_cast<unsigned long long*>(&s.sums[index_of(word) / a.chunk]), (unsigned long long)w);
-    }
-    __syncthreads();
-  }
-  draw_from_row<In>(s, a, b, rule, top, last);
+  draw_from_steps<In>(s, a, b, r, weight, last);
 }
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
-// A row's chunks: about four workgroups a compute unit over all rows, none shorter than a
-// workgroup's reads of two vectors a thread.
+// A row's chunks: about four workgroups a compute unit over all rows.
 void split(int64_t B, int V, int* G, int* chunk) {
   const int64_t want = std::max<int64_t>(1, 4 * (int64_t)device_cu_count() / std::max<int64_t>(B, 1));
-  int64_t n = std::min<int64_t>({want, kMaxChunks, (V + 2047) / 2048});
-  n = std::max<int64_t>(n, 1);
-  int64_t c = (V + n - 1) / n;
-  c = (c + 2047) / 2048 * 2048;  // whole steps and parts of either type
-  *chunk = (int)std::min<int64_t>(c, 65536);
-  *G = (int)((V + *chunk - 1) / *chunk);
+  const int64_t n = std::max<int64_t>(1, std::min<int64_t>({want, kMaxChunks, (V + 2047) / 2048}));
+  *chunk = (int)(((V + n - 1) / n + 2047) / 2048 * 2048);  // whole steps, and a peak's reads of either type
+  *G = (V + *chunk - 1) / *chunk;
 }
 
 size_t carve(SampleArgs& a, char* base) {
   size_t off = 0;
   auto take = [&](size_t bytes) { char* r = base ? base + off : nullptr; off += align256(bytes); return r; };
   const size_t B = (size_t)a.B;
+  if (a.V <= kList) return 256;  // (not used)
   a.state = reinterpret_cast<RowState*>(take(B * sizeof(RowState)));
   a.peaks = reinterpret_cast<uint64_t*>(take(B * kMaxChunks * 8));
-  a.sums = reinterpret_cast<uint64_t*>(take(B * kMaxChunks * 8));
   a.parts = reinterpret_cast<float*>(take(B * a.M * 4));
-  if (a.V > kList) {
-    a.list = reinterpret_cast<uint64_t*>(take(B * kList * 8));
-    a.counts = reinterpret_cast<uint32_t*>(take(B * kBins * 4));
-    a.weights = reinterpret_cast<uint64_t*>(take(B * kBins * 8));
-  }
+  a.sums = reinterpret_cast<uint64_t*>(take(B * kMaxSteps * 8));
+  a.list = reinterpret_cast<uint64_t*>(take(B * kList * 8));
+  a.counts = reinterpret_cast<uint32_t*>(take(B * kBins * 4));
+  a.weights = reinterpret_cast<uint64_t*>(take(B * kBins * 8));
   return off;
 }
 
 template <typename In>
 hipError_t launch_sample(const SampleArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)(a.B * a.G)), threads(kThreads);
-  hipLaunchKernelGGL(peak_kernel<In>, grid, threads, 0, stream, a);
+  const unsigned rows = (unsigned)a.B, chunks = (unsigned)(a.B * a.G);
+  if (a.V <= kList) {
+    hipLaunchKernelGGL(front_kernel<In>, dim3(rows), dim3(kFrontThreads), 0, stream, a, rows);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(peak_kernel<In>, dim3(chunks), dim3(kPeakThreads), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (a.V > kList && (a.top_k || a.top_p)) {
-    hipLaunchKernelGGL(band_kernel<In>, grid, threads, 0, stream, a);
+  if (a.top_k || a.top_p) {
+    const unsigned picks = a.top_k ? rows : 0;  // a list decides a row only where there is a top-k
+    hipLaunchKernelGGL(front_kernel<In>, dim3(picks + chunks), dim3(kFrontThreads), 0, stream, a, picks);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(draw_kernel<In>, grid, threads, 0, stream, a);
+  hipLaunchKernelGGL(row_kernel<In>, dim3(chunks), dim3(kRowThreads), 0, stream, a);
   return hipGetLastError();
 }
 

@@ -259,7 +259,7 @@ def test_binding_refusals(B):
         with pytest.raises(ValueError):
             bad()
     with pytest.raises(B.Q4Error) as err:
-        B.sample_logits(x, u, ws=torch.empty(256, dtype=torch.uint8, device="cuda"))
+        B.sample_logits(torch.zeros(3, 5000, device="cuda"), u, ws=torch.empty(256, dtype=torch.uint8, device="cuda"))
     assert err.value.status == B.EWORKSPACE
     with pytest.raises(B.Q4Error) as err:
         B.sample_logits(x, u, probs=u)
