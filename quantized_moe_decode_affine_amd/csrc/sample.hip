@@ -42,6 +42,7 @@ constexpr int kDigits = 2048;     // of a selection's level
 constexpr int kWordBits = 50, kIndexBits = 18;
 constexpr uint64_t kIndexMask = (1ull << kIndexBits) - 1;
 constexpr int kOneBits = 45;      // the largest logit's weight is 2^45
+constexpr double kNone = kOneBits + 1;  // of 2^-46 of that and less nothing is left
 
 static_assert(kMaxSampleVocab == 1 << kIndexBits, "an index fits its bits");
 
@@ -77,7 +78,7 @@ enum Kind { kGreedy, kAll, kTop, kBand, kSum };
 
 struct RowRule {
   Kind kind;
-  double scale, p, m;           // scale: log2(e) / t; m: 0 without min-p
+  double scale, p, limit;       // scale: log2(e) / t; limit: weights of 2^-limit and less drop
   int k;                        // 0 without top-k
   bool p_on;
 };
@@ -91,7 +92,11 @@ __device__ __forceinline__ RowRule row_rule(const SampleArgs& a, int64_t b) {
   r.k = k > 0 && k < a.V ? k : 0;
   r.p_on = p < 1.0f;
   r.p = p > 0.0f ? (double)p : 0.0;
-  r.m = m > 0.0f ? fmin((double)m, 1.0) : 0.0;
+  r.limit = kNone;
+  if (m > 0.0f) {  // 2^-y >= m; the next number above, as what is kept lies below the limit
+    const double most = fmax(-log2((double)m), 0.0);
+    r.limit = fmin(kNone, __longlong_as_double(__double_as_longlong(most) + 1));
+  }
   r.kind = !(t > 0.0f)                            ? kGreedy
            : a.V <= kList                         ? kAll
            : r.k && r.k <= min(a.M / 2, kTopMost) ? kTop
@@ -104,9 +109,9 @@ __device__ __forceinline__ RowRule row_rule(const SampleArgs& a, int64_t b) {
 __device__ __forceinline__ float clean(float l) { return l == l ? l + 0.0f : -__builtin_inff(); }
 
 template <typename In>
-__device__ __forceinline__ float one_logit(const In* row, int i) {
-  if constexpr (sizeof(In) == 2) return clean(bf16_bits_to_f32(row[i]));
-  else return clean(row[i]);
+__device__ __forceinline__ float as_logit(In raw) {
+  if constexpr (sizeof(In) == 2) return clean(bf16_bits_to_f32(raw));
+  else return clean(raw);
 }
 
 // 16 bytes of consecutive logits from i on; closed from `end` on.
@@ -125,10 +130,7 @@ struct Logits {
       }
     }
   }
-  __device__ __forceinline__ float at(int j) const {
-    if constexpr (sizeof(In) == 2) return clean(bf16_bits_to_f32(raw[j]));
-    else return clean(raw[j]);
-  }
+  __device__ __forceinline__ float at(int j) const { return as_logit(raw[j]); }
 };
 
 // The place in the order: 50 bits, larger first.
@@ -154,30 +156,30 @@ struct Weights {
   __device__ __forceinline__ Weights(const Powers* powers, float top_, double scale_)
       : pow(powers), top((double)top_), scale(scale_), top_f(top_), scale_f((float)scale_) {}
 
-  // (max - l) / t in powers of two.
+  // (max - l) / t in powers of two; a NaN for closed logits under an infinite t or maximum.
   __device__ __forceinline__ double distance(float l) const { return l == top_f ? 0.0 : (top - (double)l) * scale; }
 
   // Closed logits and those beyond 2^-46 of the largest have no weight, and change no
   // filter's end.
-  __device__ __forceinline__ bool weighs(float l) const { return distance(l) < 46.0; }
+  __device__ __forceinline__ bool weighs(float l) const { return distance(l) < kNone; }
 
-  // 0 where min-p drops it, too.  2^-y for y = n / 64 + r: the table's value for n % 64 with n / 64
-  // off its exponent, times exp(-r ln 2) by its series to the fifth power (|r| <= 2^-7: 2^-52 of it is left out).
-  __device__ __forceinline__ uint64_t operator()(float l, double m) const {
+  // 0 from `limit` on.  2^-y for y = n / 64 + r: the table's value for n % 64 with n / 64 off its
+  // exponent, times exp(-r ln 2) by its series to the fifth power (|r| <= 2^-7: 2^-52 of it is left out).
+  // No branches, so that several run at once; what is computed beyond the limit is not used.
+  __device__ __forceinline__ uint64_t operator()(float l, double limit) const {
     const double y = distance(l);
-    if (!(y < 46.0)) return 0;
     constexpr double kMagic = 6755399441055744.0;  // 1.5 * 2^52: the sum's low bits hold the integer
     const double z = fma(y, 64.0, kMagic);
     const uint32_t n = (uint32_t)__double_as_longlong(z);
     const double r = fma(z - kMagic, -1.0 / 64.0, y);
     constexpr double k1 = -0.69314718055994530942, k2 = k1 * k1 / 2, k3 = k2 * k1 / 3, k4 = k3 * k1 / 4, k5 = k4 * k1 / 5;
     const double s = fma(fma(fma(fma(fma(k5, r, k4), r, k3), r, k2), r, k1), r, 1.0);
-    const uint64_t t = (uint64_t)__double_as_longlong(pow->of[n & 63]) - ((uint64_t)(n >> 6) << 52);
-    const double e = __longlong_as_double((long long)t) * s;
-    if (e < m) return 0;
+    const uint64_t t = (uint64_t)__double_as_longlong(pow->of[n & 63]);
+    const double e = __longlong_as_double((long long)pair64((uint32_t)t, (uint32_t)(t >> 32) - (n >> 6 << 20))) * s;
     // rounded to an integer by the addition: the low bits of 2^52 + v
     constexpr double kOne = (double)(1ull << kOneBits);
-    return (uint64_t)__double_as_longlong(fma(e, kOne, 4503599627370496.0)) & ((1ull << 52) - 1);
+    const uint64_t w = (uint64_t)__double_as_longlong(fma(e, kOne, 4503599627370496.0));
+    return y < limit ? pair64((uint32_t)w, (uint32_t)(w >> 32) & 0xFFFFFu) : 0;
   }
 
   // Bins of the distance, as fine as its exponent and 8 bits from 2^-10 to 2^6; they follow the
@@ -421,20 +423,73 @@ __device__ __forceinline__ uint64_t select_word(Levels& s, int bits, uint32_t ne
   }
 }
 
-// The last token that the filters keep, as its word among a list of n: all tokens
+template <int kThreads>
+__device__ __forceinline__ uint64_t block_min(uint64_t mine) {
+  __shared__ uint64_t s_w[kThreads / kWave];
+  mine = wave_max_u64(~mine);
+  __syncthreads();  // an earlier call's are read
+  if (lane_id() == 0) s_w[threadIdx.x / kWave] = mine;
+  __syncthreads();
+#pragma unroll
+  for (int o = 0; o < kThreads / kWave; ++o) mine = max(mine, s_w[o]);
+  return ~mine;
+}
+
+// What a list is decided with; the list has room for 8 words more than it holds.
+union Scratch {
+  Levels levels;
+  alignas(16) uint64_t w[512];
+};
+
+// The word of the last token that the filters keep, from a list of n words: all tokens
 // from the one after the first base.c of the order (their weight base.w) on, down to
 // the last that top-k may keep or, without top-k, to the end of the row (z = 0) or of the bin in
 // which top-p ends (z: the row's weight).
 template <int kThreads>
-__device__ __forceinline__ uint64_t last_kept(Levels& s, const uint64_t* list, int n, int k, bool p_on, double p,
+__device__ __forceinline__ uint64_t last_kept(Scratch& s, uint64_t* list, int n, int k, bool p_on, double p,
                                               const Weights& weight, Pair base, uint64_t z) {
+  if (n <= kThreads) {
+    // A token a thread: its place and the weight before it by comparison with all, eight at a time.
+    const int i = threadIdx.x, n8 = (n + 7) & ~7;
+    const uint64_t word = i < n ? list[i] : 0, w = i < n ? weight(logit_of(word), kNone) : 0;
+    __syncthreads();
+    s.w[i] = w;
+    if (i < n8 - n) list[n + i] = 0;
+    __syncthreads();
+    uint32_t place = base.c;
+    uint64_t heavier = base.w;
+    if (i - lane_id() < n) {
+      for (int j = 0; j < n8; j += 8) {
+        ulonglong2 q[4], v[4];
+#pragma unroll
+        for (int o = 0; o < 4; ++o) {
+          q[o] = *reinterpret_cast<const ulonglong2*>(&list[j + 2 * o]);
+          v[o] = *reinterpret_cast<const ulonglong2*>(&s.w[j + 2 * o]);
+        }
+#pragma unroll
+        for (int o = 0; o < 4; ++o) {
+          place += q[o].x > word;
+          place += q[o].y > word;
+          heavier += q[o].x > word ? v[o].x : 0;
+          heavier += q[o].y > word ? v[o].y : 0;
+        }
+      }
+    }
+    bool kept = i < n && (!k || place < (uint32_t)k);
+    if (p_on) {
+      if (k || z == 0) z = base.w + block_sum<kThreads>(kept ? w : 0);
+      kept = kept && heavier < share_of(p, z);
+    }
+    return block_min<kThreads>(kept ? word : ~0ull);
+  }
   auto each = [&](auto visit) {
-    for (int i = threadIdx.x; i < n; i += kThreads) visit(list[i], weight(logit_of(list[i]), 0.0));
+    for (int i = threadIdx.x; i < n; i += kThreads) visit(list[i], weight(logit_of(list[i]), kNone));
   };
   uint64_t word = 0;
   Pair with;
+  __syncthreads();
   if (k && (uint32_t)k < base.c + n) {
-    word = select_word<kThreads>(s, kWordBits, k - base.c, 0, each, &with);
+    word = select_word<kThreads>(s.levels, kWordBits, k - base.c, 0, each, &with);
     z = base.w + with.w;
   } else if (k || z == 0) {  // all of them
     uint64_t mine = 0;
@@ -443,9 +498,13 @@ __device__ __forceinline__ uint64_t last_kept(Levels& s, const uint64_t* list, i
   }
   if (p_on) {
     const uint64_t need = share_of(p, z);
-    word = max(word, select_word<kThreads>(s, kWordBits, 0, need > base.w ? need - base.w : 1, each, &with));
+    word = max(word, select_word<kThreads>(s.levels, kWordBits, 0, need > base.w ? need - base.w : 1, each, &with));
   }
-  return word;
+  // that word tells the list's tokens apart: the last one's own
+  uint64_t last = ~0ull;
+  for (int i = threadIdx.x; i < n; i += kThreads)
+    if (list[i] >= word) last = min(last, list[i]);
+  return block_min<kThreads>(last);
 }
 
 // ---- the second launch: rows that a list decides, and the bins of those that need them
@@ -461,13 +520,11 @@ struct BandShared {
 struct PickShared {
   alignas(16) uint64_t list[kList + 8];
   union {
-    Levels levels;
+    Scratch scratch;
     uint32_t bins[kBins];
     uint16_t parts[kBins];
-    alignas(16) uint64_t w[kFrontThreads + 8];
   };
   uint64_t word[kFrontWaves];
-  unsigned n, parts_n;
   int at;
 };
 
@@ -493,84 +550,30 @@ __device__ __forceinline__ void append(uint64_t* list, unsigned* n, const bool (
   }
 }
 
-// The draw from a list that holds every token kept.
+// The draw from a list that holds every token kept, in the vocabulary's order.
 __device__ __forceinline__ void draw_from_list(PickShared& s, int n, const SampleArgs& a, int64_t b, const RowRule& r,
                                                const Weights& weight) {
-  constexpr int kThreads = kFrontThreads;
-  if (n <= kThreads) {
-    // A token a thread: its place and the weight before it by comparison with all, eight at a time.
-    const int i = threadIdx.x, n8 = (n + 7) & ~7;
-    const bool here = i < n;
-    const uint64_t word = here ? s.list[i] : 0;
-    uint64_t w = here ? weight(logit_of(word), 0.0) : 0;
-    s.w[i] = w;
-    if (i < 8) s.w[kThreads + i] = 0;
-    if (i < n8 - n) s.list[n + i] = 0;
-    __syncthreads();
-    auto with_each = [&](auto visit) {
-      for (int j = 0; j < n8; j += 8) {
-        ulonglong2 q[4], v[4];
+  constexpr int kThreads = kFrontThreads, kOwn = kList / kThreads;
+  const uint64_t last =
+      r.k || r.p_on ? last_kept<kThreads>(s.scratch, s.list, n, r.k, r.p_on, r.p, weight, Pair{0, 0}, 0) : 0;
+  // the running sum, kOwn tokens a thread
+  uint64_t word[kOwn], w[kOwn];
+  Pair mine{0, 0}, total;
+  const int own = n <= kThreads ? 1 : kOwn;
 #pragma unroll
-        for (int o = 0; o < 4; ++o) {
-          q[o] = *reinterpret_cast<const ulonglong2*>(&s.list[j + 2 * o]);
-          v[o] = *reinterpret_cast<const ulonglong2*>(&s.w[j + 2 * o]);
-        }
+  for (int o = 0; o < kOwn; ++o) {
+    const int i = threadIdx.x * own + o;
+    word[o] = o < own && i < n ? s.list[i] : 0;
+    w[o] = o < own && i < n && word[o] >= last ? weight(logit_of(word[o]), r.limit) : 0;
+    mine.w += w[o];
+  }
+  uint64_t before = block_before<kThreads>(mine, &total).w;
+  const uint64_t t = mark_of(a, b, total.w);
 #pragma unroll
-        for (int o = 0; o < 4; ++o) {
-          visit(q[o].x, v[o].x);
-          visit(q[o].y, v[o].y);
-        }
-      }
-    };
-    bool kept = here;
-    uint64_t total;
-    if (r.k || r.p_on) {
-      uint32_t place = 0;
-      uint64_t heavier = 0;
-      with_each([&](uint64_t other, uint64_t v) {
-        const bool ahead = other > word;
-        place += ahead;
-        heavier += ahead ? v : 0;
-      });
-      if (r.k) kept = kept && place < (uint32_t)r.k;
-      if (r.p_on) {
-        total = block_sum<kThreads>(kept ? w : 0);
-        kept = kept && heavier < share_of(r.p, total);
-      }
-    }
-    if (r.m > 0.0 && kept) w = weight(logit_of(word), r.m);
-    if (!kept) w = 0;
-    total = block_sum<kThreads>(w);  // (its barriers are after the loop's reads)
-    s.w[i] = w;
-    __syncthreads();
-    const uint64_t t = mark_of(a, b, total), mine = word & kIndexMask;
-    uint64_t before = 0;
-    with_each([&](uint64_t other, uint64_t v) { before += (other & kIndexMask) > mine ? v : 0; });
-    if (here && before <= t && before + w > t) answer(a, b, index_of(word), (double)w / (double)total);
-    return;
+  for (int o = 0; o < kOwn; ++o) {
+    if (before <= t && before + w[o] > t) answer(a, b, index_of(word[o]), (double)w[o] / (double)total.w);
+    before += w[o];
   }
-  const uint64_t last = last_kept<kThreads>(s.levels, s.list, n, r.k, r.p_on, r.p, weight, Pair{0, 0}, 0);
-  auto kept = [&](uint64_t word) -> uint64_t { return word >= last ? weight(logit_of(word), r.m) : 0; };
-  uint64_t mine = 0;
-  for (int i = threadIdx.x; i < n; i += kThreads) mine += kept(s.list[i]);
-  const uint64_t total = block_sum<kThreads>(mine);
-  // in the vocabulary's order: the inverted index from the largest down
-  Pair with;
-  const uint64_t low = select_word<kThreads>(s.levels, kIndexBits, 0, mark_of(a, b, total) + 1, [&](auto visit) {
-    for (int i = threadIdx.x; i < n; i += kThreads)
-      if (const uint64_t w = kept(s.list[i])) visit(s.list[i], w);
-  }, &with);
-  // the chosen one is the kept token of the lowest inverted index from `low` on
-  if (threadIdx.x == 0) s.word[0] = kIndexMask;
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const uint64_t at = s.list[i] & kIndexMask;
-    if (at >= low && kept(s.list[i])) atomicMin(reinterpret_cast<unsigned long long*>(&s.word[0]), (unsigned long long)at);
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kThreads)
-    if ((s.list[i] & kIndexMask) == s.word[0] && kept(s.list[i]))
-      answer(a, b, index_of(s.list[i]), (double)kept(s.list[i]) / (double)total);
 }
 
 template <typename In>
@@ -580,30 +583,31 @@ __device__ __forceinline__ void pick(PickShared& s, Powers& powers, const Sample
   const In* row = static_cast<const In*>(a.logits) + b * a.V;
   const int wave = threadIdx.x / kWave, lane = lane_id();
   const bool small = a.V <= kList;
-  // what the row may need is on its way while its rule is read
+  // What the row may need is on its way while its rule is read: consecutive tokens or parts a thread.
+  // (Loads under a condition would wait for each other: indexes are kept inside instead.)
   float l[kOwnParts > kOwnAll ? kOwnParts : kOwnAll];
   if (small) {
+    In raw[kOwnAll];
 #pragma unroll
-    for (int o = 0; o < kOwnAll; ++o) {
-      const int i = o * kThreads + threadIdx.x;
-      l[o] = i < a.V ? one_logit(row, i) : -__builtin_inff();
-    }
+    for (int o = 0; o < kOwnAll; ++o) raw[o] = row[min((int)threadIdx.x * kOwnAll + o, a.V - 1)];
+#pragma unroll
+    for (int o = 0; o < kOwnAll; ++o)
+      l[o] = (int)threadIdx.x * kOwnAll + o < a.V ? as_logit(raw[o]) : -__builtin_inff();
   } else {
 #pragma unroll
-    for (int o = 0; o < kOwnParts; ++o) {
-      const int i = o * kThreads + threadIdx.x;
-      l[o] = i < a.M ? a.parts[b * a.M + i] : -__builtin_inff();
-    }
+    for (int o = 0; o < kOwnParts; ++o) l[o] = a.parts[b * a.M + min((int)threadIdx.x * kOwnParts + o, a.M - 1)];
+#pragma unroll
+    for (int o = 0; o < kOwnParts; ++o)
+      if ((int)threadIdx.x * kOwnParts + o >= a.M) l[o] = -__builtin_inff();
   }
   uint64_t peak = small ? 0 : row_peak(a, b);
   const RowRule r = row_rule(a, b);
   if (r.kind == kBand || r.kind == kSum) return;
   powers.fill();
-  if (threadIdx.x == 0) s.n = s.parts_n = 0;
   if (small) {
 #pragma unroll
     for (int o = 0; o < kOwnAll; ++o) {
-      const int i = o * kThreads + threadIdx.x;
+      const int i = threadIdx.x * kOwnAll + o;
       if (i < a.V) peak = max(peak, word_of(l[o], i));
     }
     peak = wave_max_u64(peak);
@@ -619,20 +623,17 @@ __device__ __forceinline__ void pick(PickShared& s, Powers& powers, const Sample
     return;
   }
   const Weights weight(&powers, top, r.scale);
+  Pair mine{0, 0}, total;
 
   if (r.kind == kAll) {
-    __syncthreads();
-    bool want[kOwnAll];
-    uint64_t word[kOwnAll];
 #pragma unroll
-    for (int o = 0; o < kOwnAll; ++o) {
-      const int i = o * kThreads + threadIdx.x;
-      want[o] = i < a.V && weight.weighs(l[o]);
-      word[o] = word_of(l[o], i);
-    }
-    append(s.list, &s.n, want, word);
+    for (int o = 0; o < kOwnAll; ++o) mine.c += weight.weighs(l[o]);
+    uint32_t at = block_before<kThreads>(mine, &total).c;
+#pragma unroll
+    for (int o = 0; o < kOwnAll; ++o)
+      if (weight.weighs(l[o])) s.list[at++] = word_of(l[o], threadIdx.x * kOwnAll + o);
     __syncthreads();
-    draw_from_list(s, (int)s.n, a, b, r, weight);
+    draw_from_list(s, (int)total.c, a, b, r, weight);
     return;
   }
 
@@ -649,7 +650,6 @@ __device__ __forceinline__ void pick(PickShared& s, Powers& powers, const Sample
   __syncthreads();
   constexpr int kOwn = kBins / kThreads;
   uint32_t in[kOwn];
-  Pair mine{0, 0}, total;
 #pragma unroll
   for (int i = 0; i < kOwn; ++i) mine.c += in[i] = s.bins[threadIdx.x * kOwn + i];
   uint32_t c = block_before<kThreads>(mine, &total).c;
@@ -660,32 +660,55 @@ __device__ __forceinline__ void pick(PickShared& s, Powers& powers, const Sample
   }
   __syncthreads();
   const int bound = s.at;
-  // the parts that reach it, then their tokens that do
+  // the parts that reach it, in order, then their tokens that do
+  mine.c = 0;
+#pragma unroll
+  for (int o = 0; o < kOwnParts; ++o) mine.c += bin[o] <= bound;
+  uint32_t at = block_before<kThreads>(mine, &total).c;
 #pragma unroll
   for (int o = 0; o < kOwnParts; ++o)
-    if (bin[o] <= bound) s.parts[atomicAdd(&s.parts_n, 1u)] = (uint16_t)(o * kThreads + threadIdx.x);
+    if (bin[o] <= bound) s.parts[at++] = (uint16_t)(threadIdx.x * kOwnParts + o);
   __syncthreads();
   constexpr int kUnroll = 8;
-  const int n = (int)s.parts_n;
-  for (int o = wave * kUnroll; o < n; o += kFrontWaves * kUnroll) {
+  const int parts = (int)total.c;
+  uint32_t n = 0;
+  for (int o0 = 0; o0 < parts; o0 += kFrontWaves * kUnroll) {
+    const int o = o0 + wave * kUnroll;
+    In raw[kUnroll];
     float v[kUnroll];
-    bool want[kUnroll];
-    uint64_t word[kUnroll];
     int i[kUnroll];
 #pragma unroll
+    for (int j = 0; j < kUnroll; ++j) i[j] = s.parts[min(o + j, parts - 1)] * kPart + lane;
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j) raw[j] = row[min(i[j], a.V - 1)];
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j) v[j] = o + j < parts && i[j] < a.V ? as_logit(raw[j]) : -__builtin_inff();
+    uint64_t ball[kUnroll];
+    uint32_t all = 0;
+#pragma unroll
     for (int j = 0; j < kUnroll; ++j) {
-      i[j] = o + j < n ? s.parts[o + j] * kPart + lane : a.V;
-      v[j] = i[j] < a.V ? one_logit(row, i[j]) : -__builtin_inff();
+      ball[j] = __ballot(weight.weighs(v[j]) && weight.bin(v[j]) <= bound);
+      all += __popcll(ball[j]);
+    }
+    if (o0 > 0) __syncthreads();  // the last turn's counts are read
+    if (lane == 0) s.word[wave] = all;
+    __syncthreads();
+    uint32_t to = n;
+#pragma unroll
+    for (int j = 0; j < kFrontWaves; ++j) {
+      if (j < wave) to += (uint32_t)s.word[j];
+      n += (uint32_t)s.word[j];
     }
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j) {
-      want[j] = weight.weighs(v[j]) && weight.bin(v[j]) <= bound;
-      word[j] = word_of(v[j], i[j]);
+      const uint32_t here = to + __popcll(ball[j] & ((1ull << lane) - 1ull));
+      if ((ball[j] >> lane & 1) && here < kList) s.list[here] = word_of(v[j], i[j]);
+      to += __popcll(ball[j]);
     }
-    append(s.list, &s.n, want, word);
+    if (n > kList) break;  // uniform
   }
   __syncthreads();
-  if (s.n <= kList) draw_from_list(s, (int)s.n, a, b, r, weight);
+  if (n <= kList) draw_from_list(s, (int)n, a, b, r, weight);
   else if (threadIdx.x == 0) a.state[b].over = 1;  // row_kernel's
 }
 
@@ -711,7 +734,7 @@ __device__ __forceinline__ void band(BandShared& s, Powers& powers, const Sample
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const float l = v.at(j);
-      const uint64_t w = weight(l, 0.0);
+      const uint64_t w = weight(l, kNone);
       if (w == 0) continue;
       const int bin = weight.bin(l);
       add64(&s.w[bin], w);
@@ -788,7 +811,7 @@ __device__ __forceinline__ void band(BandShared& s, Powers& powers, const Sample
 
 // Workgroups 0 .. rows - 1: a row each; the others: a chunk's bins.
 template <typename In>
-__global__ __launch_bounds__(kFrontThreads, 2) void front_kernel(SampleArgs a, unsigned rows) {
+__global__ __launch_bounds__(kFrontThreads, 6) void front_kernel(SampleArgs a, unsigned rows) {
   __shared__ union Shared {
     BandShared band;
     PickShared pick;
@@ -800,14 +823,14 @@ __global__ __launch_bounds__(kFrontThreads, 2) void front_kernel(SampleArgs a, u
 }
 
 // ---- the third launch: rows by the sums of their steps
-constexpr int kRowThreads = 256, kRowWaves = kRowThreads / kWave;
+constexpr int kRowThreads = 512, kRowWaves = kRowThreads / kWave;
 static_assert(kMaxSteps <= kRowThreads, "a thread for each step's sum");
 
 struct RowShared {
-  uint64_t list[kList];
-  Levels levels;
+  alignas(16) uint64_t list[kList + 8];
+  Scratch scratch;
   uint64_t sums[kMaxSteps];
-  uint64_t word, found_w;
+  uint64_t found_w;
   unsigned n, base;
   int at;
 };
@@ -841,7 +864,7 @@ __device__ __forceinline__ void draw_from_steps(RowShared& s, const SampleArgs& 
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const float l = v[o].at(j);
-      sum += w[j] = word_of(l, i + j) >= last ? weight(l, r.m) : 0;
+      sum += w[j] = word_of(l, i + j) >= last ? weight(l, r.limit) : 0;
     }
     uint64_t up = wave_prefix(sum), before = up - sum;
 #pragma unroll
@@ -858,27 +881,27 @@ __device__ __forceinline__ void draw_from_steps(RowShared& s, const SampleArgs& 
 // The draw by this workgroup alone: the last token kept by digits of the row's words, then the steps' sums.
 // z: the row's weight, for a top-p without top-k.
 template <typename In>
-__device__ __noinline__ void draw_alone(RowShared& s, const SampleArgs& a, int64_t b, const RowRule& r, int k,
+__device__ __forceinline__ void draw_alone(RowShared& s, const SampleArgs& a, int64_t b, const RowRule& r, int k,
                                         const Weights& weight, uint64_t z) {
   const In* row = static_cast<const In*>(a.logits) + b * a.V;
   auto each = [&](auto visit) {
     for (int i = threadIdx.x; i < a.V; i += kRowThreads) {
-      const float l = one_logit(row, i);
-      if (const uint64_t w = weight(l, 0.0)) visit(word_of(l, i), w);
+      const float l = as_logit(row[i]);
+      if (const uint64_t w = weight(l, kNone)) visit(word_of(l, i), w);
     }
   };
   uint64_t last = 0;
   Pair with;
   if (k) {
-    last = select_word<kRowThreads>(s.levels, kWordBits, k, 0, each, &with);
+    last = select_word<kRowThreads>(s.scratch.levels, kWordBits, k, 0, each, &with);
     z = with.w;
   }
-  if (r.p_on) last = max(last, select_word<kRowThreads>(s.levels, kWordBits, 0, share_of(r.p, z), each, &with));
+  if (r.p_on) last = max(last, select_word<kRowThreads>(s.scratch.levels, kWordBits, 0, share_of(r.p, z), each, &with));
   for (int i = threadIdx.x; i < kMaxSteps; i += kRowThreads) s.sums[i] = 0;
   __syncthreads();
   each([&](uint64_t word, uint64_t w) {
     if (word < last) return;
-    if (r.m > 0.0) w = weight(logit_of(word), r.m);
+    if (r.limit < kNone) w = weight(logit_of(word), r.limit);
     add64(&s.sums[index_of(word) / kStep], w);
   });
   __syncthreads();
@@ -886,7 +909,7 @@ __device__ __noinline__ void draw_alone(RowShared& s, const SampleArgs& a, int64
 }
 
 template <typename In>
-__global__ __launch_bounds__(kRowThreads, 3) void row_kernel(SampleArgs a) {
+__global__ __launch_bounds__(kRowThreads, 6) void row_kernel(SampleArgs a) {
   __shared__ RowShared s;
   __shared__ Powers powers;
   constexpr int kPer = Logits<In>::kPer, kLoads = kStep / kWave / kPer, kParts = kStep / kPart;
@@ -919,7 +942,7 @@ __global__ __launch_bounds__(kRowThreads, 3) void row_kernel(SampleArgs a) {
   const int wave = threadIdx.x / kWave, lane = lane_id();
   const int end = min((g + 1) * a.chunk, a.V);
   for (int i0 = g * a.chunk + wave * kStep; i0 < end; i0 += kRowWaves * kStep) {
-    if (banded || r.m > 0.0) {  // what the step's largest logit does not reach none does
+    if (banded || r.limit < kNone) {  // what the step's largest logit does not reach none does
       const int i = i0 / kPart + lane;
       float most = lane < kParts && i < a.M ? a.parts[b * a.M + i] : -__builtin_inff();
       most = fmaxf(most, dpp_f32<kDppQuadXor1>(most));
@@ -928,7 +951,7 @@ __global__ __launch_bounds__(kRowThreads, 3) void row_kernel(SampleArgs a) {
       most = fmaxf(most, dpp_f32<kDppRowMirror>(most));
       most = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(most)));
       // (the list holds what min-p drops, too: the other filters count it)
-      if (b_lo < kBins ? !weight.weighs(most) || weight.bin(most) > b_hi : !weight(most, r.m)) {
+      if (b_lo < kBins ? !weight.weighs(most) || weight.bin(most) > b_hi : !weight(most, r.limit)) {
         if (lane == 0) st64(&a.sums[b * kMaxSteps + i0 / kStep], 0);
         continue;
       }
@@ -941,17 +964,24 @@ __global__ __launch_bounds__(kRowThreads, 3) void row_kernel(SampleArgs a) {
     for (int o = 0; o < kLoads; ++o) {
       if (b_lo == kBins) {
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) sum += weight(v[o].at(j), r.m);
+        for (int j = 0; j < kPer; ++j) sum += weight(v[o].at(j), r.limit);
       } else {
-        bool want[kPer];
+        bool want[kPer], above[kPer], any = false;
         uint64_t word[kPer];
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
           const float l = v[o].at(j);
           const int bin = weight.bin(l);
-          if (bin < b_lo) sum += weight(l, r.m);
+          any |= above[j] = bin < b_lo;
           want[j] = bin >= b_lo && bin <= b_hi && weight.weighs(l);
           word[j] = word_of(l, i0 + (o * kWave + lane) * kPer + j);
+        }
+        if (__any(any)) {
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) {
+            const uint64_t w = weight(v[o].at(j), r.limit);
+            sum += above[j] ? w : 0;
+          }
         }
         append(s.list, &s.n, want, word);
       }
@@ -980,18 +1010,12 @@ __global__ __launch_bounds__(kRowThreads, 3) void row_kernel(SampleArgs a) {
   for (int i = threadIdx.x; i < steps; i += kRowThreads) s.sums[i] = ld64(&a.sums[b * kMaxSteps + i]);
   if (b_lo < kBins) {
     for (unsigned i = threadIdx.x; i < n; i += kRowThreads) s.list[i] = ld64(&a.list[b * kList + i]);
-    if (threadIdx.x == 0) s.word = ~0ull;
     __syncthreads();
-    last = last_kept<kRowThreads>(s.levels, s.list, (int)n, st->k, r.p_on, r.p, weight, Pair{st->c_base, st->w_base}, st->total);
-    // that word tells the list's tokens apart, the row's others need the last one's own
+    last = last_kept<kRowThreads>(s.scratch, s.list, (int)n, st->k, r.p_on, r.p, weight, Pair{st->c_base, st->w_base}, st->total);
     for (unsigned i = threadIdx.x; i < n; i += kRowThreads) {
-      const uint64_t word = s.list[i];
-      if (word < last) continue;
-      atomicMin(reinterpret_cast<unsigned long long*>(&s.word), (unsigned long long)word);
-      if (const uint64_t w = weight(logit_of(word), r.m)) add64(&s.sums[index_of(word) / kStep], w);
+      const uint64_t word = s.list[i], w = word >= last ? weight(logit_of(word), r.limit) : 0;
+      if (w) add64(&s.sums[index_of(word) / kStep], w);
     }
-    __syncthreads();
-    last = s.word;
   }
   __syncthreads();
   draw_from_steps<In>(s, a, b, r, weight, last);

@@ -37,14 +37,26 @@ __device__ __forceinline__ uint64_t wave_sum_u64(uint64_t v) {
   return wave_reduce_u64(v, [](uint64_t a, uint64_t b) { return a + b; });
 }
 
-// The sum of the lanes up to and with this one.
+// The sum of the lanes up to and with this one: shifts inside the 16-lane rows, then the rows'
+// last lanes to the rows after them.
+constexpr int kDppRowShr = 0x110, kDppRowBcast15 = 0x142, kDppRowBcast31 = 0x143;
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_or_zero(uint32_t v) {  // 0 where the step brings nothing
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint64_t dpp_or_zero(uint64_t v) {
+  return pair64(dpp_or_zero<CTRL, ROWS>((uint32_t)v), dpp_or_zero<CTRL, ROWS>((uint32_t)(v >> 32)));
+}
 template <typename T>
 __device__ __forceinline__ T wave_prefix(T v) {
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) {
-    const T o = __shfl_up(v, d, kWave);
-    if (lane_id() >= d) v += o;
-  }
+  v += dpp_or_zero<kDppRowShr + 1, 0xF>(v);
+  v += dpp_or_zero<kDppRowShr + 2, 0xF>(v);
+  v += dpp_or_zero<kDppRowShr + 4, 0xF>(v);
+  v += dpp_or_zero<kDppRowShr + 8, 0xF>(v);
+  v += dpp_or_zero<kDppRowBcast15, 0xA>(v);
+  v += dpp_or_zero<kDppRowBcast31, 0xC>(v);
   return v;
 }
 
