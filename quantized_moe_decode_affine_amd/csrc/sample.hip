@@ -79,6 +79,7 @@ enum Kind { kGreedy, kAll, kTop, kBand, kSum };
 struct RowRule {
   Kind kind;
   double scale, p, limit;       // scale: log2(e) / t; limit: weights of 2^-limit and less drop
+  double u;                     // the draw's number, in [0, 1]
   int k;                        // 0 without top-k
   bool p_on;
 };
@@ -88,6 +89,8 @@ __device__ __forceinline__ RowRule row_rule(const SampleArgs& a, int64_t b) {
   const float t = a.temperature ? a.temperature[b] : 1.0f;
   const int k = a.top_k ? a.top_k[b] : 0;
   const float p = a.top_p ? a.top_p[b] : 1.0f, m = a.min_p ? a.min_p[b] : 0.0f;
+  const float u = a.u[b];
+  r.u = u > 0.0f ? fmin((double)u, 1.0) : 0.0;
   r.scale = 1.4426950408889634 / (double)t;
   r.k = k > 0 && k < a.V ? k : 0;
   r.p_on = p < 1.0f;
@@ -254,7 +257,7 @@ __global__ __launch_bounds__(kPeakThreads) void peak_kernel(SampleArgs a) {
   }
   uint64_t w = wave_max_u64(word_of(best, at));
   if (lane_id() == 0) s_best[threadIdx.x / kWave] = w;
-  __syncthreads();
+  lds_sync();
   if (threadIdx.x == 0) {
 #pragma unroll
     for (int o = 1; o < kThreads / kWave; ++o) w = max(w, s_best[o]);
@@ -293,12 +296,12 @@ __device__ __forceinline__ Pair block_before(Pair mine, Pair* total) {
   __shared__ uint64_t s_w[kWaves];
   const int wave = threadIdx.x / kWave;
   const Pair in{wave_prefix(mine.c), wave_prefix(mine.w)};
-  __syncthreads();  // an earlier call's totals are read
+  lds_sync();  // an earlier call's totals are read
   if (lane_id() == kWave - 1) {
     s_c[wave] = in.c;
     s_w[wave] = in.w;
   }
-  __syncthreads();
+  lds_sync();
   Pair before{in.c - mine.c, in.w - mine.w}, all{0, 0};
 #pragma unroll
   for (int o = 0; o < kWaves; ++o) {
@@ -316,9 +319,9 @@ template <int kThreads>
 __device__ __forceinline__ uint64_t block_sum(uint64_t mine) {
   __shared__ uint64_t s_w[kThreads / kWave];
   mine = wave_sum_u64(mine);
-  __syncthreads();  // an earlier call's are read
+  lds_sync();  // an earlier call's are read
   if (lane_id() == 0) s_w[threadIdx.x / kWave] = mine;
-  __syncthreads();
+  lds_sync();
   uint64_t all = 0;
 #pragma unroll
   for (int o = 0; o < kThreads / kWave; ++o) all += s_w[o];
@@ -333,10 +336,8 @@ __device__ __forceinline__ uint64_t share_of(double p, uint64_t z) {
 }
 
 // The draw's place among `total` of weight: the chosen token's running sum is the first beyond it.
-__device__ __forceinline__ uint64_t mark_of(const SampleArgs& a, int64_t b, uint64_t total) {
-  const float u = a.u[b];
-  const double x = u > 0.0f ? fmin((double)u, 1.0) : 0.0;
-  return min((uint64_t)(x * (double)total), total - 1);
+__device__ __forceinline__ uint64_t mark_of(const RowRule& r, uint64_t total) {
+  return min((uint64_t)(r.u * (double)total), total - 1);
 }
 
 __device__ __forceinline__ void answer(const SampleArgs& a, int64_t b, int id, double prob) {
@@ -373,7 +374,7 @@ __device__ __forceinline__ uint64_t select_word(Levels& s, int bits, uint32_t ne
       s.c[i] = 0;
     }
     if (threadIdx.x == 0) s.at = -1;
-    __syncthreads();
+    lds_sync();
     each([&](uint64_t word, uint64_t w) {
       word &= mask;
       if (word >> left != prefix) return;
@@ -381,7 +382,7 @@ __device__ __forceinline__ uint64_t select_word(Levels& s, int bits, uint32_t ne
       add64(&s.w[d], w);
       atomicAdd(&s.c[d], 1u);
     });
-    __syncthreads();
+    lds_sync();
     // digits from the largest down
     constexpr int kOwn = kDigits / kThreads;
     const int own = kDigits - 1 - (int)threadIdx.x * kOwn;
@@ -406,11 +407,11 @@ __device__ __forceinline__ uint64_t select_word(Levels& s, int bits, uint32_t ne
       }
       at = up;
     }
-    __syncthreads();
+    lds_sync();
     const int d = s.at;
     if (d < 0) {  // no word at all
       *with = above;
-      __syncthreads();
+      lds_sync();
       return 0;
     }
     above = Pair{s.found_c, s.found_w};
@@ -418,7 +419,7 @@ __device__ __forceinline__ uint64_t select_word(Levels& s, int bits, uint32_t ne
     *with = Pair{above.c + in.c, above.w + in.w};
     prefix = prefix << take | (uint64_t)d;
     left = rest;
-    __syncthreads();
+    lds_sync();
     if (left == 0 || in.c == 1 || (need_c && with->c == need_c)) return prefix << left;
   }
 }
@@ -427,9 +428,9 @@ template <int kThreads>
 __device__ __forceinline__ uint64_t block_min(uint64_t mine) {
   __shared__ uint64_t s_w[kThreads / kWave];
   mine = wave_max_u64(~mine);
-  __syncthreads();  // an earlier call's are read
+  lds_sync();  // an earlier call's are read
   if (lane_id() == 0) s_w[threadIdx.x / kWave] = mine;
-  __syncthreads();
+  lds_sync();
 #pragma unroll
   for (int o = 0; o < kThreads / kWave; ++o) mine = max(mine, s_w[o]);
   return ~mine;
@@ -438,7 +439,11 @@ __device__ __forceinline__ uint64_t block_min(uint64_t mine) {
 // What a list is decided with; the list has room for 8 words more than it holds.
 union Scratch {
   Levels levels;
-  alignas(16) uint64_t w[512];
+  struct {
+    alignas(16) uint64_t w[512 + 8];
+    uint64_t heavier[512];
+    uint32_t place[512];
+  } rank;
 };
 
 // The word of the last token that the filters keep, from a list of n words: all tokens
@@ -449,22 +454,33 @@ template <int kThreads>
 __device__ __forceinline__ uint64_t last_kept(Scratch& s, uint64_t* list, int n, int k, bool p_on, double p,
                                               const Weights& weight, Pair base, uint64_t z) {
   if (n <= kThreads) {
-    // A token a thread: its place and the weight before it by comparison with all, eight at a time.
-    const int i = threadIdx.x, n8 = (n + 7) & ~7;
+    // A token's place and the weight before it by comparison with all others: a token a thread, or
+    // as many threads to a token as there are, each with a slice of the others, eight at a time.
+    int across = kWave;
+    while (across < n) across *= 2;
+    const int slices = kThreads / across, slice = threadIdx.x / across, i = threadIdx.x % across;
+    const int len = ((n + slices - 1) / slices + 7) & ~7, from = slice * len, to = min(from + len, n);
     const uint64_t word = i < n ? list[i] : 0, w = i < n ? weight(logit_of(word), kNone) : 0;
-    __syncthreads();
-    s.w[i] = w;
-    if (i < n8 - n) list[n + i] = 0;
-    __syncthreads();
-    uint32_t place = base.c;
-    uint64_t heavier = base.w;
-    if (i - lane_id() < n) {
-      for (int j = 0; j < n8; j += 8) {
+    lds_sync();
+    if (slice == 0) {
+      s.rank.w[i] = w;
+      s.rank.place[i] = base.c;
+      s.rank.heavier[i] = base.w;
+    }
+    if (threadIdx.x < 8) {  // behind the last of the eights
+      list[n + threadIdx.x] = 0;
+      if (across + (int)threadIdx.x < kThreads + 8) s.rank.w[across + threadIdx.x] = 0;
+    }
+    lds_sync();
+    if (i - lane_id() < n && from < to) {
+      uint32_t place = 0;
+      uint64_t heavier = 0;
+      for (int j = from; j < to; j += 8) {
         ulonglong2 q[4], v[4];
 #pragma unroll
         for (int o = 0; o < 4; ++o) {
           q[o] = *reinterpret_cast<const ulonglong2*>(&list[j + 2 * o]);
-          v[o] = *reinterpret_cast<const ulonglong2*>(&s.w[j + 2 * o]);
+          v[o] = *reinterpret_cast<const ulonglong2*>(&s.rank.w[j + 2 * o]);
         }
 #pragma unroll
         for (int o = 0; o < 4; ++o) {
@@ -474,8 +490,15 @@ __device__ __forceinline__ uint64_t last_kept(Scratch& s, uint64_t* list, int n,
           heavier += q[o].y > word ? v[o].y : 0;
         }
       }
+      if (i < n) {
+        atomicAdd(&s.rank.place[i], place);
+        add64(&s.rank.heavier[i], heavier);
+      }
     }
-    bool kept = i < n && (!k || place < (uint32_t)k);
+    lds_sync();
+    const uint32_t place = s.rank.place[i];
+    const uint64_t heavier = s.rank.heavier[i];
+    bool kept = i < n && slice == 0 && (!k || place < (uint32_t)k);
     if (p_on) {
       if (k || z == 0) z = base.w + block_sum<kThreads>(kept ? w : 0);
       kept = kept && heavier < share_of(p, z);
@@ -487,7 +510,7 @@ __device__ __forceinline__ uint64_t last_kept(Scratch& s, uint64_t* list, int n,
   };
   uint64_t word = 0;
   Pair with;
-  __syncthreads();
+  lds_sync();
   if (k && (uint32_t)k < base.c + n) {
     word = select_word<kThreads>(s.levels, kWordBits, k - base.c, 0, each, &with);
     z = base.w + with.w;
@@ -525,8 +548,10 @@ struct PickShared {
     uint16_t parts[kBins];
   };
   uint64_t word[kFrontWaves];
+  alignas(16) uint32_t found[kFrontWaves];
   int at;
 };
+static_assert(kFrontWaves == 8, "found is read by fours");
 
 // Appends a wave's words to the list; what is beyond its end is counted only.
 template <int kN>
@@ -568,7 +593,7 @@ __device__ __forceinline__ void draw_from_list(PickShared& s, int n, const Sampl
     mine.w += w[o];
   }
   uint64_t before = block_before<kThreads>(mine, &total).w;
-  const uint64_t t = mark_of(a, b, total.w);
+  const uint64_t t = mark_of(r, total.w);
 #pragma unroll
   for (int o = 0; o < kOwn; ++o) {
     if (before <= t && before + w[o] > t) answer(a, b, index_of(word[o]), (double)w[o] / (double)total.w);
@@ -612,7 +637,7 @@ __device__ __forceinline__ void pick(PickShared& s, Powers& powers, const Sample
     }
     peak = wave_max_u64(peak);
     if (lane == 0) s.word[wave] = peak;
-    __syncthreads();
+    lds_sync();
 #pragma unroll
     for (int o = 0; o < kFrontWaves; ++o) peak = max(peak, s.word[o]);
   }
@@ -632,7 +657,7 @@ __device__ __forceinline__ void pick(PickShared& s, Powers& powers, const Sample
 #pragma unroll
     for (int o = 0; o < kOwnAll; ++o)
       if (weight.weighs(l[o])) s.list[at++] = word_of(l[o], threadIdx.x * kOwnAll + o);
-    __syncthreads();
+    lds_sync();
     draw_from_list(s, (int)total.c, a, b, r, weight);
     return;
   }
@@ -643,11 +668,11 @@ __device__ __forceinline__ void pick(PickShared& s, Powers& powers, const Sample
   for (int o = 0; o < kOwnParts; ++o) bin[o] = weight.weighs(l[o]) ? weight.bin(l[o]) : kBins;
   for (int i = threadIdx.x; i < kBins; i += kThreads) s.bins[i] = 0;
   if (threadIdx.x == 0) s.at = kBins - 1;  // fewer parts than k hold a token of any weight
-  __syncthreads();
+  lds_sync();
 #pragma unroll
   for (int o = 0; o < kOwnParts; ++o)
     if (bin[o] < kBins) atomicAdd(&s.bins[bin[o]], 1u);
-  __syncthreads();
+  lds_sync();
   constexpr int kOwn = kBins / kThreads;
   uint32_t in[kOwn];
 #pragma unroll
@@ -658,56 +683,89 @@ __device__ __forceinline__ void pick(PickShared& s, Powers& powers, const Sample
     if (c < (uint32_t)r.k && c + in[i] >= (uint32_t)r.k) s.at = threadIdx.x * kOwn + i;
     c += in[i];
   }
-  __syncthreads();
+  lds_sync();
   const int bound = s.at;
-  // the parts that reach it, in order, then their tokens that do
+  // The parts that reach it, in order, and the least of their maxima: at least k tokens reach that.
+  // With fewer parts than k, every token of any weight (and some of none, which do not matter).
   mine.c = 0;
+  uint32_t least = ~0u;
 #pragma unroll
-  for (int o = 0; o < kOwnParts; ++o) mine.c += bin[o] <= bound;
+  for (int o = 0; o < kOwnParts; ++o) {
+    mine.c += bin[o] <= bound;
+    if (bin[o] <= bound) least = min(least, float_key(l[o]));
+  }
   uint32_t at = block_before<kThreads>(mine, &total).c;
 #pragma unroll
   for (int o = 0; o < kOwnParts; ++o)
     if (bin[o] <= bound) s.parts[at++] = (uint16_t)(threadIdx.x * kOwnParts + o);
-  __syncthreads();
-  constexpr int kUnroll = 8;
+  least = (uint32_t)block_min<kThreads>(least);  // (its barriers are behind the parts' writes)
   const int parts = (int)total.c;
+  const float reach = fmaxf(parts < r.k ? top - (float)(kNone / r.scale) * 1.0001f : key_float(least), -3.402823466e38f);
+  // Their tokens that do, in order: 16 bytes a lane, so a load covers kPer parts, kLoads of them
+  // at a time and the next ones on their way (the barriers wait for LDS alone).
+  constexpr int kPer = Logits<In>::kPer, kLanes = kPart / kPer, kLoads = 4, kTurn = kFrontWaves * kLoads * kPer;
   uint32_t n = 0;
-  for (int o0 = 0; o0 < parts; o0 += kFrontWaves * kUnroll) {
-    const int o = o0 + wave * kUnroll;
-    In raw[kUnroll];
-    float v[kUnroll];
-    int i[kUnroll];
+  Logits<In> next[kLoads];
+  // A lane's first token, moved back where its 16 bytes would pass the row's end; tokens before `from` are
+  // another lane's.
+  auto tokens = [&](int o, int u, int* from) {
+    *from = s.parts[min(o + u * kPer + lane / kLanes, parts - 1)] * kPart + lane % kLanes * kPer;
+    return min(*from, a.V - kPer);
+  };
+  auto fetch = [&](int o) {
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j) i[j] = s.parts[min(o + j, parts - 1)] * kPart + lane;
-#pragma unroll
-    for (int j = 0; j < kUnroll; ++j) raw[j] = row[min(i[j], a.V - 1)];
-#pragma unroll
-    for (int j = 0; j < kUnroll; ++j) v[j] = o + j < parts && i[j] < a.V ? as_logit(raw[j]) : -__builtin_inff();
-    uint64_t ball[kUnroll];
-    uint32_t all = 0;
-#pragma unroll
-    for (int j = 0; j < kUnroll; ++j) {
-      ball[j] = __ballot(weight.weighs(v[j]) && weight.bin(v[j]) <= bound);
-      all += __popcll(ball[j]);
+    for (int u = 0; u < kLoads; ++u) {
+      int from;
+      __builtin_memcpy(next[u].raw, row + tokens(o, u, &from), 16);
     }
-    if (o0 > 0) __syncthreads();  // the last turn's counts are read
-    if (lane == 0) s.word[wave] = all;
-    __syncthreads();
-    uint32_t to = n;
+  };
+  fetch(wave * kLoads * kPer);
+  for (int o0 = 0; o0 < parts; o0 += kTurn) {
+    const int o = o0 + wave * kLoads * kPer;
+    Logits<In> v[kLoads];
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) v[u] = next[u];
+    if (o0 + kTurn < parts) fetch(o + kTurn);
+    uint32_t want[kLoads], before[kLoads], all = 0;
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      int from;
+      const int i = tokens(o, u, &from);
+      want[u] = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) want[u] |= (uint32_t)(v[u].at(j) >= reach && i + j >= from) << j;
+      if (o + u * kPer + lane / kLanes >= parts) want[u] = 0;
+      const uint32_t here = __popc(want[u]), upto = wave_prefix(here);
+      before[u] = all + upto - here;
+      all += __builtin_amdgcn_readlane(upto, kWave - 1);
+    }
+    if (o0 > 0) lds_sync();  // the last turn's counts are read
+    if (lane == 0) s.found[wave] = all;
+    lds_sync();
+    uint32_t to = n, found[kFrontWaves];
+    *reinterpret_cast<uint4*>(found) = *reinterpret_cast<const uint4*>(s.found);
+    *reinterpret_cast<uint4*>(found + 4) = *reinterpret_cast<const uint4*>(s.found + 4);
 #pragma unroll
     for (int j = 0; j < kFrontWaves; ++j) {
-      if (j < wave) to += (uint32_t)s.word[j];
-      n += (uint32_t)s.word[j];
+      to += j < wave ? found[j] : 0;
+      n += found[j];
     }
+    n = __builtin_amdgcn_readfirstlane(n);
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j) {
-      const uint32_t here = to + __popcll(ball[j] & ((1ull << lane) - 1ull));
-      if ((ball[j] >> lane & 1) && here < kList) s.list[here] = word_of(v[j], i[j]);
-      to += __popcll(ball[j]);
+    for (int u = 0; u < kLoads; ++u) {
+      int from;
+      const int i = tokens(o, u, &from);
+      uint32_t at = to + before[u];
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (want[u] >> j & 1) {
+          if (at < kList) s.list[at] = word_of(v[u].at(j), i + j);
+          ++at;
+        }
     }
-    if (n > kList) break;  // uniform
+    if (n > kList) break;
   }
-  __syncthreads();
+  lds_sync();
   if (n <= kList) draw_from_list(s, (int)n, a, b, r, weight);
   else if (threadIdx.x == 0) a.state[b].over = 1;  // row_kernel's
 }
@@ -724,7 +782,7 @@ __device__ __forceinline__ void band(BandShared& s, Powers& powers, const Sample
     s.w[i] = 0;
     s.c[i] = 0;
   }
-  __syncthreads();
+  lds_sync();
   const Weights weight(&powers, top, r.scale);
   const In* row = static_cast<const In*>(a.logits) + b * a.V;
   const int end = min((g + 1) * a.chunk, a.V);
@@ -741,7 +799,7 @@ __device__ __forceinline__ void band(BandShared& s, Powers& powers, const Sample
       if (r.k) atomicAdd(&s.c[bin], 1u);
     }
   }
-  __syncthreads();
+  lds_sync();
   uint32_t* counts = a.counts + b * kBins;
   uint64_t* weights = a.weights + b * kBins;
   for (int i = threadIdx.x; i < kBins; i += kThreads) {
@@ -756,7 +814,7 @@ __device__ __forceinline__ void band(BandShared& s, Powers& powers, const Sample
     s.w[i] = ld64(&weights[i]);
     s.c[i] = r.k ? __hip_atomic_load(&counts[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
   }
-  __syncthreads();
+  lds_sync();
   constexpr int kOwn = kBins / kThreads;
   const int own = threadIdx.x * kOwn;
   Pair mine{0, 0}, total;
@@ -777,10 +835,10 @@ __device__ __forceinline__ void band(BandShared& s, Powers& powers, const Sample
       }
       at = with;
     }
-    __syncthreads();
+    lds_sync();
     const int bin = s.bin;
     *base = s.before;
-    __syncthreads();
+    lds_sync();
     return bin;
   };
   const int k = r.k && (uint32_t)r.k <= total.c ? r.k : 0;
@@ -845,12 +903,12 @@ __device__ __forceinline__ void draw_from_steps(RowShared& s, const SampleArgs& 
   const Pair mine{0, (int)threadIdx.x < steps ? s.sums[threadIdx.x] : 0};
   Pair total;
   const Pair at = block_before<kRowThreads>(mine, &total);
-  uint64_t t = mark_of(a, b, total.w);
+  uint64_t t = mark_of(r, total.w);
   if (at.w <= t && at.w + mine.w > t) {
     s.at = threadIdx.x;
     s.found_w = at.w;
   }
-  __syncthreads();
+  lds_sync();
   if (threadIdx.x >= kWave) return;
   t -= s.found_w;
   const In* row = static_cast<const In*>(a.logits) + b * a.V;
@@ -898,13 +956,13 @@ __device__ __forceinline__ void draw_alone(RowShared& s, const SampleArgs& a, in
   }
   if (r.p_on) last = max(last, select_word<kRowThreads>(s.scratch.levels, kWordBits, 0, share_of(r.p, z), each, &with));
   for (int i = threadIdx.x; i < kMaxSteps; i += kRowThreads) s.sums[i] = 0;
-  __syncthreads();
+  lds_sync();
   each([&](uint64_t word, uint64_t w) {
     if (word < last) return;
     if (r.limit < kNone) w = weight(logit_of(word), r.limit);
     add64(&s.sums[index_of(word) / kStep], w);
   });
-  __syncthreads();
+  lds_sync();
   draw_from_steps<In>(s, a, b, r, weight, last);
 }
 
@@ -927,7 +985,7 @@ __global__ __launch_bounds__(kRowThreads, 6) void row_kernel(SampleArgs a) {
   }
   powers.fill();
   if (threadIdx.x == 0) s.n = 0;
-  __syncthreads();
+  lds_sync();
   const Weights weight(&powers, top, r.scale);
   if (r.kind == kTop) {
     draw_alone<In>(s, a, b, r, r.k, weight, 0);
@@ -990,10 +1048,10 @@ __global__ __launch_bounds__(kRowThreads, 6) void row_kernel(SampleArgs a) {
     if (lane == 0) st64(&a.sums[b * kMaxSteps + i0 / kStep], sum);
   }
   if (b_lo < kBins) {
-    __syncthreads();
+    lds_sync();
     if (threadIdx.x == 0)
       s.base = s.n ? __hip_atomic_fetch_add(&a.state[b].listed, s.n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
-    __syncthreads();
+    lds_sync();
     const unsigned base = s.base;
     for (unsigned i = threadIdx.x; i < min(s.n, (unsigned)kList) && base + i < kList; i += kRowThreads)
       st64(&a.list[b * kList + base + i], s.list[i]);
@@ -1010,14 +1068,14 @@ __global__ __launch_bounds__(kRowThreads, 6) void row_kernel(SampleArgs a) {
   for (int i = threadIdx.x; i < steps; i += kRowThreads) s.sums[i] = ld64(&a.sums[b * kMaxSteps + i]);
   if (b_lo < kBins) {
     for (unsigned i = threadIdx.x; i < n; i += kRowThreads) s.list[i] = ld64(&a.list[b * kList + i]);
-    __syncthreads();
+    lds_sync();
     last = last_kept<kRowThreads>(s.scratch, s.list, (int)n, st->k, r.p_on, r.p, weight, Pair{st->c_base, st->w_base}, st->total);
     for (unsigned i = threadIdx.x; i < n; i += kRowThreads) {
       const uint64_t word = s.list[i], w = word >= last ? weight(logit_of(word), r.limit) : 0;
       if (w) add64(&s.sums[index_of(word) / kStep], w);
     }
   }
-  __syncthreads();
+  lds_sync();
   draw_from_steps<In>(s, a, b, r, weight, last);
 }
 
