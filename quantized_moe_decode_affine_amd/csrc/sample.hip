@@ -23,6 +23,7 @@
 // Steps whose parts' maxima reach nothing that is kept are not read.  Where a list would
 // overflow (many equal logits) a workgroup selects from the row itself, digit by digit.
 #include <algorithm>
+#include <type_traits>
 
 #include "kernels.h"
 #include "wave64.h"
@@ -134,6 +135,11 @@ struct Logits {
     }
   }
   __device__ __forceinline__ float at(int j) const { return as_logit(raw[j]); }
+  // The same where a NaN and a zero's sign make no difference.
+  __device__ __forceinline__ float as_is(int j) const {
+    if constexpr (sizeof(In) == 2) return bf16_bits_to_f32(raw[j]);
+    else return raw[j];
+  }
 };
 
 // The place in the order: 50 bits, larger first.
@@ -143,52 +149,59 @@ __device__ __forceinline__ uint64_t word_of(float l, int i) {
 __device__ __forceinline__ int index_of(uint64_t word) { return (int)(kIndexMask - (word & kIndexMask)); }
 __device__ __forceinline__ float logit_of(uint64_t word) { return key_float((uint32_t)(word >> kIndexBits)); }
 
-// 2^(-j/64), the fractions of the weights' exponential.
+// 2^(45 - j/256), the fractions of the weights' exponential.
+constexpr int kPowers = 256;
 struct Powers {
-  double of[64];
+  double of[kPowers];
   __device__ __forceinline__ void fill() {
-    if (threadIdx.x < 64) of[threadIdx.x] = exp2(-(double)threadIdx.x / 64.0);
+    if (threadIdx.x < kPowers) of[threadIdx.x] = exp2(kOneBits - (double)threadIdx.x / kPowers);
   }
 };
 
-// A row's weights.
+// A row's weights.  kFinite (the row's largest logit is) leaves out what an infinite one needs.
 struct Weights {
   const Powers* pow;
   double top, scale;
   float top_f, scale_f;
   __device__ __forceinline__ Weights(const Powers* powers, float top_, double scale_)
       : pow(powers), top((double)top_), scale(scale_), top_f(top_), scale_f((float)scale_) {}
+  __device__ __forceinline__ bool finite() const { return top_f < __builtin_inff(); }
 
   // (max - l) / t in powers of two; a NaN for closed logits under an infinite t or maximum.
-  __device__ __forceinline__ double distance(float l) const { return l == top_f ? 0.0 : (top - (double)l) * scale; }
+  template <bool kFinite = false>
+  __device__ __forceinline__ double distance(float l) const {
+    const double y = (top - (double)l) * scale;
+    return !kFinite && l == top_f ? 0.0 : y;
+  }
 
   // Closed logits and those beyond 2^-46 of the largest have no weight, and change no
   // filter's end.
   __device__ __forceinline__ bool weighs(float l) const { return distance(l) < kNone; }
 
-  // 0 from `limit` on.  2^-y for y = n / 64 + r: the table's value for n % 64 with n / 64 off its
-  // exponent, times exp(-r ln 2) by its series to the fifth power (|r| <= 2^-7: 2^-52 of it is left out).
-  // No branches, so that several run at once; what is computed beyond the limit is not used.
+  // 0 from `limit` on, and for a NaN.  2^(45-y) for y = n / 256 + r: the table's value for n % 256
+  // with n / 256 off its exponent, times exp(-r ln 2) by its series to the fourth power (|r| <= 2^-9:
+  // 2^-54 of it is left out), rounded to an integer by the addition of 2^52: the sum's low bits.  No branches,
+  // so that several run at once; what is computed beyond the limit is not used.
+  template <bool kFinite = false>
   __device__ __forceinline__ uint64_t operator()(float l, double limit) const {
-    const double y = distance(l);
-    constexpr double kMagic = 6755399441055744.0;  // 1.5 * 2^52: the sum's low bits hold the integer
-    const double z = fma(y, 64.0, kMagic);
+    const double y = distance<kFinite>(l);
+    constexpr double kMagic = 6755399441055744.0 / kPowers;  // 1.5 * 2^52 steps of 1 / 256
+    const double z = y + kMagic;
     const uint32_t n = (uint32_t)__double_as_longlong(z);
-    const double r = fma(z - kMagic, -1.0 / 64.0, y);
-    constexpr double k1 = -0.69314718055994530942, k2 = k1 * k1 / 2, k3 = k2 * k1 / 3, k4 = k3 * k1 / 4, k5 = k4 * k1 / 5;
-    const double s = fma(fma(fma(fma(fma(k5, r, k4), r, k3), r, k2), r, k1), r, 1.0);
-    const uint64_t t = (uint64_t)__double_as_longlong(pow->of[n & 63]);
-    const double e = __longlong_as_double((long long)pair64((uint32_t)t, (uint32_t)(t >> 32) - (n >> 6 << 20))) * s;
-    // rounded to an integer by the addition: the low bits of 2^52 + v
-    constexpr double kOne = (double)(1ull << kOneBits);
-    const uint64_t w = (uint64_t)__double_as_longlong(fma(e, kOne, 4503599627370496.0));
+    const double r = y - (z - kMagic);
+    constexpr double k1 = -0.69314718055994530942, k2 = k1 * k1 / 2, k3 = k2 * k1 / 3, k4 = k3 * k1 / 4;
+    const double s = fma(fma(fma(fma(k4, r, k3), r, k2), r, k1), r, 1.0);
+    const uint64_t t = (uint64_t)__double_as_longlong(pow->of[n % kPowers]);
+    const uint64_t w = (uint64_t)__double_as_longlong(
+        fma(__longlong_as_double((long long)pair64((uint32_t)t, (uint32_t)(t >> 32) - (n / kPowers << 20))), s, 4503599627370496.0));
     return y < limit ? pair64((uint32_t)w, (uint32_t)(w >> 32) & 0xFFFFFu) : 0;
   }
 
   // Bins of the distance, as fine as its exponent and 8 bits from 2^-10 to 2^6; they follow the
   // order of the logits.
+  template <bool kFinite = false>
   __device__ __forceinline__ int bin(float l) const {
-    const float d = l == top_f ? 0.0f : (top_f - l) * scale_f;
+    const float v = (top_f - l) * scale_f, d = !kFinite && l == top_f ? 0.0f : v;
     constexpr int kFirst = (127 - 10) << 8;
     return min(max((int)(__float_as_uint(d) >> 15) - kFirst, 0), kBins - 1);
   }
@@ -786,19 +799,25 @@ __device__ __forceinline__ void band(BandShared& s, Powers& powers, const Sample
   const Weights weight(&powers, top, r.scale);
   const In* row = static_cast<const In*>(a.logits) + b * a.V;
   const int end = min((g + 1) * a.chunk, a.V);
-  for (int i = g * a.chunk + (int)threadIdx.x * kPer; i < end; i += kThreads * kPer) {
-    Logits<In> v;
-    v.load(row, i, end);
+  auto all = [&](auto finite) {
+    constexpr bool kFinite = decltype(finite)::value;
+    for (int i = g * a.chunk + (int)threadIdx.x * kPer; i < end; i += kThreads * kPer) {
+      Logits<In> v;
+      v.load(row, i, end);
+      uint64_t w[kPer];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const float l = v.at(j);
-      const uint64_t w = weight(l, kNone);
-      if (w == 0) continue;
-      const int bin = weight.bin(l);
-      add64(&s.w[bin], w);
-      if (r.k) atomicAdd(&s.c[bin], 1u);
+      for (int j = 0; j < kPer; ++j) w[j] = weight.template operator()<kFinite>(v.as_is(j), kNone);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        if (w[j] == 0) continue;
+        const int bin = weight.template bin<kFinite>(v.as_is(j));
+        add64(&s.w[bin], w[j]);
+        if (r.k) atomicAdd(&s.c[bin], 1u);
+      }
     }
-  }
+  };
+  if (weight.finite()) all(std::true_type{});
+  else all(std::false_type{});
   lds_sync();
   uint32_t* counts = a.counts + b * kBins;
   uint64_t* weights = a.weights + b * kBins;
@@ -973,9 +992,10 @@ __global__ __launch_bounds__(kRowThreads, 6) void row_kernel(SampleArgs a) {
   constexpr int kPer = Logits<In>::kPer, kLoads = kStep / kWave / kPer, kParts = kStep / kPart;
   const int64_t b = blockIdx.x / a.G;
   const int g = blockIdx.x % a.G;
+  const unsigned over = a.state[b].over;
   const RowRule r = row_rule(a, b);
   if (r.kind == kGreedy && a.top_k) return;  // front_kernel's
-  if (r.kind == kTop && (g > 0 || !a.state[b].over)) return;
+  if (r.kind == kTop && (g > 0 || !over)) return;
   const uint64_t peak = row_peak(a, b);
   const float top = logit_of(peak);
   if (r.kind == kGreedy || top == -__builtin_inff()) {
@@ -999,54 +1019,66 @@ __global__ __launch_bounds__(kRowThreads, 6) void row_kernel(SampleArgs a) {
   const In* row = static_cast<const In*>(a.logits) + b * a.V;
   const int wave = threadIdx.x / kWave, lane = lane_id();
   const int end = min((g + 1) * a.chunk, a.V);
-  for (int i0 = g * a.chunk + wave * kStep; i0 < end; i0 += kRowWaves * kStep) {
-    if (banded || r.limit < kNone) {  // what the step's largest logit does not reach none does
-      const int i = i0 / kPart + lane;
-      float most = lane < kParts && i < a.M ? a.parts[b * a.M + i] : -__builtin_inff();
-      most = fmaxf(most, dpp_f32<kDppQuadXor1>(most));
-      most = fmaxf(most, dpp_f32<kDppQuadXor2>(most));
-      most = fmaxf(most, dpp_f32<kDppRowHalfMirror>(most));
-      most = fmaxf(most, dpp_f32<kDppRowMirror>(most));
-      most = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(most)));
-      // (the list holds what min-p drops, too: the other filters count it)
-      if (b_lo < kBins ? !weight.weighs(most) || weight.bin(most) > b_hi : !weight(most, r.limit)) {
-        if (lane == 0) st64(&a.sums[b * kMaxSteps + i0 / kStep], 0);
-        continue;
-      }
-    }
-    Logits<In> v[kLoads];
-#pragma unroll
-    for (int o = 0; o < kLoads; ++o) v[o].load(row, i0 + (o * kWave + lane) * kPer, end);
-    uint64_t sum = 0;
-#pragma unroll
-    for (int o = 0; o < kLoads; ++o) {
-      if (b_lo == kBins) {
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) sum += weight(v[o].at(j), r.limit);
-      } else {
-        bool want[kPer], above[kPer], any = false;
-        uint64_t word[kPer];
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          const float l = v[o].at(j);
-          const int bin = weight.bin(l);
-          any |= above[j] = bin < b_lo;
-          want[j] = bin >= b_lo && bin <= b_hi && weight.weighs(l);
-          word[j] = word_of(l, i0 + (o * kWave + lane) * kPer + j);
+  auto all = [&](auto finite) {
+    constexpr bool kFinite = decltype(finite)::value;
+    for (int i0 = g * a.chunk + wave * kStep; i0 < end; i0 += kRowWaves * kStep) {
+      if (banded || r.limit < kNone) {  // what the step's largest logit does not reach none does
+        const int i = i0 / kPart + lane;
+        float most = lane < kParts && i < a.M ? a.parts[b * a.M + i] : -__builtin_inff();
+        most = fmaxf(most, dpp_f32<kDppQuadXor1>(most));
+        most = fmaxf(most, dpp_f32<kDppQuadXor2>(most));
+        most = fmaxf(most, dpp_f32<kDppRowHalfMirror>(most));
+        most = fmaxf(most, dpp_f32<kDppRowMirror>(most));
+        most = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(most)));
+        // (the list holds what min-p drops, too: the other filters count it)
+        if (b_lo < kBins ? !weight.weighs(most) || weight.bin(most) > b_hi : !weight(most, r.limit)) {
+          if (lane == 0) st64(&a.sums[b * kMaxSteps + i0 / kStep], 0);
+          continue;
         }
-        if (__any(any)) {
+      }
+      Logits<In> v[kLoads];
+#pragma unroll
+      for (int o = 0; o < kLoads; ++o) v[o].load(row, i0 + (o * kWave + lane) * kPer, end);
+      uint64_t sum = 0;
+#pragma unroll
+      for (int o = 0; o < kLoads; ++o) {
+        if (b_lo == kBins) {
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) sum += weight.template operator()<kFinite>(v[o].as_is(j), r.limit);
+        } else {
+          bool want[kPer], above[kPer], any = false, listed = false;
 #pragma unroll
           for (int j = 0; j < kPer; ++j) {
-            const uint64_t w = weight(v[o].at(j), r.limit);
-            sum += above[j] ? w : 0;
+            const int bin = weight.template bin<kFinite>(v[o].as_is(j));
+            any |= above[j] = bin < b_lo;
+            want[j] = bin >= b_lo && bin <= b_hi;
+            listed |= want[j];
+          }
+          if (__any(any)) {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+              const uint64_t w = weight.template operator()<kFinite>(v[o].as_is(j), r.limit);
+              sum += above[j] ? w : 0;
+            }
+          }
+          if (__any(listed)) {
+            uint64_t word[kPer];
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+              const float l = v[o].at(j);
+              want[j] = want[j] && weight.weighs(l);
+              word[j] = word_of(l, i0 + (o * kWave + lane) * kPer + j);
+            }
+            append(s.list, &s.n, want, word);
           }
         }
-        append(s.list, &s.n, want, word);
       }
+      sum = wave_sum_u64(sum);
+      if (lane == 0) st64(&a.sums[b * kMaxSteps + i0 / kStep], sum);
     }
-    sum = wave_sum_u64(sum);
-    if (lane == 0) st64(&a.sums[b * kMaxSteps + i0 / kStep], sum);
-  }
+  };
+  if (weight.finite()) all(std::true_type{});
+  else all(std::false_type{});
   if (b_lo < kBins) {
     lds_sync();
     if (threadIdx.x == 0)
