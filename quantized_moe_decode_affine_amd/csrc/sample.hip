@@ -50,10 +50,11 @@ static_assert(kMaxSampleVocab == 1 << kIndexBits, "an index fits its bits");
 // A row's state between the launches.
 struct RowState {
   unsigned band_arrived, row_arrived, listed, over;  // over: top-k's list overflowed
-  int b_lo, b_hi;               // the bins that are listed; b_lo = kBins: none
-  unsigned c_base;              // top-k: tokens in the bins before b_lo
+  float above, reach;           // logits above are kept by top-k and top-p, those from reach on are listed
+  int banded;                   // 0: neither ends in the row, all are kept
+  unsigned c_base;              // top-k: tokens above
   int k;                        // top-k among the tokens that have a weight, 0: none
-  uint64_t w_base, total;       // weight of the bins before b_lo, and the row's
+  uint64_t w_base, total;       // weight of those above, and the row's
 };
 
 struct SampleArgs {
@@ -75,7 +76,13 @@ struct SampleArgs {
   RowState* state;              // [B]
 };
 
-enum Kind { kGreedy, kAll, kTop, kBand, kSum };
+enum Kind {
+  kGreedy,
+  kAll,   // a list of all tokens
+  kTop,   // a list of the tokens that top-k, or min-p alone, may keep
+  kBand,  // the band in which top-p or a large top-k ends
+  kSum    // no filter
+};
 
 struct RowRule {
   Kind kind;
@@ -103,8 +110,9 @@ __device__ __forceinline__ RowRule row_rule(const SampleArgs& a, int64_t b) {
   }
   r.kind = !(t > 0.0f)                            ? kGreedy
            : a.V <= kList                         ? kAll
-           : r.k && r.k <= min(a.M / 2, kTopMost) ? kTop
-           : r.k || r.p_on                        ? kBand
+           : r.k ? (r.k <= min(a.M / 2, kTopMost) ? kTop : kBand)
+           : r.p_on                               ? kBand
+           : r.limit < kNone                      ? kTop
                                                   : kSum;
   return r;
 }
@@ -164,7 +172,7 @@ struct Weights {
   double top, scale;
   float top_f, scale_f;
   __device__ __forceinline__ Weights(const Powers* powers, float top_, double scale_)
-      : pow(powers), top((double)top_), scale(scale_), top_f(top_), scale_f((float)scale_) {}
+      : pow(powers), top((double)top_), scale(scale_), top_f(top_), scale_f(fminf((float)scale_, 3.402823466e38f)) {}  // (0 times it stays 0)
   __device__ __forceinline__ bool finite() const { return top_f < __builtin_inff(); }
 
   // (max - l) / t in powers of two; a NaN for closed logits under an infinite t or maximum.
@@ -276,9 +284,7 @@ __global__ __launch_bounds__(kPeakThreads) void peak_kernel(SampleArgs a) {
     for (int o = 1; o < kThreads / kWave; ++o) w = max(w, s_best[o]);
     a.peaks[b * a.G + g] = w;
     if (g == 0) {
-      RowState s{};
-      s.b_lo = s.b_hi = kBins;
-      a.state[b] = s;
+      a.state[b] = RowState{};
     }
   }
   if (row_rule(a, b).kind == kBand) {
@@ -438,6 +444,17 @@ __device__ __forceinline__ uint64_t select_word(Levels& s, int bits, uint32_t ne
 }
 
 template <int kThreads>
+__device__ __forceinline__ uint64_t block_or(uint64_t mine) {
+  __shared__ uint64_t s_w[kThreads / kWave];
+  mine = wave_reduce_u64(mine, [](uint64_t a, uint64_t b) { return a | b; });
+  lds_sync();  // an earlier call's are read
+  if (lane_id() == 0) s_w[threadIdx.x / kWave] = mine;
+  lds_sync();
+#pragma unroll
+  for (int o = 0; o < kThreads / kWave; ++o) mine |= s_w[o];
+  return mine;
+}
+template <int kThreads>
 __device__ __forceinline__ uint64_t block_min(uint64_t mine) {
   __shared__ uint64_t s_w[kThreads / kWave];
   mine = wave_max_u64(~mine);
@@ -449,13 +466,17 @@ __device__ __forceinline__ uint64_t block_min(uint64_t mine) {
   return ~mine;
 }
 
+// Up to so many tokens are compared with each other (n^2 / 8 cycles and a turn's latency; measured ...),
+// more are told apart by digits.
+constexpr int kRanked = 256;
+
 // What a list is decided with; the list has room for 8 words more than it holds.
 union Scratch {
   Levels levels;
   struct {
-    alignas(16) uint64_t w[512 + 8];
-    uint64_t heavier[512];
-    uint32_t place[512];
+    alignas(16) uint64_t w[kRanked + 8];
+    uint64_t heavier[kRanked];
+    uint32_t place[kRanked];
   } rank;
 };
 
@@ -466,7 +487,7 @@ union Scratch {
 template <int kThreads>
 __device__ __forceinline__ uint64_t last_kept(Scratch& s, uint64_t* list, int n, int k, bool p_on, double p,
                                               const Weights& weight, Pair base, uint64_t z) {
-  if (n <= kThreads) {
+  if (n <= kRanked) {
     // A token's place and the weight before it by comparison with all others: a token a thread, or
     // as many threads to a token as there are, each with a slice of the others, eight at a time.
     int across = kWave;
@@ -482,7 +503,7 @@ __device__ __forceinline__ uint64_t last_kept(Scratch& s, uint64_t* list, int n,
     }
     if (threadIdx.x < 8) {  // behind the last of the eights
       list[n + threadIdx.x] = 0;
-      if (across + (int)threadIdx.x < kThreads + 8) s.rank.w[across + threadIdx.x] = 0;
+      s.rank.w[across + threadIdx.x] = 0;
     }
     lds_sync();
     if (i - lane_id() < n && from < to) {
@@ -521,11 +542,14 @@ __device__ __forceinline__ uint64_t last_kept(Scratch& s, uint64_t* list, int n,
   auto each = [&](auto visit) {
     for (int i = threadIdx.x; i < n; i += kThreads) visit(list[i], weight(logit_of(list[i]), kNone));
   };
-  uint64_t word = 0;
+  // from the first bit on in which the words differ
+  uint64_t word = 0, differ = 0;
+  for (int i = threadIdx.x; i < n; i += kThreads) differ |= list[i] ^ list[0];
+  const int bits = 64 - __clzll((long long)(block_or<kThreads>(differ) | 1));
+  const uint64_t common = list[0] >> bits << bits;
   Pair with;
-  lds_sync();
   if (k && (uint32_t)k < base.c + n) {
-    word = select_word<kThreads>(s.levels, kWordBits, k - base.c, 0, each, &with);
+    word = common | select_word<kThreads>(s.levels, bits, k - base.c, 0, each, &with);
     z = base.w + with.w;
   } else if (k || z == 0) {  // all of them
     uint64_t mine = 0;
@@ -534,7 +558,7 @@ __device__ __forceinline__ uint64_t last_kept(Scratch& s, uint64_t* list, int n,
   }
   if (p_on) {
     const uint64_t need = share_of(p, z);
-    word = max(word, select_word<kThreads>(s.levels, kWordBits, 0, need > base.w ? need - base.w : 1, each, &with));
+    word = max(word, common | select_word<kThreads>(s.levels, bits, 0, need > base.w ? need - base.w : 1, each, &with));
   }
   // that word tells the list's tokens apart: the last one's own
   uint64_t last = ~0ull;
@@ -551,6 +575,7 @@ struct BandShared {
   uint32_t c[kBins];
   Pair before;
   int bin;
+  uint32_t edge[2];
 };
 
 struct PickShared {
@@ -675,31 +700,35 @@ __device__ __forceinline__ void pick(PickShared& s, Powers& powers, const Sample
     return;
   }
 
-  // the bin of the k-th largest of the parts' maxima
-  int bin[kOwnParts];
-#pragma unroll
-  for (int o = 0; o < kOwnParts; ++o) bin[o] = weight.weighs(l[o]) ? weight.bin(l[o]) : kBins;
-  for (int i = threadIdx.x; i < kBins; i += kThreads) s.bins[i] = 0;
-  if (threadIdx.x == 0) s.at = kBins - 1;  // fewer parts than k hold a token of any weight
-  lds_sync();
+  // The parts whose largest token is kept where min-p rules; for top-k those that reach the bin
+  // of the k-th largest of them.
+  int bin[kOwnParts], bound = kBins - 1;
 #pragma unroll
   for (int o = 0; o < kOwnParts; ++o)
-    if (bin[o] < kBins) atomicAdd(&s.bins[bin[o]], 1u);
-  lds_sync();
-  constexpr int kOwn = kBins / kThreads;
-  uint32_t in[kOwn];
+    bin[o] = weight.distance(l[o]) < (r.k ? kNone : r.limit) ? weight.bin(l[o]) : kBins;
+  if (r.k) {
+    for (int i = threadIdx.x; i < kBins; i += kThreads) s.bins[i] = 0;
+    if (threadIdx.x == 0) s.at = kBins - 1;  // fewer parts than k hold a token of any weight
+    lds_sync();
 #pragma unroll
-  for (int i = 0; i < kOwn; ++i) mine.c += in[i] = s.bins[threadIdx.x * kOwn + i];
-  uint32_t c = block_before<kThreads>(mine, &total).c;
+    for (int o = 0; o < kOwnParts; ++o)
+      if (bin[o] < kBins) atomicAdd(&s.bins[bin[o]], 1u);
+    lds_sync();
+    constexpr int kOwn = kBins / kThreads;
+    uint32_t in[kOwn];
 #pragma unroll
-  for (int i = 0; i < kOwn; ++i) {
-    if (c < (uint32_t)r.k && c + in[i] >= (uint32_t)r.k) s.at = threadIdx.x * kOwn + i;
-    c += in[i];
+    for (int i = 0; i < kOwn; ++i) mine.c += in[i] = s.bins[threadIdx.x * kOwn + i];
+    uint32_t c = block_before<kThreads>(mine, &total).c;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      if (c < (uint32_t)r.k && c + in[i] >= (uint32_t)r.k) s.at = threadIdx.x * kOwn + i;
+      c += in[i];
+    }
+    lds_sync();
+    bound = s.at;
   }
-  lds_sync();
-  const int bound = s.at;
-  // The parts that reach it, in order, and the least of their maxima: at least k tokens reach that.
-  // With fewer parts than k, every token of any weight (and some of none, which do not matter).
+  // These parts, in order, and the least of their maxima: at least k tokens reach that.  Without
+  // k parts, and for min-p, every token that may be kept (and some that may not, which do not matter).
   mine.c = 0;
   uint32_t least = ~0u;
 #pragma unroll
@@ -713,7 +742,7 @@ __device__ __forceinline__ void pick(PickShared& s, Powers& powers, const Sample
     if (bin[o] <= bound) s.parts[at++] = (uint16_t)(threadIdx.x * kOwnParts + o);
   least = (uint32_t)block_min<kThreads>(least);  // (its barriers are behind the parts' writes)
   const int parts = (int)total.c;
-  const float reach = fmaxf(parts < r.k ? top - (float)(kNone / r.scale) * 1.0001f : key_float(least), -3.402823466e38f);
+  const float reach = fmaxf(parts < r.k || !r.k ? top - (float)((r.k ? kNone : r.limit) / r.scale) * 1.0001f - fabsf(top) * 1e-6f : key_float(least), -3.402823466e38f);
   // Their tokens that do, in order: 16 bytes a lane, so a load covers kPer parts, kLoads of them
   // at a time and the next ones on their way (the barriers wait for LDS alone).
   constexpr int kPer = Logits<In>::kPer, kLanes = kPart / kPer, kLoads = 4, kTurn = kFrontWaves * kLoads * kPer;
@@ -875,10 +904,23 @@ __device__ __forceinline__ void band(BandShared& s, Powers& powers, const Sample
     lo = 0;
     base = Pair{0, 0};
   }
+  // the least logits of the bins before lo and up to hi: their keys bit by bit, as bins follow the logits
+  if (threadIdx.x < 2) {
+    const int most = threadIdx.x ? hi : lo - 1;
+    uint32_t key = 0;  // the largest below which a logit's bin is beyond `most`
+    for (int bit = 31; bit >= 0; --bit) {
+      const uint32_t up = key | 1u << bit;
+      const float l = key_float(up);
+      if (up <= float_key(top) && (!(l > -__builtin_inff()) || weight.bin(l) > most)) key = up;
+    }
+    s.edge[threadIdx.x] = key;
+  }
+  lds_sync();
   if (threadIdx.x == 0) {  // read by the next launch
     RowState* st = &a.state[b];
-    st->b_lo = lo;
-    st->b_hi = hi;
+    st->banded = lo < kBins;
+    st->above = key_float(s.edge[0]);
+    st->reach = key_float(s.edge[1] + 1);
     st->c_base = base.c;
     st->k = k;
     st->w_base = base.w;
@@ -888,7 +930,7 @@ __device__ __forceinline__ void band(BandShared& s, Powers& powers, const Sample
 
 // Workgroups 0 .. rows - 1: a row each; the others: a chunk's bins.
 template <typename In>
-__global__ __launch_bounds__(kFrontThreads, 6) void front_kernel(SampleArgs a, unsigned rows) {
+__global__ __launch_bounds__(kFrontThreads, 4) void front_kernel(SampleArgs a, unsigned rows) {
   __shared__ union Shared {
     BandShared band;
     PickShared pick;
@@ -907,6 +949,7 @@ struct RowShared {
   alignas(16) uint64_t list[kList + 8];
   Scratch scratch;
   uint64_t sums[kMaxSteps];
+  float queue[kRowWaves][2 * kWave];
   uint64_t found_w;
   unsigned n, base;
   int at;
@@ -967,7 +1010,7 @@ __device__ __forceinline__ void draw_alone(RowShared& s, const SampleArgs& a, in
       if (const uint64_t w = weight(l, kNone)) visit(word_of(l, i), w);
     }
   };
-  uint64_t last = 0;
+  uint64_t last = 0;  // (min-p alone: nothing to find)
   Pair with;
   if (k) {
     last = select_word<kRowThreads>(s.scratch.levels, kWordBits, k, 0, each, &with);
@@ -986,7 +1029,7 @@ __device__ __forceinline__ void draw_alone(RowShared& s, const SampleArgs& a, in
 }
 
 template <typename In>
-__global__ __launch_bounds__(kRowThreads, 6) void row_kernel(SampleArgs a) {
+__global__ __launch_bounds__(kRowThreads, 4) void row_kernel(SampleArgs a) {
   __shared__ RowShared s;
   __shared__ Powers powers;
   constexpr int kPer = Logits<In>::kPer, kLoads = kStep / kWave / kPer, kParts = kStep / kPart;
@@ -994,7 +1037,7 @@ __global__ __launch_bounds__(kRowThreads, 6) void row_kernel(SampleArgs a) {
   const int g = blockIdx.x % a.G;
   const unsigned over = a.state[b].over;
   const RowRule r = row_rule(a, b);
-  if (r.kind == kGreedy && a.top_k) return;  // front_kernel's
+  if (r.kind == kGreedy && (a.top_k || a.min_p)) return;  // front_kernel's
   if (r.kind == kTop && (g > 0 || !over)) return;
   const uint64_t peak = row_peak(a, b);
   const float top = logit_of(peak);
@@ -1012,17 +1055,19 @@ __global__ __launch_bounds__(kRowThreads, 6) void row_kernel(SampleArgs a) {
     return;
   }
 
-  // steps' sums; of a band's row those above the listed bins
-  const bool banded = r.kind == kBand;
+  // steps' sums; of a band's row those above what is listed
   const RowState* st = &a.state[b];
-  const int b_lo = banded ? st->b_lo : kBins, b_hi = banded ? st->b_hi : kBins;
+  const bool banded = r.kind == kBand && st->banded;
+  const float above = st->above, reach = st->reach;
   const In* row = static_cast<const In*>(a.logits) + b * a.V;
   const int wave = threadIdx.x / kWave, lane = lane_id();
   const int end = min((g + 1) * a.chunk, a.V);
   auto all = [&](auto finite) {
     constexpr bool kFinite = decltype(finite)::value;
+    auto value = [&](float l) { return weight.template operator()<kFinite>(l, r.limit); };
+    float* queue = s.queue[wave];
     for (int i0 = g * a.chunk + wave * kStep; i0 < end; i0 += kRowWaves * kStep) {
-      if (banded || r.limit < kNone) {  // what the step's largest logit does not reach none does
+      if (banded) {  // what the step's largest logit does not reach none does
         const int i = i0 / kPart + lane;
         float most = lane < kParts && i < a.M ? a.parts[b * a.M + i] : -__builtin_inff();
         most = fmaxf(most, dpp_f32<kDppQuadXor1>(most));
@@ -1030,8 +1075,7 @@ __global__ __launch_bounds__(kRowThreads, 6) void row_kernel(SampleArgs a) {
         most = fmaxf(most, dpp_f32<kDppRowHalfMirror>(most));
         most = fmaxf(most, dpp_f32<kDppRowMirror>(most));
         most = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(most)));
-        // (the list holds what min-p drops, too: the other filters count it)
-        if (b_lo < kBins ? !weight.weighs(most) || weight.bin(most) > b_hi : !weight(most, r.limit)) {
+        if (!(most >= reach)) {
           if (lane == 0) st64(&a.sums[b * kMaxSteps + i0 / kStep], 0);
           continue;
         }
@@ -1040,38 +1084,51 @@ __global__ __launch_bounds__(kRowThreads, 6) void row_kernel(SampleArgs a) {
 #pragma unroll
       for (int o = 0; o < kLoads; ++o) v[o].load(row, i0 + (o * kWave + lane) * kPer, end);
       uint64_t sum = 0;
+      if (!banded) {
 #pragma unroll
-      for (int o = 0; o < kLoads; ++o) {
-        if (b_lo == kBins) {
+        for (int o = 0; o < kLoads; ++o)
 #pragma unroll
-          for (int j = 0; j < kPer; ++j) sum += weight.template operator()<kFinite>(v[o].as_is(j), r.limit);
-        } else {
-          bool want[kPer], above[kPer], any = false, listed = false;
+          for (int j = 0; j < kPer; ++j) sum += value(v[o].as_is(j));
+      } else {
+        // What is above goes through a queue, so that weights are computed for 64 of them at a time
+        // however few they are.
+        int queued = 0;
+#pragma unroll
+        for (int o = 0; o < kLoads; ++o) {
+          bool listed = false;
 #pragma unroll
           for (int j = 0; j < kPer; ++j) {
-            const int bin = weight.template bin<kFinite>(v[o].as_is(j));
-            any |= above[j] = bin < b_lo;
-            want[j] = bin >= b_lo && bin <= b_hi;
-            listed |= want[j];
-          }
-          if (__any(any)) {
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-              const uint64_t w = weight.template operator()<kFinite>(v[o].as_is(j), r.limit);
-              sum += above[j] ? w : 0;
+            const float l = v[o].as_is(j);
+            const uint64_t ball = __ballot(l > above);
+            listed |= l >= reach && !(l > above);
+            if (ball == 0) continue;  // uniform
+            if (l > above)
+              queue[queued + __builtin_amdgcn_mbcnt_hi((uint32_t)(ball >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)ball, 0))] = l;
+            queued += __popcll(ball);
+            if (queued >= kWave) {
+              __builtin_amdgcn_wave_barrier();
+              const float first = queue[lane], rest = queue[lane + kWave];
+              __builtin_amdgcn_wave_barrier();  // the queue is the wave's own, and LDS keeps its order
+              queue[lane] = rest;
+              sum += value(first);
+              queued -= kWave;
             }
           }
           if (__any(listed)) {
+            bool want[kPer];
             uint64_t word[kPer];
 #pragma unroll
             for (int j = 0; j < kPer; ++j) {
               const float l = v[o].at(j);
-              want[j] = want[j] && weight.weighs(l);
+              want[j] = l >= reach && !(l > above) && weight.weighs(l);
               word[j] = word_of(l, i0 + (o * kWave + lane) * kPer + j);
             }
             append(s.list, &s.n, want, word);
           }
         }
+        __builtin_amdgcn_wave_barrier();
+        if (lane < queued) sum += value(queue[lane]);
+        __builtin_amdgcn_wave_barrier();
       }
       sum = wave_sum_u64(sum);
       if (lane == 0) st64(&a.sums[b * kMaxSteps + i0 / kStep], sum);
@@ -1079,7 +1136,7 @@ __global__ __launch_bounds__(kRowThreads, 6) void row_kernel(SampleArgs a) {
   };
   if (weight.finite()) all(std::true_type{});
   else all(std::false_type{});
-  if (b_lo < kBins) {
+  if (banded) {
     lds_sync();
     if (threadIdx.x == 0)
       s.base = s.n ? __hip_atomic_fetch_add(&a.state[b].listed, s.n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
@@ -1091,14 +1148,14 @@ __global__ __launch_bounds__(kRowThreads, 6) void row_kernel(SampleArgs a) {
   if (!last_to_arrive(&a.state[b].row_arrived, a.G)) return;
 
   uint64_t last = 0;
-  const unsigned n = b_lo < kBins ? __hip_atomic_load(&a.state[b].listed, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
+  const unsigned n = banded ? __hip_atomic_load(&a.state[b].listed, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
   if (n > kList) {
     draw_alone<In>(s, a, b, r, st->k, weight, st->total);
     return;
   }
   const int steps = (a.V + kStep - 1) / kStep;
   for (int i = threadIdx.x; i < steps; i += kRowThreads) s.sums[i] = ld64(&a.sums[b * kMaxSteps + i]);
-  if (b_lo < kBins) {
+  if (banded) {
     for (unsigned i = threadIdx.x; i < n; i += kRowThreads) s.list[i] = ld64(&a.list[b * kList + i]);
     lds_sync();
     last = last_kept<kRowThreads>(s.scratch, s.list, (int)n, st->k, r.p_on, r.p, weight, Pair{st->c_base, st->w_base}, st->total);
@@ -1146,9 +1203,9 @@ hipError_t launch_sample(const SampleArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL(peak_kernel<In>, dim3(chunks), dim3(kPeakThreads), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (a.top_k || a.top_p) {
-    const unsigned picks = a.top_k ? rows : 0;  // a list decides a row only where there is a top-k
-    hipLaunchKernelGGL(front_kernel<In>, dim3(picks + chunks), dim3(kFrontThreads), 0, stream, a, picks);
+  if (a.top_k || a.top_p || a.min_p) {
+    const unsigned picks = a.top_k || a.min_p ? rows : 0;  // what a list decides
+    hipLaunchKernelGGL(front_kernel<In>, dim3(picks + (a.top_k || a.top_p ? chunks : 0)), dim3(kFrontThreads), 0, stream, a, picks);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
