@@ -111,17 +111,18 @@ constexpr int lcm(int a, int b) { return a % b == 0 ? a : b % a == 0 ? b : a * b
 // while the ones before are multiplied, and puts them into the other of two LDS buffers at the
 // end; a lane then reads its row's 8 bytes once a K step and keeps the 4 that its half of the
 // wave multiplies with.  K is a multiple of 64; the last K step is filled up with zeros.
-template <int WM, int WN, int FM, int FN, int kStages, int EPI>
+template <int WM, int WN, int FM, int FN, int kStages, int EPI, bool kWide>
 __device__ __forceinline__ void mx4_tile_body(const Mx4GemmArgs& p) {
   constexpr int TM = WM * FM * 32, TN = WN * FN * 32, kWaves = WM * WN;
   constexpr int kOps = (TM + TN) / 8 / kWaves;  // DMA loads per wave and step, 8 rows each
   static_assert((TM + TN) / 8 % kWaves == 0 && (kStages == 2 || kStages == 3), "whole blocks of 8 rows per wave");
   static_assert(TM + TN <= kWaves * kWave, "a thread for each row's scales");
   constexpr int kStageBytes = (TM + TN) * kStepBytes;
-  constexpr int kScale = 2;  // K steps of a scale buffer
-  // a row's scales in a buffer: 24 bytes spread 32 rows over all banks; where three stages leave
-  // no room for the pad, 16 (two rows a bank)
-  constexpr int kScalePitch = kScale * kStepScales + (kStages == 2 ? 8 : 0);
+  // Wide: one buffer of kScale K steps, 64 bytes a row, or 32 where three stages leave no room for more.
+  // Otherwise two of two K steps; a row's 16 bytes padded to 24 spread 32 rows over all banks, unpadded
+  // two rows share a bank.
+  constexpr int kScale = !kWide ? 2 : kStages == 2 ? 8 : 4;
+  constexpr int kScalePitch = kScale * kStepScales + (!kWide && kStages == 2 ? 8 : 0);
   // one array per stage, so that the compiler can tell a stage's reads from the loads
   // still filling another
   __shared__ __align__(16) uint8_t s_st0[kStageBytes], s_st1[kStageBytes];
@@ -130,7 +131,7 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4GemmArgs& p) {
     __shared__ __align__(16) uint8_t s_st2[kStageBytes];
     st2 = s_st2;
   }
-  __shared__ __align__(16) uint8_t s_sc[2][(TM + TN) * kScalePitch];
+  __shared__ __align__(16) uint8_t s_sc[kWide ? 1 : 2][(TM + TN) * kScalePitch];
   constexpr bool kSwiglu = EPI == kEpiSwiglu;
   constexpr int kCols = kSwiglu ? TN / 2 : TN;  // output columns of a tile
   const int lane = lane_id();
@@ -232,11 +233,12 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4GemmArgs& p) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, stage(st) + dst[j], 16, at, k0, 0, 0);
   };
 
-  // This thread's row of scales (threads beyond the rows repeat some).  Rows and columns outside
-  // the matrices take another's: their sums are not stored.
+  // ---- scales, narrow: this thread's row (threads beyond the rows repeat some).  Rows and columns
+  // outside the matrices take another's: their sums are not stored.
   const int srow = threadIdx.x % (TM + TN);
-  const uint8_t* sp;
-  if (srow < TM) {
+  const uint8_t* sp = p.sa;
+  if (kWide) {
+  } else if (srow < TM) {
     sp = p.sa + source(srow) * Ks;
   } else {
     const int b = (srow - TM) / 32;  // block of 32 rows of the stage
@@ -253,7 +255,6 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4GemmArgs& p) {
     for (int o = 0; o < kScale; ++o) {
       const int at = (chunk * kScale + o) * kStepScales, from = min(at, max(Ks, kStepScales) - kStepScales);
       __builtin_memcpy(&held[o], sp + from, kStepScales);
-      held[o] >>= min(at - from, kStepScales - 1) * 8;
     }
   };
   auto load_short = [&] {  // rows of fewer than 8: one K step
@@ -268,8 +269,52 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4GemmArgs& p) {
   auto scale_at = [&](int r, int step) { return r * kScalePitch + step * kStepScales; };
   auto put_scales = [&](int chunk) __attribute__((always_inline)) {
 #pragma unroll
-    for (int o = 0; o < kScale; ++o)
-      *reinterpret_cast<uint64_t*>(s_sc[chunk & 1] + scale_at(srow, o)) = held[o];
+    for (int o = 0; o < kScale; ++o) {
+      const int at = (chunk * kScale + o) * kStepScales, from = min(at, max(Ks, kStepScales) - kStepScales);
+      // (shifted here, not where it is loaded: a use would wait for the load)
+      *reinterpret_cast<uint64_t*>(s_sc[chunk & 1] + scale_at(srow, o)) = held[o] >> min(at - from, kStepScales - 1) * 8;
+    }
+  };
+
+  // ---- scales, wide: DMA loads of 16 bytes, kPieces lanes to a row.  A row's pieces are XOR-rotated by the
+  // rows whose banks would repeat.
+  constexpr int kPieces = kScale * kStepScales / 16, kRowsPer = kWave / kPieces;
+  constexpr int kScaleOps = ((TM + TN) / kRowsPer + kWaves - 1) / kWaves;  // loads per wave and buffer
+  auto piece_swz = [](int r) { return kPieces == 4 ? (r >> 2) & 3 : (r >> 3) & 1; };
+  int soff[kWide ? kScaleOps : 1];
+  // (uniform) first row of the j-th load's rows in the stage; the last ones repeat some
+  auto scale_rows = [&](int j) { return min(wave * kScaleOps + j, (TM + TN) / kRowsPer - 1) * kRowsPer; };
+  if constexpr (kWide) {
+#pragma unroll
+    for (int j = 0; j < kScaleOps; ++j) {
+      const int r = scale_rows(j) + lane / kPieces;
+      uint32_t row;
+      bool inside = true;
+      if (r < TM) {
+        row = p.row_src ? (uint32_t)source(r) : (uint32_t)r;
+        inside = r < rows;
+      } else {
+        const int blk = (r - TM) / 32;
+        row = (kSwiglu ? blk / FN * kPairs + blk % kPairs : blk) * 32 + r % 32;
+      }
+      soff[j] = inside ? (int)(row * (uint32_t)Ks + (uint32_t)(lane % kPieces ^ piece_swz(r)) * 16) : (int)0xFFFFFFF0u;
+    }
+  }
+  // (the chunk after the last one is not used: it repeats the last)
+  auto issue_scales = [&](int chunk) __attribute__((always_inline)) {
+    const int k0 = min(chunk, (steps - 1) / kScale) * (kScale * kStepScales);
+#pragma unroll
+    for (int j = 0; j < kScaleOps; ++j) {
+      // which matrix: uniform, and selected as an address (a selected descriptor went through scratch memory)
+      const int r = scale_rows(j);
+      const uint8_t* at = p.row_src ? p.sa : p.sa + first * Ks;
+      uint32_t bytes = (p.row_src ? p.a_rows : (uint32_t)rows) * (uint32_t)Ks;
+      if (r >= TM) {
+        at = (kSwiglu && (r - TM) / 32 % FN >= kPairs ? w2.scales : w.scales) + (e_row + n0) * Ks;
+        bytes = (uint32_t)min(kCols, p.N - n0) * (uint32_t)Ks;
+      }
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(at, bytes), s_sc[0] + r * kScalePitch, 16, soff[j], k0, 0, 0);
+    }
   };
 
   // Operand reads run one MFMA step (64 columns) ahead of the products.  At the end of a K
@@ -282,41 +327,54 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4GemmArgs& p) {
   auto run = [&](auto nf_c) __attribute__((always_inline)) {
     constexpr int NF = decltype(nf_c)::value;
     i32x4_t a[2][NF > 0 ? NF : 1], b[2][FN];
-    uint32_t xa[2][NF > 0 ? NF : 1], xb[2][FN];
+    uint32_t xa[NF > 0 ? NF : 1], xb[FN];
     auto read = [&](const uint8_t* base, int kk, int set) __attribute__((always_inline)) {
       __builtin_amdgcn_sched_barrier(0);  // these reads go out before the products that follow in the source
       if constexpr (NF > 0) {
-        const int c = 2 * kk + h;
+        // (a row's rotation is that of the row 32 further: one address for all blocks)
+        const int c = ((2 * kk + h) ^ row_swz(m)) << 4;
 #pragma unroll
-        for (int f = 0; f < NF; ++f) {
-          const int r = (wm * FM + f) * 32 + m;
-          a[set][f] = *reinterpret_cast<const i32x4_t*>(base + r * kStepBytes + ((c ^ row_swz(r)) << 4));
-        }
+        for (int f = 0; f < NF; ++f)
+          a[set][f] = *reinterpret_cast<const i32x4_t*>(base + (wm * FM * 32 + m) * kStepBytes + c + f * 32 * kStepBytes);
 #pragma unroll
-        for (int f = 0; f < FN; ++f) {
-          const int r = TM + (wn * FN + f) * 32 + m;
-          b[set][f] = *reinterpret_cast<const i32x4_t*>(base + r * kStepBytes + ((c ^ row_swz(r)) << 4));
-        }
+        for (int f = 0; f < FN; ++f)
+          b[set][f] = *reinterpret_cast<const i32x4_t*>(base + (TM + wn * FN * 32 + m) * kStepBytes + c + f * 32 * kStepBytes);
       }
       __builtin_amdgcn_sched_barrier(0);
     };
-    // the scales of K step i, whose chunk's buffer and place in it are those of u
-    auto read_scales = [&](int buffer, int step, int set) __attribute__((always_inline)) {
+    // a K step's scales: a row's eight, on their way while the last products of the step before run,
+    // then those of them that this lane multiplies with
+    typedef typename std::conditional<kWide, uint4, uint2>::type raw_t;  // wide: of two K steps
+    raw_t raw_a[NF > 0 ? NF : 1], raw_b[FN];
+    auto read_scales = [&](int buffer, int step) __attribute__((always_inline)) {
       if constexpr (NF > 0) {
-        auto one = [&](int r) {
-          const uint2 v = *reinterpret_cast<const uint2*>(s_sc[buffer] + scale_at(r, step));
-          return __builtin_amdgcn_perm(v.y, v.x, pick);
-        };
+        const int in_row = kWide ? (step / 2 ^ piece_swz(m)) * 16 : step * kStepScales;  // (as that of the row 32 further)
+        const uint8_t* at = s_sc[kWide ? 0 : buffer] + in_row;
 #pragma unroll
-        for (int f = 0; f < NF; ++f) xa[set][f] = one((wm * FM + f) * 32 + m);
+        for (int f = 0; f < NF; ++f)
+          raw_a[f] = *reinterpret_cast<const raw_t*>(at + (wm * FM * 32 + m) * kScalePitch + f * 32 * kScalePitch);
 #pragma unroll
-        for (int f = 0; f < FN; ++f) xb[set][f] = one(TM + (wn * FN + f) * 32 + m);
+        for (int f = 0; f < FN; ++f)
+          raw_b[f] = *reinterpret_cast<const raw_t*>(at + (TM + wn * FN * 32 + m) * kScalePitch + f * 32 * kScalePitch);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto take_scales = [&](auto u_c) __attribute__((always_inline)) {
+      auto mine = [&](const auto& v) {
+        if constexpr (kWide && decltype(u_c)::value % 2 == 1) return __builtin_amdgcn_perm(v.w, v.z, pick);
+        else return __builtin_amdgcn_perm(v.y, v.x, pick);
+      };
+      if constexpr (NF > 0) {
+#pragma unroll
+        for (int f = 0; f < NF; ++f) xa[f] = mine(raw_a[f]);
+#pragma unroll
+        for (int f = 0; f < FN; ++f) xb[f] = mine(raw_b[f]);
       }
     };
     // One MFMA step of operand set kk % 2, with the loads [j0, j1) of a K step into stage st
     // between its products.
-    auto mul = [&](auto kk_c, auto sc_c, int i, auto st_c, auto j0_c, auto j1_c) __attribute__((always_inline)) {
-      constexpr int kk = decltype(kk_c)::value, set = kk % 2, sc = decltype(sc_c)::value;
+    auto mul = [&](auto kk_c, int i, auto st_c, auto j0_c, auto j1_c) __attribute__((always_inline)) {
+      constexpr int kk = decltype(kk_c)::value, set = kk % 2;
       constexpr int st = decltype(st_c)::value, j0 = decltype(j0_c)::value, j1 = decltype(j1_c)::value;
       constexpr int kPer = (j1 - j0 + NF - 1) / (NF > 0 ? NF : 1);  // loads after each row of products
 #pragma unroll
@@ -324,8 +382,7 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4GemmArgs& p) {
 #pragma unroll
         for (int fn = 0; fn < FN; ++fn)
           acc[fm][fn] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-              mx4_operand(b[set][fn]), mx4_operand(a[set][fm]), acc[fm][fn], kFp4, kFp4, kk, (int)xb[sc][fn], kk,
-              (int)xa[sc][fm]);
+              mx4_operand(b[set][fn]), mx4_operand(a[set][fm]), acc[fm][fn], kFp4, kFp4, kk, (int)xb[fn], kk, (int)xa[fm]);
         if constexpr (j1 > j0) {
           __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -351,32 +408,39 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4GemmArgs& p) {
     using Half = std::integral_constant<int, kOps / 2>;
     using All = std::integral_constant<int, kOps>;
     // K step i = u modulo the unrolled steps.  kk = 0's operands are in set 0 and the step's
-    // scales in set u % 2 on entry, and the next step's on return.
-    constexpr int kUnroll = lcm(lcm(kStages, kScale), 2);
+    // scales on their way on entry, and the next step's on return.
+    constexpr int kUnroll = lcm(kStages, kScale);
     auto step = [&](int i, auto u_c) __attribute__((always_inline)) {
       constexpr int u = decltype(u_c)::value, st = u % kStages;
       using St = std::integral_constant<int, st>;
-      using Sc = std::integral_constant<int, u % 2>;
       using Free = std::integral_constant<int, (st + kStages - 1) % kStages>;  // the stage read before this one
-      if constexpr (u % kScale == 0) load_scales(i / kScale + 1);
+      // Wide: the scales of the buffer's last two K steps were read before the workgroup last met, so its next
+      // ones go out in the last of them, and land before the workgroup meets again.
+      constexpr bool kNext = kWide && u % kScale == kScale - 1;
+      take_scales(u_c);
+      if constexpr (kNext) issue_scales(i / kScale + 1);
+      if constexpr (!kWide && u % kScale == 0) load_scales(i / kScale + 1);
       read(stage(st), 1, 1);
-      mul(C0{}, Sc{}, i + kStages - 1, Free{}, Half{}, All{});
+      mul(C0{}, i + kStages - 1, Free{}, Half{}, All{});
       read(stage(st), 2, 0);
-      mul(C1{}, Sc{}, 0, St{}, C0{}, C0{});
+      mul(C1{}, 0, St{}, C0{}, C0{});
       read(stage(st), 3, 1);
-      mul(C2{}, Sc{}, 0, St{}, C0{}, C0{});
-      if constexpr (u % kScale == kScale - 1) put_scales(i / kScale + 1);
-      meet(std::integral_constant<int, kOps * (kStages - 2)>{});
+      mul(C2{}, 0, St{}, C0{}, C0{});
+      if constexpr (!kWide && u % kScale == kScale - 1) put_scales(i / kScale + 1);
+      // (three stages: of what may still be in flight only the second half of this step's loads is younger)
+      meet(std::integral_constant<int, (kNext && kStages > 2 ? kOps - kOps / 2 : kOps * (kStages - 2))>{});
       read(stage((st + 1) % kStages), 0, 0);
-      read_scales((i + 1) / kScale & 1, (u + 1) % kScale, (u + 1) % 2);
-      mul(C3{}, Sc{}, i + kStages, St{}, C0{}, Half{});
+      if constexpr (!kWide || u % 2 == 1) read_scales((i + 1) / kScale & 1, (u + 1) % kScale);
+      mul(C3{}, i + kStages, St{}, C0{}, Half{});
     };
-    if (Ks < kStepScales) load_short();
-    else load_scales(0);
-    put_scales(0);
+    if constexpr (!kWide) {
+      if (Ks < kStepScales) load_short();
+      else load_scales(0);
+      put_scales(0);
+    }
     meet(std::integral_constant<int, kOps * (kStages - 2) + kOps / 2>{});
     read(stage(0), 0, 0);
-    read_scales(0, 0, 0);
+    read_scales(0, 0);
     int i = 0;
     for (; i + kUnroll <= steps; i += kUnroll)
       each_of([&](auto u_c) { step(i + decltype(u_c)::value, u_c); }, std::make_integer_sequence<int, kUnroll>{});
@@ -386,6 +450,7 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4GemmArgs& p) {
         },
         std::make_integer_sequence<int, kUnroll - 1>{});
   };
+  if constexpr (kWide) issue_scales(0);
 #pragma unroll
   for (int st = 0; st < kStages; ++st)
 #pragma unroll
@@ -496,9 +561,16 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4GemmArgs& p) {
   }
 }
 
-template <int WM, int WN, int FM, int FN, int kStages, int EPI>
-__global__ __launch_bounds__(WM* WN* kWave, 8 / (WM * WN)) void mx4_tile_kernel(Mx4GemmArgs p) {
-  mx4_tile_body<WM, WN, FM, FN, kStages, EPI>(p);
+template <int WM, int WN, int FM, int FN, int kStages, int EPI, bool kWide>
+__global__ __launch_bounds__(WM* WN* kWave, 2) void mx4_tile_kernel(Mx4GemmArgs p) {
+  mx4_tile_body<WM, WN, FM, FN, kStages, EPI, kWide>(p);
+}
+
+// Rows of scales that 16-byte loads can take.
+bool wide_scales(const Mx4GemmArgs& p) {
+  uintptr_t at = reinterpret_cast<uintptr_t>(p.sa) | (uintptr_t)(p.K / kMxBlock);
+  for (const Mx4Mat* m : {&p.W, &p.W2, &p.S, &p.S2}) at |= reinterpret_cast<uintptr_t>(m->scales);
+  return at % 16 == 0;
 }
 
 template <int WM, int WN, int FM, int FN, int kStages, int EPI>
@@ -510,8 +582,9 @@ hipError_t launch_tiles(Mx4GemmArgs p, int64_t tiles, hipStream_t stream) {
                                  : (tiles * p.n_slices + kXcds - 1) / kXcds * kXcds;
   if (blocks <= 0) return hipSuccess;
   if (blocks * (WM * WN * kWave) > kMaxThreads) return hipErrorInvalidValue;  // bounded by the callers
-  hipLaunchKernelGGL((mx4_tile_kernel<WM, WN, FM, FN, kStages, EPI>), dim3((unsigned)blocks),
-                     dim3(WM * WN * kWave), 0, stream, p);
+  const dim3 grid((unsigned)blocks), threads(WM * WN * kWave);
+  if (wide_scales(p)) hipLaunchKernelGGL((mx4_tile_kernel<WM, WN, FM, FN, kStages, EPI, true>), grid, threads, 0, stream, p);
+  else hipLaunchKernelGGL((mx4_tile_kernel<WM, WN, FM, FN, kStages, EPI, false>), grid, threads, 0, stream, p);
   return hipGetLastError();
 }
 

@@ -1170,10 +1170,11 @@ __global__ __launch_bounds__(kRowThreads, 4) void row_kernel(SampleArgs a) {
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
-// A row's chunks: about four workgroups a compute unit over all rows.
+// A row's chunks: two workgroups a compute unit over all rows, as many as fit together (256 rows under
+// a top-p: 137 us against 165 with four), none for fewer than 4,096 tokens (37 rows of 32,003: 44 us against 55 with 2,048).
 void split(int64_t B, int V, int* G, int* chunk) {
-  const int64_t want = std::max<int64_t>(1, 4 * (int64_t)device_cu_count() / std::max<int64_t>(B, 1));
-  const int64_t n = std::max<int64_t>(1, std::min<int64_t>({want, kMaxChunks, (V + 2047) / 2048}));
+  const int64_t want = std::max<int64_t>(1, 2 * (int64_t)device_cu_count() / std::max<int64_t>(B, 1));
+  const int64_t n = std::max<int64_t>(1, std::min<int64_t>({want, kMaxChunks, (V + 4095) / 4096}));
   *chunk = (int)(((V + n - 1) / n + 2047) / 2048 * 2048);  // whole steps, and a peak's reads of either type
   *G = (V + *chunk - 1) / *chunk;
 }
