@@ -1010,7 +1010,7 @@ __device__ __forceinline__ void draw_alone(RowShared& s, const SampleArgs& a, in
       if (const uint64_t w = weight(l, kNone)) visit(word_of(l, i), w);
     }
   };
-  uint64_t last = 0;  // (min-p alone: nothing to find)
+  uint64_t last = 0;
   Pair with;
   if (k) {
     last = select_word<kRowThreads>(s.scratch.levels, kWordBits, k, 0, each, &with);
@@ -1038,7 +1038,8 @@ __global__ __launch_bounds__(kRowThreads, 4) void row_kernel(SampleArgs a) {
   const unsigned over = a.state[b].over;
   const RowRule r = row_rule(a, b);
   if (r.kind == kGreedy && (a.top_k || a.min_p)) return;  // front_kernel's
-  if (r.kind == kTop && (g > 0 || !over)) return;
+  // A list that overflowed: under top-k one workgroup selects from the row, under min-p alone the steps are added.
+  if (r.kind == kTop && (!over || (r.k && g > 0))) return;
   const uint64_t peak = row_peak(a, b);
   const float top = logit_of(peak);
   if (r.kind == kGreedy || top == -__builtin_inff()) {
@@ -1050,7 +1051,7 @@ __global__ __launch_bounds__(kRowThreads, 4) void row_kernel(SampleArgs a) {
   if (threadIdx.x == 0) s.n = 0;
   lds_sync();
   const Weights weight(&powers, top, r.scale);
-  if (r.kind == kTop) {
+  if (r.kind == kTop && r.k) {
     draw_alone<In>(s, a, b, r, r.k, weight, 0);
     return;
   }
@@ -1067,7 +1068,7 @@ __global__ __launch_bounds__(kRowThreads, 4) void row_kernel(SampleArgs a) {
     auto value = [&](float l) { return weight.template operator()<kFinite>(l, r.limit); };
     float* queue = s.queue[wave];
     for (int i0 = g * a.chunk + wave * kStep; i0 < end; i0 += kRowWaves * kStep) {
-      if (banded) {  // what the step's largest logit does not reach none does
+      if (banded || r.limit < kNone) {  // what the step's largest logit does not reach none does
         const int i = i0 / kPart + lane;
         float most = lane < kParts && i < a.M ? a.parts[b * a.M + i] : -__builtin_inff();
         most = fmaxf(most, dpp_f32<kDppQuadXor1>(most));
@@ -1075,7 +1076,7 @@ __global__ __launch_bounds__(kRowThreads, 4) void row_kernel(SampleArgs a) {
         most = fmaxf(most, dpp_f32<kDppRowHalfMirror>(most));
         most = fmaxf(most, dpp_f32<kDppRowMirror>(most));
         most = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(most)));
-        if (!(most >= reach)) {
+        if (banded ? !(most >= reach) : !weight(most, r.limit)) {
           if (lane == 0) st64(&a.sums[b * kMaxSteps + i0 / kStep], 0);
           continue;
         }
@@ -1170,10 +1171,11 @@ __global__ __launch_bounds__(kRowThreads, 4) void row_kernel(SampleArgs a) {
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
-// A row's chunks: two workgroups a compute unit over all rows, as many as fit together (256 rows under
-// a top-p: 137 us against 165 with four), none for fewer than 4,096 tokens (37 rows of 32,003: 44 us against 55 with 2,048).
+// A row's chunks: four workgroups a compute unit over all rows (256 rows of mixed parameters, few of which
+// need every chunk: 103 us against 133 with two and 96 with eight; all under a top-p of 0.9: 164, 137 and more),
+// none for fewer than 4,096 tokens (37 rows of 32,003: 44 us against 55 with 2,048).
 void split(int64_t B, int V, int* G, int* chunk) {
-  const int64_t want = std::max<int64_t>(1, 2 * (int64_t)device_cu_count() / std::max<int64_t>(B, 1));
+  const int64_t want = std::max<int64_t>(1, 4 * (int64_t)device_cu_count() / std::max<int64_t>(B, 1));
   const int64_t n = std::max<int64_t>(1, std::min<int64_t>({want, kMaxChunks, (V + 4095) / 4096}));
   *chunk = (int)(((V + n - 1) / n + 2047) / 2048 * 2048);  // whole steps, and a peak's reads of either type
   *G = (V + *chunk - 1) / *chunk;

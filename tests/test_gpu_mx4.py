@@ -146,7 +146,8 @@ def test_gemm_exact(B, m, n, k):
     assert torch.equal(B.mx4_gemm(W, x, B.OUT_BF16), ref.float().bfloat16())
 
 
-@pytest.mark.parametrize("m,n,k", [(256, 256, 256), (256, 512, 16384), (200, 130, 28608)])
+@pytest.mark.parametrize("m,n,k", [(256, 256, 256), (256, 512, 16384), (200, 130, 28608), (70, 200, 4096), (90, 4000, 1536),
+                                   (1100, 1500, 2560), (4100, 4200, 512), (4100, 4200, 1024), (4100, 4200, 4608), (33, 65, 512)])
 def test_gemm_tiles_over_many_steps(B, m, n, k):
     """The scale buffers and stages taken in turn many times, each tile size (chosen by rows)."""
     X, v, w = _exact_case(k, m, n, k)
@@ -184,6 +185,18 @@ def test_gemm_extreme_scales_and_nan(B):
         nan[:, [7, 9]] = nan[[2, 3]] = True
         assert (np.isnan(y) == nan).all()
         assert (np.abs(y - ref)[~nan] <= k * HALF * size[~nan] + 2.0 ** -149 * k).all()
+
+
+def test_gemm_scales_at_any_place(B):
+    """Scales at addresses that 16-byte loads cannot take: the results of those that they can."""
+    for m, n, k in ((40, 70, 512), (300, 600, 2048), (4100, 4100, 1024)):
+        X, v, w = _exact_case(m, m, n, k)
+        x, W = B.bf16_tensor(X), _dev(B, w)
+        buf = torch.zeros(n * (k // 32) + 64, dtype=torch.uint8, device="cuda")
+        for start in (2, 4, 8):
+            sc = buf[start:start + n * (k // 32)].view(1, n, k // 32)
+            sc.copy_(W.scales)
+            assert torch.equal(B.mx4_gemm(B.DeviceMx4(W.codes, sc), x), B.mx4_gemm(W, x))
 
 
 def test_gemm_stack_and_row_of_neighbours(B):
@@ -297,7 +310,7 @@ def _values(mats):
 @pytest.mark.parametrize("T,E,H,inter,k,shared", [
     (1, 4, 64, 64, 2, False), (1, 8, 2048, 512, 8, True), (2, 8, 128, 64, 2, True), (7, 5, 320, 192, 4, False),
     (16, 3, 704, 128, 4, True), (3, 40, 1088, 704, 20, True), (17, 6, 128, 64, 3, True), (65, 8, 64, 64, 2, False),
-    (40, 60, 1088, 704, 4, True), (333, 7, 320, 448, 5, True), (200, 2, 576, 64, 1, False), (9, 1, 64, 64, 32, True)])
+    (40, 60, 1088, 704, 4, True), (333, 7, 320, 448, 5, True), (150, 6, 1024, 512, 3, True), (700, 3, 512, 1536, 2, True), (200, 2, 576, 64, 1, False), (9, 1, 64, 64, 32, True)])
 def test_experts(B, T, E, H, inter, k, shared):
     case = _experts_case(T + E + H, T, E, H, inter, k, shared)
     X, ids, w, mats, sh = case

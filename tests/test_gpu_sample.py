@@ -147,6 +147,23 @@ def test_scales_of_logits(B):
             _check(B, logits, rng.random(n), np.full(n, t), None if k is None else np.full(n, k), None if p is None else np.full(n, p))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_lists_that_overflow(B, dtype):
+    """Flat rows: more tokens than a list holds under min-p alone, under top-k by ties, and in top-p's band."""
+    rng = np.random.default_rng(21)
+    V, n = 60000, 6
+    flat = _logits(rng, n, V, 0.4, dtype)
+    u = rng.random(n)
+    for m in (0.01, 0.2, 0.5, 0.9):
+        _check(B, flat, u, None, None, None, np.full(n, m))
+        _check(B, flat, u, rng.choice([0.3, 1.0, 2.0], n), None, None, np.full(n, m))
+    steps = torch.round(flat.float() * 8) / 8   # some tens of values: thousands of tokens to each
+    steps = steps.bfloat16() if dtype == "bf16" else steps
+    for k, p, m in ((30, None, None), (300, 0.5, None), (None, 0.5, None), (None, 0.99, 0.3), (5000, 0.9, None), (None, None, 0.6)):
+        full = lambda v: None if v is None else np.full(n, v)  # noqa: E731
+        _check(B, steps, u, rng.choice([0.2, 1.0], n), full(k), full(p), full(m))
+
+
 def test_frequencies(B):
     """Draws by evenly spaced numbers occur as often as their probability says, to within one."""
     rng = np.random.default_rng(8)
