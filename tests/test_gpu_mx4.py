@@ -132,7 +132,7 @@ def _exact_case(seed, m, n, k):
 
 GEMM = [(1, 16, 64), (1, 1, 64), (2, 5, 128), (3, 33, 192), (1, 1024, 2048), (5, 20, 8192), (16, 100, 576), (16, 17000, 256),
         (9, 16400, 704), (17, 16, 64), (17, 40, 128), (40, 70, 192), (64, 64, 256), (65, 129, 320), (33, 1027, 832), (16, 96, 28672),
-        (381, 1027, 832), (300, 250, 8192), (128, 2048, 512), (1000, 3, 448), (2100, 2300, 384), (4200, 4300, 320), (16, 200, 16384)]
+        (381, 1027, 832), (300, 250, 8192), (128, 2048, 512), (1000, 3, 448), (2100, 2300, 384), (4200, 4300, 320), (16, 200, 16384), (16, 50, 7680), (16, 17000, 7680), (8, 30, 15360)]
 
 
 @pytest.mark.parametrize("m,n,k", GEMM)
@@ -310,7 +310,7 @@ def _values(mats):
 @pytest.mark.parametrize("T,E,H,inter,k,shared", [
     (1, 4, 64, 64, 2, False), (1, 8, 2048, 512, 8, True), (2, 8, 128, 64, 2, True), (7, 5, 320, 192, 4, False),
     (16, 3, 704, 128, 4, True), (3, 40, 1088, 704, 20, True), (17, 6, 128, 64, 3, True), (65, 8, 64, 64, 2, False),
-    (40, 60, 1088, 704, 4, True), (333, 7, 320, 448, 5, True), (150, 6, 1024, 512, 3, True), (700, 3, 512, 1536, 2, True), (200, 2, 576, 64, 1, False), (9, 1, 64, 64, 32, True)])
+    (40, 60, 1088, 704, 4, True), (333, 7, 320, 448, 5, True), (150, 6, 1024, 512, 3, True), (700, 3, 512, 1536, 2, True), (8, 2, 7680, 64, 2, False), (2, 2, 64, 16384, 2, True), (200, 2, 576, 64, 1, False), (9, 1, 64, 64, 32, True)])
 def test_experts(B, T, E, H, inter, k, shared):
     case = _experts_case(T + E + H, T, E, H, inter, k, shared)
     X, ids, w, mats, sh = case
