@@ -2,7 +2,7 @@
 // and dispatch to the kernel launchers.  Declarations and the contract of
 // every entry point are in include/q4moe.h.
 #include "../../include/q4moe.h"
-#include "kernels.h"
+#include "steps.h"
 
 #include <algorithm>
 #include <cmath>

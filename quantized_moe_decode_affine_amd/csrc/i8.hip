@@ -14,7 +14,7 @@
 
 #include "i8_tiles.h"
 #include "int8.h"
-#include "kernels.h"
+#include "steps.h"
 
 namespace q4moe {
 

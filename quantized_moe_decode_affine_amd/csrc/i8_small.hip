@@ -11,7 +11,7 @@
 #include <algorithm>
 
 #include "int8.h"
-#include "kernels.h"
+#include "steps.h"
 
 namespace q4moe {
 

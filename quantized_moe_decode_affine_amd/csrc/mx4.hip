@@ -11,7 +11,7 @@
 #include <utility>
 
 #include "i8_tiles.h"
-#include "kernels.h"
+#include "steps.h"
 #include "mx4.h"
 
 namespace q4moe {

@@ -10,7 +10,7 @@
 // which memory brings them.
 #include <algorithm>
 
-#include "kernels.h"
+#include "steps.h"
 #include "mx4.h"
 
 namespace q4moe {

@@ -25,7 +25,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "kernels.h"
+#include "steps.h"
 #include "wave64.h"
 
 namespace q4moe {
