@@ -6,8 +6,13 @@
 // One pass: a row's t stay in registers between its sums and its results.  The sum of squares
 // and what the codes' borders hang on (y, the largest |t w|, y / scale) are in fp64, so a
 // code is the definition's: in fp32 about one code in 50,000 fell on the other side of a
-// border.  The fp64 operations cost nothing beside the bytes: about ten an element, at a rate
-// of 64 a clock and compute unit.
+// border.  The fp64 operations hide behind the bytes: about ten an element, at a rate of 64 a
+// clock and compute unit.
+//
+// Bound by memory: 8191 rows of 4096 with a residual and a bf16 result take 49.8 us, 5.4 TB/s
+// (a copy of 1 GiB reaches 5.2); 4096 rows of 2048 with a residual to codes 17 us (59 MB,
+// some of it still in the last cache).  One row of 2048 takes 3 us (bf16) to 4 (codes): the
+// launch, a turn of memory and the reduction.
 #include <algorithm>
 
 #include "int8.h"
@@ -33,33 +38,70 @@ struct NormArgs {
 
 constexpr uint64_t kInf64 = 0x7FF0000000000000ull;
 
-// kTeam waves to a row, kHeld chunks of 8 columns a lane (kTeam * kHeld * 512 >= k); 4 waves a
-// workgroup, or kTeam.  The weights' chunks stay in registers over the rows of a workgroup.
-template <int kTeam, int kHeld, bool kCodes>
-__global__ __launch_bounds__(kTeam > 4 ? kTeam * kWave : 4 * kWave) void rms_norm_kernel(NormArgs p) {
-  constexpr int kWaves = kTeam > 4 ? kTeam : 4, kRows = kWaves / kTeam;  // rows at a time
+// kLanes lanes to a row (a part of a wave, a wave, or several), kHeld chunks of 8 columns a lane
+// (kLanes * kHeld * 8 >= k); 4 waves a workgroup, or a row's.  A whole wave to rows of 128
+// columns, as the norm of an attention's heads has them, would leave three lanes of four idle:
+// 65,536 such rows to codes 17.5 us against 51.8.  The weights' chunks stay in registers over
+// the rows of a workgroup, but for rows of more than 16384 columns: their registers hold t,
+// and weights and residual come two chunks at a time (256 rows of 32768 to codes 19.4 us
+// against 56.3 with everything held, which spills).
+template <int kLanes>
+struct NormShape {
+  static constexpr int kTeam = kLanes > kWave ? kLanes / kWave : 1;  // waves to a row
+  static constexpr int kWaves = kTeam > 4 ? kTeam : 4;
+  static constexpr int kRows = kWaves * kWave / kLanes;  // rows at a time
+};
+
+template <int kLanes, int kHeld, bool kCodes>
+__global__ __launch_bounds__(NormShape<kLanes>::kWaves* kWave) void rms_norm_kernel(NormArgs p) {
+  constexpr int kTeam = NormShape<kLanes>::kTeam, kWaves = NormShape<kLanes>::kWaves, kRows = NormShape<kLanes>::kRows;
+  constexpr int kPart = kLanes < kWave ? kLanes : kWave;
+  constexpr bool kKeep = kLanes < 1024 || kHeld <= 2;
+  constexpr int kGroup = kKeep ? kHeld : 2;  // chunks of the residual in flight
   __shared__ double s_sum[kTeam > 1 ? kWaves : 1];
   __shared__ uint64_t s_most[kTeam > 1 ? kWaves : 1];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int part = wave % kTeam;
-  const int j0 = (part * kWave + lane_id()) * 8;
-  constexpr int kStep = kTeam * kWave * 8;
-  u16x8_t w[kHeld];
+  const int j0 = (part * kWave + lane_id() % kPart) * 8;
+  constexpr int kStep = kLanes * 8;
+  const auto weight = [&](int c) { return *reinterpret_cast<const u16x8_t*>(p.w + min(j0 + c * kStep, p.k - 8)); };
+  u16x8_t kept[kKeep ? kHeld : 1];
+  if constexpr (kKeep) {
 #pragma unroll
-  for (int c = 0; c < kHeld; ++c) w[c] = *reinterpret_cast<const u16x8_t*>(p.w + min(j0 + c * kStep, p.k - 8));
-  for (int64_t row = (int64_t)blockIdx.x * kRows + wave / kTeam; row < p.rows; row += (int64_t)gridDim.x * kRows) {
-    u16x8_t t[kHeld], r[kHeld];
+    for (int c = 0; c < kHeld; ++c) kept[c] = weight(c);
+  }
+  const auto w = [&](int c) {
+    if constexpr (kKeep) return kept[c];
+    else return weight(c);
+  };
+  // Of a wave's rows the first: lanes whose own lies past the last one read the last and write
+  // nothing, so that the whole wave takes part in what follows.
+  for (int64_t first = (int64_t)blockIdx.x * kRows + (kLanes < kWave ? wave * (kWave / kPart) : wave / kTeam);
+       first < p.rows; first += (int64_t)gridDim.x * kRows) {
+    int64_t row = first;
+    bool live = true;
+    if constexpr (kLanes < kWave) {
+      row = first + lane_id() / kPart;
+      live = row < p.rows;
+      row = min(row, p.rows - 1);
+    }
+    u16x8_t t[kHeld], r[kGroup];
     const int64_t at = row * p.k;
 #pragma unroll
     for (int c = 0; c < kHeld; ++c) t[c] = *reinterpret_cast<const u16x8_t*>(p.x + at + min(j0 + c * kStep, p.k - 8));
     if (p.r) {
 #pragma unroll
-      for (int c = 0; c < kHeld; ++c) r[c] = *reinterpret_cast<const u16x8_t*>(p.r + at + min(j0 + c * kStep, p.k - 8));
+      for (int g = 0; g < kHeld; g += kGroup) {
 #pragma unroll
-      for (int c = 0; c < kHeld; ++c) {
+        for (int c = 0; c < kGroup; ++c)
+          r[c] = *reinterpret_cast<const u16x8_t*>(p.r + at + min(j0 + (g + c) * kStep, p.k - 8));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t[c][i] = i8_bf16(bf16_bits_to_f32(t[c][i]) + bf16_bits_to_f32(r[c][i]));
-        if (j0 + c * kStep < p.k) *reinterpret_cast<u16x8_t*>(p.total + at + j0 + c * kStep) = t[c];
+        for (int c = 0; c < kGroup; ++c) {
+          u16x8_t& v = t[g + c];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = i8_bf16(bf16_bits_to_f32(v[i]) + bf16_bits_to_f32(r[c][i]));
+          if (live && j0 + (g + c) * kStep < p.k) *reinterpret_cast<u16x8_t*>(p.total + at + j0 + (g + c) * kStep) = v;
+        }
       }
     }
     double sum = 0.0;
@@ -67,18 +109,19 @@ __global__ __launch_bounds__(kTeam > 4 ? kTeam * kWave : 4 * kWave) void rms_nor
 #pragma unroll
     for (int c = 0; c < kHeld; ++c) {
       if (j0 + c * kStep >= p.k) continue;
+      const u16x8_t wc = w(c);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const double v = bf16_bits_to_f32(t[c][i]);
         sum = fma(v, v, sum);
         if constexpr (kCodes) {  // as bits: a NaN lies above infinity
-          const double u = v * (double)bf16_bits_to_f32(w[c][i]);
+          const double u = v * (double)bf16_bits_to_f32(wc[i]);
           most = max(most, (uint64_t)__double_as_longlong(u) & 0x7FFFFFFFFFFFFFFFull);
         }
       }
     }
-    sum = wave_sum_f64(sum);
-    if constexpr (kCodes) most = wave_max_u64(most);
+    sum = wave_sum_f64<kPart>(sum);
+    if constexpr (kCodes) most = wave_max_u64<kPart>(most);
     if constexpr (kTeam > 1) {
       if (lane_id() == 0) {
         s_sum[wave] = sum;
@@ -99,10 +142,11 @@ __global__ __launch_bounds__(kTeam > 4 ? kTeam * kWave : 4 * kWave) void rms_nor
       const float f = (float)inv;
 #pragma unroll
       for (int c = 0; c < kHeld; ++c) {
+        const u16x8_t wc = w(c);
         u16x8_t o;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = i8_bf16(bf16_bits_to_f32(t[c][i]) * f * bf16_bits_to_f32(w[c][i]));
-        if (j0 + c * kStep < p.k) *reinterpret_cast<u16x8_t*>(p.y + at + j0 + c * kStep) = o;
+        for (int i = 0; i < 8; ++i) o[i] = i8_bf16(bf16_bits_to_f32(t[c][i]) * f * bf16_bits_to_f32(wc[i]));
+        if (live && j0 + c * kStep < p.k) *reinterpret_cast<u16x8_t*>(p.y + at + j0 + c * kStep) = o;
       }
     } else {
       const bool bad = most >= kInf64 || !(sum < __longlong_as_double((long long)kInf64));
@@ -110,33 +154,34 @@ __global__ __launch_bounds__(kTeam > 4 ? kTeam * kWave : 4 * kWave) void rms_nor
       const double per = scale > 0.0f ? inv / (double)scale : 0.0;  // zero and NaN scales: codes 0
 #pragma unroll
       for (int c = 0; c < kHeld; ++c) {
+        const u16x8_t wc = w(c);
         uint32_t q[2] = {};
         u16x8_t o;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const double u = (double)bf16_bits_to_f32(t[c][i]) * (double)bf16_bits_to_f32(w[c][i]);
+          const double u = (double)bf16_bits_to_f32(t[c][i]) * (double)bf16_bits_to_f32(wc[i]);
           const int code = scale > 0.0f ? max(-127, min(127, (int)rint(u * per))) : 0;
           q[i / 4] |= (uint32_t)(code & 0xFF) << (8 * (i % 4));
           o[i] = i8_bf16((float)(u * inv));
         }
-        if (j0 + c * kStep < p.k) {
+        if (live && j0 + c * kStep < p.k) {
           *reinterpret_cast<uint2*>(p.codes + at + j0 + c * kStep) = make_uint2(q[0], q[1]);
           if (p.y) *reinterpret_cast<u16x8_t*>(p.y + at + j0 + c * kStep) = o;
         }
       }
-      if (part == 0 && lane_id() == 0) p.scales[row] = scale;
+      if (live && part == 0 && lane_id() % kPart == 0) p.scales[row] = scale;
     }
   }
 }
 
-template <int kTeam, int kHeld>
+template <int kLanes, int kHeld>
 hipError_t launch_norm(const NormArgs& p, hipStream_t stream) {
-  constexpr int kWaves = kTeam > 4 ? kTeam : 4, kRows = kWaves / kTeam;
+  constexpr int kWaves = NormShape<kLanes>::kWaves, kRows = NormShape<kLanes>::kRows;
   // two workgroups' worth of waves a SIMD and more: the rest in turn, with the weights held
   const int64_t most = (int64_t)device_cu_count() * (32 / kWaves);
   const dim3 grid((unsigned)std::min<int64_t>((p.rows + kRows - 1) / kRows, most)), threads(kWaves * kWave);
-  if (p.codes) hipLaunchKernelGGL((rms_norm_kernel<kTeam, kHeld, true>), grid, threads, 0, stream, p);
-  else hipLaunchKernelGGL((rms_norm_kernel<kTeam, kHeld, false>), grid, threads, 0, stream, p);
+  if (p.codes) hipLaunchKernelGGL((rms_norm_kernel<kLanes, kHeld, true>), grid, threads, 0, stream, p);
+  else hipLaunchKernelGGL((rms_norm_kernel<kLanes, kHeld, false>), grid, threads, 0, stream, p);
   return hipGetLastError();
 }
 
@@ -145,16 +190,22 @@ hipError_t launch_norm(const NormArgs& p, hipStream_t stream) {
 hipError_t run_rms_norm(const uint16_t* x, const uint16_t* r, const uint16_t* w, int64_t rows, int k, double eps,
                         uint16_t* total, uint16_t* y, int8_t* codes, float* scales, hipStream_t stream) {
   const NormArgs p{x, r, w, rows, k, eps, total, y, codes, scales};
-  // Few rows: four waves to each, for the latency.
+  // Up to two rows a compute unit: four waves to each, for the latency (2048 columns to codes:
+  // 512 rows 4.8 us against 5.6 with a wave to each, 1 row 3.7 against 4.7).  More rows: a wave
+  // to each, which needs no barrier (1024 rows 6.1 us against 6.9, 8192 rows of 1024 18.6
+  // against 26.2).
   const bool few = rows <= 2 * (int64_t)device_cu_count();
-  if (k <= 512) return launch_norm<1, 1>(p, stream);
-  if (!few && k <= 1024) return launch_norm<1, 2>(p, stream);
-  if (!few && k <= 2048) return launch_norm<1, 4>(p, stream);
-  if (k <= 2048) return launch_norm<4, 1>(p, stream);
-  if (k <= 4096) return launch_norm<4, 2>(p, stream);
-  if (k <= 8192) return launch_norm<4, 4>(p, stream);
-  if (k <= 16384) return launch_norm<16, 2>(p, stream);
-  return launch_norm<16, 8>(p, stream);
+  if (k <= 128) return launch_norm<16, 1>(p, stream);
+  if (k <= 256) return launch_norm<32, 1>(p, stream);
+  if (k <= 512) return launch_norm<64, 1>(p, stream);
+  if (!few && k <= 1024) return launch_norm<64, 2>(p, stream);
+  if (!few && k <= 2048) return launch_norm<64, 4>(p, stream);
+  if (k <= 2048) return launch_norm<256, 1>(p, stream);
+  if (k <= 4096) return launch_norm<256, 2>(p, stream);
+  if (k <= 8192) return launch_norm<256, 4>(p, stream);
+  if (k <= 16384) return launch_norm<1024, 2>(p, stream);
+  if (k <= 32768) return launch_norm<1024, 4>(p, stream);
+  return launch_norm<1024, 8>(p, stream);
 }
 
 }  // namespace q4moe

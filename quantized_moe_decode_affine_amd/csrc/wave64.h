@@ -9,29 +9,34 @@ namespace q4moe {
 
 __device__ __forceinline__ uint64_t pair64(uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; }
 
-// op over the wave's values, in every lane; both partners of a step combine the same two.
-template <typename Op>
+// op over the values of kLanes neighbouring lanes (16, 32 or the wave), in every lane; both
+// partners of a step combine the same two.
+template <int kLanes = kWave, typename Op>
 __device__ __forceinline__ uint64_t wave_reduce_u64(uint64_t v, Op op) {
   v = op(v, pair64(dpp_u32<kDppQuadXor1>((uint32_t)v), dpp_u32<kDppQuadXor1>((uint32_t)(v >> 32))));
   v = op(v, pair64(dpp_u32<kDppQuadXor2>((uint32_t)v), dpp_u32<kDppQuadXor2>((uint32_t)(v >> 32))));
   v = op(v, pair64(dpp_u32<kDppRowHalfMirror>((uint32_t)v), dpp_u32<kDppRowHalfMirror>((uint32_t)(v >> 32))));
   v = op(v, pair64(dpp_u32<kDppRowMirror>((uint32_t)v), dpp_u32<kDppRowMirror>((uint32_t)(v >> 32))));
+  if constexpr (kLanes == 16) return v;
   uint32_t al, bl, ah, bh;
   swap_rows16((uint32_t)v, al, bl);
   swap_rows16((uint32_t)(v >> 32), ah, bh);
   v = op(pair64(al, ah), pair64(bl, bh));
+  if constexpr (kLanes == 32) return v;
   swap_halves32((uint32_t)v, al, bl);
   swap_halves32((uint32_t)(v >> 32), ah, bh);
   return op(pair64(al, ah), pair64(bl, bh));
 }
 
+template <int kLanes = kWave>
 __device__ __forceinline__ double wave_sum_f64(double v) {
-  return __longlong_as_double((long long)wave_reduce_u64((uint64_t)__double_as_longlong(v), [](uint64_t a, uint64_t b) {
+  return __longlong_as_double((long long)wave_reduce_u64<kLanes>((uint64_t)__double_as_longlong(v), [](uint64_t a, uint64_t b) {
     return (uint64_t)__double_as_longlong(__longlong_as_double((long long)a) + __longlong_as_double((long long)b));
   }));
 }
+template <int kLanes = kWave>
 __device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
-  return wave_reduce_u64(v, [](uint64_t a, uint64_t b) { return max(a, b); });
+  return wave_reduce_u64<kLanes>(v, [](uint64_t a, uint64_t b) { return max(a, b); });
 }
 __device__ __forceinline__ uint64_t wave_sum_u64(uint64_t v) {
   return wave_reduce_u64(v, [](uint64_t a, uint64_t b) { return a + b; });

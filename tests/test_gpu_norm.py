@@ -46,7 +46,8 @@ def _check_codes(codes, scales, y):
 
 
 SHAPES = [(1, 8), (3, 64), (5, 200), (1, 512), (7, 520), (600, 1024), (600, 1000), (1, 2048), (700, 2048), (513, 2040),
-          (2, 4096), (515, 4104), (3, 8192), (2, 8200), (1, 16384), (2, 16392), (1, 65536), (2, 50000), (4097, 64)]
+          (2, 4096), (515, 4104), (3, 8192), (2, 8200), (1, 16384), (2, 16392), (1, 65536), (2, 50000), (4097, 64),
+          (1, 128), (3, 128), (65, 128), (40000, 128), (9, 136), (33, 256), (5, 264), (2, 32768), (3, 32776)]
 
 
 @pytest.mark.parametrize("rows,k", SHAPES)
