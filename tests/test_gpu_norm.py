@@ -85,6 +85,20 @@ def test_total_over_an_input(B, rows, k):
         assert torch.equal(ins[1 - over], (x, r)[1 - over])
 
 
+@pytest.mark.parametrize("rows,k", [(5, 128), (3, 8), (65, 256), (2, 512), (2, 1000), (1, 16392), (2, 40000)])
+def test_leaves_rows_behind(B, rows, k):
+    """Rows behind the last one, in every buffer that is written, stay as they were; the stream's state in place."""
+    X, R, w = _rows(1, rows, k), _rows(2, rows, k), B.bf16_tensor(_rows(3, 1, k)[0])
+    want = B.rms_norm_i8(B.bf16_tensor(X), w, EPS, residual=B.bf16_tensor(R))
+    codes, scales = torch.full((rows + 9, k), 77, dtype=torch.int8, device="cuda"), torch.full((rows + 9,), 7.0, device="cuda")
+    y, x = (torch.full((rows + 9, k), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    x[:rows] = B.bf16_tensor(X)
+    got = B.rms_norm_i8(x[:rows], w, EPS, residual=B.bf16_tensor(R), total=x[:rows], codes=codes[:rows], scales=scales[:rows],
+                        out=y[:rows])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert (codes[rows:] == 77).all() and all((t[rows:] == 7).all() for t in (scales, y, x))
+
+
 def test_extremes(B):
     k = 256
     x = np.zeros((12, k))
