@@ -29,7 +29,8 @@ from collections import defaultdict
 PKG = os.path.dirname(os.path.abspath(__file__))
 DECODE_SOURCES = ("decode.hip", "common.h", "vecstage.h", "topk.h", "kernels.h", "handoff.h")
 ALL_SOURCES = ("abi.hip", "decode.hip", "decode_batch.hip", "gemm.hip", "gemv.hip", "route.hip", "common.h", "kernels.h", "topk.h",
-               "vecstage.h", "handoff.h", "preprows.h", "select.hip", "i8.hip", "i8_small.hip", "i8_tiles.h", "int8.h")
+               "vecstage.h", "handoff.h", "preprows.h", "select.hip", "i8.hip", "i8_small.hip", "i8_tiles.h", "int8.h",
+               "steps.h", "wave64.h", "norm.hip", "mx4.h", "mx4.hip", "mx4_small.hip", "sample.hip")
 
 
 def _sha256(names) -> str:
