@@ -66,6 +66,7 @@ __global__ __launch_bounds__(NormShape<kLanes>::kWaves* kWave) void rms_norm_ker
   constexpr int kStep = kLanes * 8;
   const auto weight = [&](int c) { return *reinterpret_cast<const u16x8_t*>(p.w + min(j0 + c * kStep, p.k - 8)); };
   u16x8_t kept[kKeep ? kHeld : 1];
+  bool large = false, looked = false;
   if constexpr (kKeep) {
 #pragma unroll
     for (int c = 0; c < kHeld; ++c) kept[c] = weight(c);
@@ -138,7 +139,8 @@ __global__ __launch_bounds__(NormShape<kLanes>::kWaves* kWave) void rms_norm_ker
     }
     const double inv = 1.0 / sqrt(sum / p.k + p.eps);
     if constexpr (!kCodes) {
-      // two fp32 roundings of 2^-24 before the one to bf16
+      // Two fp32 roundings of 2^-24 before the one to bf16.  t * f may lie below 2^-126, where fp32 is
+      // off by up to 2^-150; weights below 2^14 make that 2^-136 at most, an eighth of bf16's last bit.
       const float f = (float)inv;
 #pragma unroll
       for (int c = 0; c < kHeld; ++c) {
@@ -147,6 +149,21 @@ __global__ __launch_bounds__(NormShape<kLanes>::kWaves* kWave) void rms_norm_ker
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = i8_bf16(bf16_bits_to_f32(t[c][i]) * f * bf16_bits_to_f32(wc[i]));
         if (live && j0 + c * kStep < p.k) *reinterpret_cast<u16x8_t*>(p.y + at + j0 + c * kStep) = o;
+      }
+      if (!looked) {  // at the weights once, and here, where no row's loads wait for them
+        u16x8_t most = {};
+#pragma unroll
+        for (int c = 0; c < kHeld; ++c) most = __builtin_elementwise_max(most, w(c) & (uint16_t)0x7FFF);
+        large = __any(__builtin_reduce_max(most) >= 0x4680) != 0;  // 2^14
+        looked = true;
+      }
+      // Larger weights, and a factor that is below 2^-126 itself, take fp64: again, from memory, so that
+      // the registers are the ordinary rows'.
+      if (large || __any(f < 0x1p-126f)) {
+        const uint16_t* from = (p.r ? p.total : p.x) + at;
+#pragma unroll 1
+        for (int j = live ? j0 : p.k; j < p.k; j += j % 8 == 7 ? kStep - 7 : 1)
+          p.y[at + j] = i8_bf16((float)((double)bf16_bits_to_f32(from[j]) * (double)bf16_bits_to_f32(p.w[j]) * inv));
       }
     } else {
       const bool bad = most >= kInf64 || !(sum < __longlong_as_double((long long)kInf64));

@@ -236,3 +236,27 @@ def test_binding_refusals(B):
             bad()
         assert err.value.status == B.EINVAL
     assert B.rms_norm(x[:0], w).shape == (0, 64)
+
+
+@pytest.mark.parametrize("rows,k", [(5, 64), (3, 200), (4, 512), (700, 1000), (2, 2048), (3, 4104), (2, 8200), (2, 20000), (1, 40000)])
+def test_range_of_values_and_weights(B, rows, k):
+    """Values and weights of every size that the type has: what underflows on the way to y, but not in y, is not lost."""
+    rng = np.random.default_rng(k)
+    x, w = (rng.choice([-1.0, 1.0], n) * np.exp2(rng.uniform(-130, 127, n)) for n in ((rows, k), k))
+    x[0] = 2.0 ** -100
+    x[0, 0] = 2.0 ** 60                     # a small value beside a large one, under a large weight: 2^-160 on the way
+    w[:4] = 2.0 ** 60, 2.0 ** 60, 1.0, 2.0 ** 100
+    x[-1] = 3e38 * rng.uniform(0.1, 1, k)   # the norm's factor itself is below 2^-126
+    for most in (2.0 ** 127, 2.0 ** 14, 2.0 ** 13.9, 1.0):
+        v = np.clip(w, -most, most)
+        X, W = synth.to_bf16_bits(x.astype(np.float32)), synth.to_bf16_bits(v.astype(np.float32))
+        _, y = orc.rms_norm(X, W, EPS)
+        xt, wt = B.bf16_tensor(X), B.bf16_tensor(W)
+        both = torch.empty_like(xt)
+        B.rms_norm_i8(xt, wt, EPS, out=both)
+        want = orc.f64_to_bf16(y)
+        big = np.isinf(want)
+        for got in (B.rms_norm(xt, wt, EPS), both):
+            got = qorc.bf16_to_f64(_bits(got))
+            assert (got[big] == want[big]).all()
+            assert (np.abs(got - y)[~big] <= Y_REL * np.abs(y[~big]) + Y_ABS).all()
