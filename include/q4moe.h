@@ -551,7 +551,8 @@ int lmhead_argmax(const q4moe_matrix* W, const q4moe_bf16* X, int64_t B, int32_t
  * and probability 0; of a row with a logit of +infinity these share the weight.  A u outside
  * [0, 1) counts as the nearest in it, a NaN as 0.  NaN parameters are: a temperature greedy,
  * a top_p or min_p none.  Weights are taken in fp64 to multiples of 2^-45 of the largest and
- * added as integers, so a row gets the same token in any batch and on any run.
+ * added as integers, and top_p's and u's shares of their totals are exact, so a row gets the
+ * same token in any batch and on any run.
  * V up to 262144, B up to 65536; logits aligned to their type; ids and probs overlap no
  * input, each other or the workspace (Q4MOE_EINVAL).  Needs a workspace of
  * sample_logits_workspace_bytes; calls that share one must not overlap.

@@ -91,8 +91,8 @@ enum Kind {
 
 struct RowRule {
   Kind kind;
-  double scale, p, limit;       // scale: log2(e) / t; limit: weights of 2^-limit and less drop
-  double u;                     // the draw's number, in [0, 1]
+  double scale, limit;          // scale: log2(e) / t; limit: weights of 2^-limit and less drop
+  float p, u;                   // top-p's share and the draw's number, in [0, 1]
   int k;                        // 0 without top-k
   bool p_on;
 };
@@ -103,11 +103,11 @@ __device__ __forceinline__ RowRule row_rule(const SampleArgs& a, int64_t b) {
   const int k = a.top_k ? a.top_k[b] : 0;
   const float p = a.top_p ? a.top_p[b] : 1.0f, m = a.min_p ? a.min_p[b] : 0.0f;
   const float u = a.u[b];
-  r.u = u > 0.0f ? fmin((double)u, 1.0) : 0.0;
+  r.u = u > 0.0f ? fminf(u, 1.0f) : 0.0f;
   r.scale = 1.4426950408889634 / (double)t;
   r.k = k > 0 && k < a.V ? k : 0;
   r.p_on = p < 1.0f;
-  r.p = p > 0.0f ? (double)p : 0.0;
+  r.p = p > 0.0f ? p : 0.0f;
   r.limit = kNone;
   if (m > 0.0f) {  // 2^-y >= m; the next number above, as what is kept lies below the limit
     const double most = fmax(-log2((double)m), 0.0);
@@ -353,16 +353,31 @@ __device__ __forceinline__ uint64_t block_sum(uint64_t mine) {
   return all;
 }
 
+// The whole part of x n for x in [0, 1), and whether something is left: exactly, as a total has up to 63
+// bits, ten more than fp64 holds.
+struct Share {
+  uint64_t whole;
+  bool rest;
+};
+__device__ __forceinline__ Share share(float x, uint64_t n) {
+  const uint32_t bits = __float_as_uint(x);
+  const int down = 150 - (int)(bits >> 23);  // x is a whole number of 24 bits by 2^-down, 24 and more
+  const uint64_t m = (bits & 0x7FFFFFu) | 0x800000u, lo = m * n, hi = __umul64hi(m, n);
+  if (down >= 88 || x == 0.0f) return Share{0, x > 0.0f && n > 0};  // (subnormal numbers among them)
+  if (down >= 64) return Share{hi >> (down - 64), (lo | (hi & ((1ull << (down - 64)) - 1))) != 0};
+  return Share{hi << (64 - down) | lo >> down, (lo & ((1ull << down) - 1)) != 0};
+}
+
 // The least whole number that is at least p z, and 1 at least: a sum reaches p z when it
 // reaches this.
-__device__ __forceinline__ uint64_t share_of(double p, uint64_t z) {
-  const double v = ceil(p * (double)z);
-  return v < 1.0 ? 1 : min((uint64_t)v, z);
+__device__ __forceinline__ uint64_t share_of(float p, uint64_t z) {
+  const Share s = share(p, z);
+  return max(s.whole + s.rest, (uint64_t)1);
 }
 
 // The draw's place among `total` of weight: the chosen token's running sum is the first beyond it.
 __device__ __forceinline__ uint64_t mark_of(const RowRule& r, uint64_t total) {
-  return min((uint64_t)(r.u * (double)total), total - 1);
+  return r.u < 1.0f ? share(r.u, total).whole : total - 1;
 }
 
 __device__ __forceinline__ void answer(const SampleArgs& a, int64_t b, int id, double prob) {
@@ -494,7 +509,7 @@ union Scratch {
 // the last that top-k may keep or, without top-k, to the end of the row (z = 0) or of the bin in
 // which top-p ends (z: the row's weight).
 template <int kThreads>
-__device__ __forceinline__ uint64_t last_kept(Scratch& s, uint64_t* list, int n, int k, bool p_on, double p,
+__device__ __forceinline__ uint64_t last_kept(Scratch& s, uint64_t* list, int n, int k, bool p_on, float p,
                                               const Weights& weight, Pair base, uint64_t z) {
   if (n <= kRanked) {
     // A token's place and the weight before it by comparison with all others: a token a thread, or

@@ -282,3 +282,41 @@ def test_binding_refusals(B):
         B.sample_logits(x, u, probs=u)
     assert err.value.status == B.EINVAL
     assert B.sample_logits(x[:0], u[:0])[0].shape == (0,)
+
+
+# Weights in units of 2^-45 of the largest, by hand at a temperature of 1: a logit of 0 weighs 2^45, one of -2^-45 (a
+# 45th of a bit below it) 2^45 - 1, one of -45 ln 2 a single unit, one of -1000 nothing.
+ONE_LESS, UNIT, NONE = -2.0 ** -45, -45 * np.log(2.0), -1000.0
+
+
+def _draw(B, row, u, k=None, p=None):
+    x = torch.from_numpy(np.asarray(row, dtype=np.float32)[None]).cuda()
+    ids, _ = B.sample_logits(x, _gpu([u]), None, _gpu(k and [k], torch.int32), _gpu(p and [p]))
+    return int(ids[0])
+
+
+def _with(rng, V, values):
+    """A row of V tokens without weight but those of `values`, at places in order, and these places."""
+    at = np.sort(rng.permutation(V)[:len(values)])
+    row = np.full(V, NONE)
+    row[at] = values
+    return row, at
+
+
+@pytest.mark.parametrize("V,k,p", [(512, None, None), (2000, None, None), (8192, None, None), (2000, 512, None), (60000, 512, None),
+                                   (2000, None, 1 - 2.0 ** -24), (8192, None, 1 - 2.0 ** -24), (60000, 3000, None)])
+def test_draw_at_a_border(B, V, k, p):
+    """512 tokens whose weights sum to 2^54 - 1, which fp64 does not hold: half of it is 2^53 - 1/2, and the running sum
+    exceeds that with the 256th token, not with the one after."""
+    row, at = _with(np.random.default_rng(V), V, [0.0] * 511 + [ONE_LESS])
+    assert _draw(B, row, 0.5, k, p) == at[255]
+    assert _draw(B, row, 0.5 + 2.0 ** -24, k, p) == at[256]
+
+
+@pytest.mark.parametrize("V,k", [(513, None), (2000, None), (8192, None), (151936, None), (2000, 600), (60000, 600), (60000, 5000)])
+def test_top_p_at_a_border(B, V, k):
+    """513 tokens whose weights sum to 2^54 + 1: the fewest that reach half of it, 2^53 + 1/2, are 257."""
+    row, at = _with(np.random.default_rng(V), V, [0.0] * 512 + [UNIT])
+    assert _draw(B, row, 1.0, k, 0.5) == at[256]
+    row[at[-1]] = NONE
+    assert _draw(B, row, 1.0, k, 0.5) == at[255]
