@@ -68,26 +68,6 @@ def mx4_round(x):
     return mx4_values(*mx4_quantize(x))
 
 
-def mx4_experts(x, ids, weights, gate, up, down, shared=None):
-    """y float64 [T][H]: x float64 rows, gate/up/down float64 values [E][n][k], ids [T][k] (outside: nothing)."""
-    q = mx4_round(x)
-    y = np.zeros((x.shape[0], down.shape[1]))
-
-    def one(rows, g, u, d):
-        a = rows @ g.T
-        with np.errstate(over="ignore"):
-            h = a / (1 + np.exp(-a)) * (rows @ u.T)
-        return mx4_round(h) @ d.T
-
-    for t in range(x.shape[0]):
-        for e, w in zip(ids[t], weights[t]):
-            if 0 <= e < gate.shape[0]:
-                y[t] += w * one(q[t:t + 1], gate[e], up[e], down[e])[0]
-    if shared is not None:
-        y += one(q, *shared)
-    return y
-
-
 # -------------------------------------------------------------------- sampling --
 
 def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None):
