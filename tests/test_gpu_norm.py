@@ -260,3 +260,58 @@ def test_range_of_values_and_weights(B, rows, k):
             got = qorc.bf16_to_f64(_bits(got))
             assert (got[big] == want[big]).all()
             assert (np.abs(got - y)[~big] <= Y_REL * np.abs(y[~big]) + Y_ABS).all()
+
+
+@pytest.mark.parametrize("rows,k,residual", [(2500, 4096, True), (2500, 4104, False), (2100, 8192, False), (1100, 16384, True),
+                                             (600, 20000, False), (600, 32768, True), (530, 65536, False), (70000, 136, True)])
+def test_rows_in_turn(B, rows, k, residual):
+    """More rows than workgroups, several waves to each: what a row leaves (its sums, an infinity or a NaN in one of its
+    waves) does not reach the next."""
+    X, w = _rows(rows + k, rows, k), _rows(k, 1, k)[0]
+    R = _rows(rows * 3 + k, rows, k, 3.0) if residual else None
+    bad = np.random.default_rng(k).permutation(rows)[:rows // 8]
+    X[bad, (np.arange(len(bad)) * 997) % k] = np.array([0x7F80, 0xFF80, 0x7FC0], np.uint16)[np.arange(len(bad)) % 3]
+    fine = np.ones(rows, dtype=bool)
+    fine[bad] = False
+    t, y = orc.rms_norm(X, w, EPS, R)
+    x, wt = B.bf16_tensor(X), B.bf16_tensor(w)
+    r = B.bf16_tensor(R) if residual else None
+    codes, scales, *total = B.rms_norm_i8(x, wt, EPS, residual=r)
+    one = B.rms_norm(x, wt, EPS, residual=r)
+    if residual:
+        assert torch.equal(total[0].view(torch.int16), one[1].view(torch.int16))
+        np.testing.assert_array_equal(qorc.bf16_to_f64(_bits(total[0])), t)
+        one = one[0]
+    keep = torch.from_numpy(fine).cuda()
+    _check_codes(codes[keep], scales[keep], y[fine])
+    _check_y(one[keep], y[fine])
+    assert torch.isnan(scales[~keep]).all() and not codes[~keep].any()
+    got = qorc.bf16_to_f64(_bits(one[~keep]))
+    assert (np.isnan(got) == np.isnan(y[~fine])).all() and (got[~np.isnan(got)] == 0).all()
+
+
+@pytest.mark.parametrize("k", [512, 2048, 4096, 8192, 16384, 40000])
+def test_not_finite_in_any_wave(B, k):
+    """An infinity or a NaN, alone in a row or in the weights, in each eighth of the columns; a large value crosses the waves too."""
+    w = synth.to_bf16_bits(np.ones(k, np.float32))
+    at = np.arange(8) * (k // 8) + 3
+    X = _rows(k, 24, k)
+    for i, bits in enumerate((0x7F80, 0xFFC1, 0x7F00)):
+        X[np.arange(8) + 8 * i, at] = bits
+    for rows in (slice(0, 24), slice(8, 9), slice(23, 24)):
+        _, y = orc.rms_norm(X[rows], w, EPS)
+        xt, wt = B.bf16_tensor(X[rows]), B.bf16_tensor(w)
+        got = qorc.bf16_to_f64(_bits(B.rms_norm(xt, wt, EPS)))
+        assert (np.isnan(got) == np.isnan(y)).all()
+        there = ~np.isnan(y)
+        assert (np.abs(got - y)[there] <= Y_REL * np.abs(y[there]) + Y_ABS).all()
+        codes, scales = B.rms_norm_i8(xt, wt, EPS)
+        large = np.arange(24)[rows] >= 16
+        assert torch.isnan(scales[torch.from_numpy(~large).cuda()]).all() and not codes[torch.from_numpy(~large).cuda()].any()
+        if large.any():
+            _check_codes(codes[torch.from_numpy(large).cuda()], scales[torch.from_numpy(large).cuda()], y[large])
+    for j in at:
+        v = w.copy()
+        v[j] = 0x7F80
+        codes, scales = B.rms_norm_i8(B.bf16_tensor(X[16:18]), B.bf16_tensor(v))
+        assert torch.isnan(scales).all() and not codes.any()
