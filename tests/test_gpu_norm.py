@@ -315,3 +315,22 @@ def test_not_finite_in_any_wave(B, k):
         v[j] = 0x7F80
         codes, scales = B.rms_norm_i8(B.bf16_tensor(X[16:18]), B.bf16_tensor(v))
         assert torch.isnan(scales).all() and not codes.any()
+
+
+@pytest.mark.parametrize("k", [256, 1000, 4096, 20000])
+@pytest.mark.parametrize("eps", [1.0, 1e-6, 1e-12])
+def test_codes_of_exact_halves(B, k, eps):
+    """Rows so small that eps alone is under the root, the largest 127 times a weight of 8 bits: scales are exact and a
+    quotient is its value, halves among them, which go to the even code."""
+    q = np.concatenate([[127.0], np.resize(np.arange(-127, 127) + 0.5, k - 1)])
+    x = np.where(np.arange(64)[:, None] % 2 == 0, q, -q) * 2.0 ** -100
+    X = synth.to_bf16_bits(x.astype(np.float32))
+    xt = B.bf16_tensor(X)
+    for s in range(129, 256, 14):
+        W = synth.to_bf16_bits(np.full(k, s, np.float32))
+        codes, scales = B.rms_norm_i8(xt, B.bf16_tensor(W), eps)
+        assert (scales.double().cpu().numpy() == s * 2.0 ** -100 * round(1 / np.sqrt(eps))).all()
+        np.testing.assert_array_equal(codes.cpu().numpy(), np.rint(x * 2.0 ** 100))
+        R = torch.zeros_like(xt)
+        more = B.rms_norm_i8(xt.clone(), B.bf16_tensor(W), eps, residual=R)
+        assert torch.equal(more[0], codes) and torch.equal(more[1], scales) and torch.equal(more[2], xt)
