@@ -159,7 +159,7 @@ __global__ __launch_bounds__(NormShape<kLanes>::kWaves* kWave) void rms_norm_ker
       }
       // Larger weights, and a factor that is below 2^-126 itself, take fp64: again, from memory, so that
       // the registers are the ordinary rows'.
-      if (large || __any(f < 0x1p-126f)) {
+      if (large || f < 0x1p-126f) {
         const uint16_t* from = (p.r ? p.total : p.x) + at;
 #pragma unroll 1
         for (int j = live ? j0 : p.k; j < p.k; j += j % 8 == 7 ? kStep - 7 : 1)

@@ -334,3 +334,16 @@ def test_codes_of_exact_halves(B, k, eps):
         R = torch.zeros_like(xt)
         more = B.rms_norm_i8(xt.clone(), B.bf16_tensor(W), eps, residual=R)
         assert torch.equal(more[0], codes) and torch.equal(more[1], scales) and torch.equal(more[2], xt)
+
+
+@pytest.mark.parametrize("k", [64, 128, 256, 512])
+def test_rows_beside_rows_beyond_fp32(B, k):
+    """A row's bits do not hang on the rows that share its wave: rows of 1e38 between ordinary ones, which take fp64."""
+    X, w = _rows(k, 200, k), B.bf16_tensor(_rows(k + 1, 1, k)[0])
+    alone = B.rms_norm(B.bf16_tensor(X), w, EPS)
+    X[1::3] = synth.to_bf16_bits((3e38 * np.random.default_rng(k).uniform(0.1, 1, X[1::3].shape)).astype(np.float32))
+    _, y = orc.rms_norm(X, _bits(w), EPS)
+    got = B.rms_norm(B.bf16_tensor(X), w, EPS)
+    _check_y(got, y)
+    for first in (0, 2):
+        assert torch.equal(got[first::3], alone[first::3])
