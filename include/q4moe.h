@@ -439,12 +439,13 @@ size_t i8_gemm_workspace_bytes(const q4moe_i8_matrix* W, int64_t m);
  * total bf16 [rows][k] receives t, the residual stream that the next addition takes; it
  * may be X or residual itself.  The result goes to y as bf16 [rows][k] (rounded once from
  * fp32 that is within 2^-22 of it, or 2^-136 where that is more), or in i8_quantize's 8-bit
- * form to codes int8 [rows][k] and scales fp32 [rows], or to both: codes and scales are those of the unrounded y
- * (scales[r] the fp32 nearest to max|y| / 127, codes computed in fp64), so that a product
- * takes them with one rounding less than a bf16 y would bring.  y is null, or codes and
- * scales are.  A row that holds an infinity or a NaN (in t, or in weight) gives scale NaN and
- * codes 0; its y is what the formula gives.  weight bf16 [k]; k a multiple of 8 up to
- * 65536; eps at least 1.2e-38 and finite.  Buffers overlap no other (but total as said).
+ * form to codes int8 [rows][k] and scales fp32 [rows], or to both: codes and scales are those
+ * of the unrounded y (scales[r] the fp32 nearest to max|y| / 127, codes computed in fp64,
+ * halves to the even one), so that a product takes them with one rounding less than a bf16 y
+ * would bring.  y is null, or codes and scales are.  A row that holds an infinity or a NaN
+ * (in t, or in weight) gives scale NaN and codes 0; its y is what the formula gives.  weight
+ * bf16 [k]; k a multiple of 8 up to 65536; eps at least 1.2e-38 and finite.  Buffers overlap
+ * no other (but total as said).
  */
 int rms_norm(const q4moe_bf16* X, const q4moe_bf16* residual, const q4moe_bf16* weight, int64_t rows, int64_t k,
              double eps, q4moe_bf16* total, q4moe_bf16* y, int8_t* codes, float* scales, q4moe_stream stream);

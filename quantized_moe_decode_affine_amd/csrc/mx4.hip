@@ -116,11 +116,12 @@ constexpr int lcm(int a, int b) { return a % b == 0 ? a : b % a == 0 ? b : a * b
 // Where rows of scales are 16-byte aligned (kWide) DMA brings 64 bytes of each at a time
 // instead: 8192 x 8192 x 4096 with the rows' quantization 173 us against 185.
 //
-// That is 3.2 PFLOP/s; the matrix instructions alone, on such data, reach 6.2.  Of 185 us, without the
-// loads 163 were left and without the multiplications 111: bound by the LDS reads
-// and the matrix instructions of the two waves of a SIMD, which overlap in part.  Four waves of 128 x 128
-// instead of eight read less from LDS, but hide less (192-199 us); raising a wave's priority
-// around its multiplications changed nothing.
+// The tiles alone take 150 us of that, 3.7 PFLOP/s; the matrix instructions alone, on such data,
+// reach 6.2.  Bound by the LDS reads and the matrix instructions of the two waves of a SIMD, which
+// overlap in part: of the 185 us with a thread's scales 163 were left without the loads and 111
+// without the multiplications.  Beside those 185, four waves of 128 x 128 instead of eight read less
+// from LDS, but hide less (192-199 us); raising a wave's priority around its multiplications changed
+// nothing.
 template <int WM, int WN, int FM, int FN, int kStages, int EPI, bool kWide>
 __device__ __forceinline__ void mx4_tile_body(const Mx4GemmArgs& p) {
   constexpr int TM = WM * FM * 32, TN = WN * FN * 32, kWaves = WM * WN;
@@ -651,8 +652,9 @@ __global__ __launch_bounds__(256) void mx4_combine_kernel(const float* __restric
 
 // Rows of a grouped tile: 128 x 256 columns by eight waves.  2048 tokens, top-k 8 of 256
 // experts, hidden 2048, intermediate 512: quantization 5 us, sorting 12, gate and up 86, down 72,
-// combining 28.  64 rows an expert leave half of a tile's rows empty, and each tile reads its
-// weights once: bound by the tiles' latency, two K steps of the down product among it.
+// combining 28 (kernel times).  64 rows an expert on average leave half of a tile's rows empty, and each
+// tile reads its weights once, 429 MB in all at 2.7 TB/s: bound by the tiles' latency, as gate and up have
+// 8 K steps and the down product 2.
 // Tiles of 128 x 128, two to a compute unit: 205 us against 203; 512 tokens 145 against 150.
 constexpr int kExpertRows = 128;
 

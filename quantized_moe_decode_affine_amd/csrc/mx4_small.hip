@@ -9,9 +9,11 @@
 // here: the matrix cores take 1 KB of weights in 16 cycles a SIMD, many times the rate at
 // which memory brings them.
 //
-// Measured: 8 rows on 151936 x 2048 36-37 us, 4.6 TB/s; 1 row on 1024 x 2048 in 3.5 us, a
-// launch and two turns of memory; experts of one token (8 of 256 and a shared one, 2048 x 512)
-// 5.2 us for gate and up and 4.3 for down.
+// Measured: 8 rows on 151936 x 2048 (165 MB of weights and 5 of results) 29 us where the last cache
+// holds a part of the weights from the call before, 5.8 TB/s; a call after others 37 us, 4.6 TB/s.
+// 1 row on 1024 x 2048 in 3.5 us, a launch and two turns of memory; experts of one token (8 of 256
+// and a shared one, 2048 x 512) 5.0 us for gate and up and 4.4 for down, traced apart; 8.7 the two
+// in a graph.
 #include <algorithm>
 
 #include "steps.h"
@@ -211,7 +213,7 @@ namespace {
 // Gate/up: a workgroup per (slot, 8 intermediate columns): the 16 rows of its operand are 8
 // rows of gate and the same 8 of up, its four waves share the columns.  The first slot of an
 // expert takes all slots of that expert (up to 16 at a time), the others leave.
-constexpr int kMaxSlots = 128;  // no more than the workgroup's threads
+constexpr int kMaxSlots = 128;  // (at most the workgroup's threads, 256)
 constexpr int kUpCols = 8;
 
 __global__ __launch_bounds__(kSmallWaves* kWave) void mx4_slots_up_kernel(Mx4Experts L, const uint16_t* __restrict__ X,
@@ -353,11 +355,21 @@ int down_waves(int I, int slots) {
 }  // namespace
 
 // Up to 32 tokens and 96 slots, or 128 of 256 experts and more, where fewer share an expert:
-// the down product reads an expert's weights once a token, the tiles read them once.  Hidden
-// 2048, intermediate 512, 256 experts, top-k 8 and a shared expert, against the tiles: 1 token
-// 8.6 us to 29, 8 tokens 30 to 45, 12 tokens 41 to 57, 16 tokens 51 to 64, 24 tokens 74 to 81; of
-// 16 experts 8 tokens 23 to 33, but 16 tokens 38 to 33; hidden 4096, intermediate 1536, 128 experts,
-// 12 tokens 160 to 170, but 16 tokens 204 to 182.
+// the down product reads an expert's weights once a token, the tiles read them once.  What decides
+// is the slots an expert and its size, which the rule knows only by the number of experts; whole calls
+// in a graph against the tiles, us:
+//   hidden 2048, intermediate 512, top-k 8 and a shared expert:
+//   experts     1 token     8        12       16       20       24
+//   512                  31  56   44  67   55  70            83  89
+//   256         9.6 31   31  50   43  60   53  63   66  69   78  82
+//   128                  30  43   41  56   52  58
+//   64                   29  41   38  43   46  44
+//   16                   24  34   32  34   41  35
+//   hidden 4096, intermediate 1536, top-k 8, 256 experts: 8 tokens 120 141, 12 176 207, 16 223 226; 128
+//   experts: 8 tokens 118 137, 12 157 152, 16 212 211; 8 experts, top-k 2: 2048 x 512 16 tokens 12 28,
+//   32 tokens 17 28; 4096 x 14336 1 token 54 139, 4 tokens 100 154, 8 tokens 207 183, 32 tokens 537 185.
+// So it leaves a tenth of the time to 20 and 24 tokens of 256 experts (more slots than kMaxSlots; the
+// figures are with 256) and to 16 of 128, and few large experts go the slower way from 8 tokens on.
 bool mx4_few_slots(const Mx4Experts& L, int64_t T, int k) {
   if (T > 32 || T * k > (L.n_experts >= 256 ? kMaxSlots : 96)) return false;
   return image_bytes(T * k < 16 ? T * k : 16, L.hidden) <= kSmallLds;

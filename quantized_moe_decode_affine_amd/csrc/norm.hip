@@ -6,13 +6,13 @@
 // One pass: a row's t stay in registers between its sums and its results.  The sum of squares
 // and what the codes' borders hang on (y, the largest |t w|, y / scale) are in fp64, so a
 // code is the definition's: in fp32 about one code in 50,000 fell on the other side of a
-// border.  The fp64 operations hide behind the bytes: about ten an element, at a rate of 64 a
-// clock and compute unit.
+// border.
 //
-// Bound by memory: 8191 rows of 4096 with a residual and a bf16 result take 49.8 us, 5.4 TB/s
-// (a copy of 1 GiB reaches 5.2); 4096 rows of 2048 with a residual to codes 17 us (59 MB,
-// some of it still in the last cache).  One row of 2048 takes 3 us (bf16) to 4 (codes): the
-// launch, a turn of memory and the reduction.
+// A bf16 result is bound by memory: 8191 rows of 4096 with a residual take 50 us, 5.4 TB/s (a
+// copy of 1 GiB reaches 5.2), 42 us where the last cache holds a part.  Codes on many rows are
+// bound by fp64, some ten operations and conversions an element: 4096 rows of 2048 with a residual
+// 17.2 us for 59 MB, 3.4 TB/s, where a bf16 result takes 12.9 us for 67 MB.  One row of 2048 takes
+// 3 us either way: the launch, a turn of memory and the reduction.
 #include <algorithm>
 
 #include "int8.h"
@@ -41,9 +41,9 @@ constexpr uint64_t kInf64 = 0x7FF0000000000000ull;
 // kLanes lanes to a row (a part of a wave, a wave, or several), kHeld chunks of 8 columns a lane
 // (kLanes * kHeld * 8 >= k); 4 waves a workgroup, or a row's.  A whole wave to rows of 128
 // columns, as the norm of an attention's heads has them, would leave three lanes of four idle:
-// 65,536 such rows to codes 17.5 us against 51.8.  The weights' chunks stay in registers over
+// 65,536 such rows to codes 17.1 us against 51.8.  The weights' chunks stay in registers over
 // the rows of a workgroup, but for rows of more than 16384 columns: their registers hold t,
-// and weights and residual come two chunks at a time (256 rows of 32768 to codes 19.4 us
+// and weights and residual come two chunks at a time (256 rows of 32768 to codes 18.2 us
 // against 56.3 with everything held, which spills).
 template <int kLanes>
 struct NormShape {

@@ -23,10 +23,11 @@
 // Steps whose parts' maxima reach nothing that is kept are not read.  Where a list would
 // overflow (many equal logits) a workgroup selects from the row itself, digit by digit.
 //
-// Measured on 151,936 fp32 logits: one row 11 us without a filter, 16 with top-k 50, 35 with a
-// top-p of 0.9 alone; 256 rows 74, 40 and 164, of mixed parameters 105.  The first reading is
-// bound by memory; a list's selection by latency (one workgroup a row); the bins by their
-// atomic adds in LDS, the steps' sums by the fp64 of the weights.
+// Measured on 151,936 fp32 logits, whole calls in a graph: one row 14 us without a filter, 18 with
+// top-k 50, 36 with a top-p of 0.9 alone; 256 rows 75, 42 and 167, of mixed parameters 102.  The first
+// reading is bound by memory; a list's selection by latency (one workgroup a row); the bins by
+// their atomic adds in LDS, the steps' sums by the fp64 of the weights (not told apart by counters).
+// Rows whose list overflows are far slower (draw_alone).
 #include <algorithm>
 #include <type_traits>
 
@@ -1024,6 +1025,12 @@ __device__ __forceinline__ void draw_from_steps(RowShared& s, const SampleArgs& 
 
 // The draw by this workgroup alone: the last token kept by digits of the row's words, then the steps' sums.
 // z: the row's weight, for a top-p without top-k.
+// Up to five readings of the row for each filter and one more, every token's weight taken each time and
+// most of them added to few counters: 151,936 logits in 0.6-1.1 ms, where a list takes 20-40 us.  Rows of many
+// equal logits come here, bf16 ones away from zero among them (of mean 10 to 20 and a deviation of 1 to 2,
+// under a top-p of 0.9 alone, more than 2,048 tokens share the logit in which p ends: one row 0.60-0.66 ms,
+// 64 rows 1.1-1.3, 256 rows 2.2-2.3), rows under a top-p far inside a large top-k (5,000, p 0.9: 256 rows
+// 1.8 ms), and rows of one value (one row 1.1 ms, 256 rows 4.6).
 template <typename In>
 __device__ __forceinline__ void draw_alone(RowShared& s, const SampleArgs& a, int64_t b, const RowRule& r, int k,
                                         const Weights& weight, uint64_t z) {
@@ -1196,8 +1203,10 @@ __global__ __launch_bounds__(kRowThreads, 4) void row_kernel(SampleArgs a) {
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // A row's chunks: four workgroups a compute unit over all rows (256 rows of mixed parameters, few of which
-// need every chunk: 103 us against 133 with two and 96 with eight; all under a top-p of 0.9: 164, 137 and more),
-// none for fewer than 4,096 tokens (37 rows of 32,003: 44 us against 55 with 2,048).
+// need every chunk: 103 us against 133 with two and 96 with eight), none for fewer than 4,096 tokens (37 rows of
+// 32,003: 44 us against 55 with 2,048).  Taken for such mixed rows; where every row needs every chunk two
+// are faster: 256 rows under a top-p of 0.9 alone 167 us against 141 with two, without a filter 75 against 71,
+// 64 rows 86 against 69, and rows whose lists overflow 2.3 ms against 1.2.
 void split(int64_t B, int V, int* G, int* chunk) {
   const int64_t want = std::max<int64_t>(1, 4 * (int64_t)device_cu_count() / std::max<int64_t>(B, 1));
   const int64_t n = std::max<int64_t>(1, std::min<int64_t>({want, kMaxChunks, (V + 4095) / 4096}));
