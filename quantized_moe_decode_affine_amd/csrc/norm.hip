@@ -137,7 +137,7 @@ __global__ __launch_bounds__(NormShape<kLanes>::kWaves* kWave) void rms_norm_ker
       }
       lds_sync();  // read before the next row's are written
     }
-    const double inv = 1.0 / sqrt(sum / p.k + p.eps);
+    const double root = sqrt(sum / p.k + p.eps), inv = 1.0 / root;
     if constexpr (!kCodes) {
       // Two fp32 roundings of 2^-24 before the one to bf16.  t * f may lie below 2^-126, where fp32 is
       // off by up to 2^-150; weights below 2^14 make that 2^-136 at most, an eighth of bf16's last bit.
@@ -187,14 +187,18 @@ __global__ __launch_bounds__(NormShape<kLanes>::kWaves* kWave) void rms_norm_ker
         }
       }
       if (live && part == 0 && lane_id() % kPart == 0) p.scales[row] = scale;
-      // A row that eps rules has a factor as short as 1 or 1000, and quotients just between two codes: with
-      // one of 37 bits at most u * inv is exact, and decides them (again, from memory).
-      if (scale > 0.0f && ((uint64_t)__double_as_longlong(inv) & 0xFFFFu) == 0) {
+      // Quotients just between two codes, which one rounding moves off the border: rows of one magnitude have
+      // them, whose root is short, and rows that eps rules, whose factor is 1 or 1000.  With a root of 29
+      // bits at most root * scale is exact, with a factor of 37 u * inv, and one division decides (again,
+      // from memory).
+      const bool short_root = ((uint64_t)__double_as_longlong(root) & 0xFFFFFFu) == 0;
+      if (scale > 0.0f && (short_root || ((uint64_t)__double_as_longlong(inv) & 0xFFFFu) == 0)) {
+        const double times = short_root ? 1.0 : inv, step = short_root ? root * (double)scale : (double)scale;
         const uint16_t* from = (p.r ? p.total : p.x) + at;
 #pragma unroll 1
         for (int j = live ? j0 : p.k; j < p.k; j += j % 8 == 7 ? kStep - 7 : 1) {
           const double u = (double)bf16_bits_to_f32(from[j]) * (double)bf16_bits_to_f32(p.w[j]);
-          p.codes[at + j] = (int8_t)max(-127, min(127, (int)rint(u * inv / (double)scale)));
+          p.codes[at + j] = (int8_t)max(-127, min(127, (int)rint(u * times / step)));
         }
       }
     }

@@ -347,3 +347,17 @@ def test_rows_beside_rows_beyond_fp32(B, k):
     _check_y(got, y)
     for first in (0, 2):
         assert torch.equal(got[first::3], alone[first::3])
+
+
+@pytest.mark.parametrize("k", [256, 4096])
+@pytest.mark.parametrize("every", [1, 4])
+def test_codes_of_exact_halves_in_rows_of_one_magnitude(B, k, every):
+    """Rows of +-t and zeros, beside which eps vanishes: y is +-w (or twice that), its quotients halves."""
+    w = np.resize(np.concatenate([[127.0], np.arange(-127, 127) + 0.5, [1.0]]), k)
+    W = synth.to_bf16_bits(w.astype(np.float32))
+    t = np.arange(128.0, 256.0)[:, None]
+    x = t * np.where(np.arange(k) % 3 == 0, -1, 1) * (np.arange(k) % every == 0)
+    codes, scales = B.rms_norm_i8(B.bf16_tensor(synth.to_bf16_bits(x.astype(np.float32))), B.bf16_tensor(W), 1e-37)
+    y = np.sign(x) * w * np.sqrt(every)
+    assert (scales.double().cpu().numpy() == np.sqrt(every)).all()
+    np.testing.assert_array_equal(codes.cpu().numpy(), np.rint(y / np.sqrt(every)))
